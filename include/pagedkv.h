@@ -77,6 +77,8 @@ extern "C" {
 #define PKV_DEV_WAIT_TIMEOUT     6  /* a pipeline wait exceeded its limit (internal fault) */
 #define PKV_DEV_TABLE_TOO_NARROW 7  /* context needs more blocks than max_blocks_per_seq */
 #define PKV_DEV_BAD_POSITION     8  /* rotary position outside [0, max_position) */
+#define PKV_DEV_BAD_SEQ_ROW      9  /* table row outside [0, max_seqs), named twice, or released twice */
+#define PKV_DEV_NO_FREE_BLOCKS  10  /* a step needs more blocks than the device free list holds */
 
 /* ---- data types -------------------------------------------------------- */
 #define PKV_F32  0
@@ -484,6 +486,152 @@ PKV_API int paged_attention_decode_int8(void* out, const void* q, const void* kv
                                         const int32_t* context_lens, int32_t num_seqs,
                                         int32_t max_context_len, float scale, void* workspace,
                                         size_t workspace_bytes, void* stream);
+
+/* ======================================================================== *
+ * Block tables held on the device.
+ *
+ * The counterpart of the host pool for loops that do not return to the host
+ * between steps (a captured decode graph, several steps enqueued ahead): a row
+ * of block ids per sequence and a stack of free ids live in device memory, and
+ * a step builds everything that the append and the attention take from the
+ * requests' lengths.  The blocks handed out are those of a host pool without
+ * sharing [Deploy §2.1 3.; Infra 二] that serves the requests one after the
+ * other: the entry on top of the stack is taken first, and a released
+ * sequence's blocks go back in table order.  Rows share no blocks (no fork).
+ *
+ * All memory is the caller's.  Calls on one pkv_device_tables must be ordered
+ * (one stream, or events between streams).
+ * ======================================================================== */
+#define PKV_TABLES_MAX_SEQS 262144
+
+typedef struct pkv_device_tables {
+    int32_t* block_table;  /* device [max_seqs][max_blocks] */
+    int32_t* free_list;    /* device [num_blocks]: ids, entry *free_count - 1 handed out first */
+    int32_t* free_count;   /* device [1] */
+    int32_t max_seqs;      /* at most PKV_TABLES_MAX_SEQS */
+    int32_t max_blocks;    /* blocks of a row */
+    int32_t num_blocks;    /* blocks of the pool */
+    int32_t block_size;    /* tokens of a block (any) */
+} pkv_device_tables;
+
+/* One step: request i, whose blocks are row seq_rows[i] (NULL: row i), holds
+ * cached_lens[i] tokens and adds new_lens[i] (NULL: one each; 0 is allowed).
+ * New blocks are taken from the free list for the tokens that its last block
+ * has no room for, and the row gets them.  Written, all device memory:
+ *   context_lens[i]     cached + new (may be the cached_lens buffer itself)
+ *   query_start_loc     [num_seqs + 1] running sums of the new tokens
+ *   slot_mapping[t]     int64 [max_tokens]: block * block_size + row of each new
+ *                       token in request order; -1 behind the last one
+ *   positions[t]        [max_tokens] position in its sequence; 0 behind the last
+ *                       (optional)
+ *   block_tables        [num_seqs][max_blocks_per_seq] the requests' rows, padded
+ *                       with -1 (optional)
+ *   *free_count_out     blocks left (NULL: tables->free_count, in place).  With a
+ *                       separate count the same step can be built again: it
+ *                       takes the same blocks.
+ * Requests are served in order up to the first that does not fit; it and all
+ * behind it get no tokens (context_lens[i] = cached_lens[i], their table rows
+ * unchanged) and can be asked for again: PKV_DEV_NO_FREE_BLOCKS when blocks ran
+ * out, PKV_DEV_BAD_QUERY_LAYOUT when max_tokens did.  A request with a row out
+ * of range or named twice in the batch (PKV_DEV_BAD_SEQ_ROW), a negative length
+ * (PKV_DEV_BAD_CONTEXT_LEN) or more tokens than a row or block_tables has room
+ * for (PKV_DEV_TABLE_TOO_NARROW) is skipped: context_lens[i] = 0, no tokens, a
+ * row of -1.  num_seqs == 0 writes the padding, query_start_loc[0] and the
+ * count.  Outputs do not overlap inputs but where said. */
+PKV_API int pkv_tables_step(const pkv_device_tables* tables, const int32_t* seq_rows,
+                            const int32_t* cached_lens, const int32_t* new_lens,
+                            int32_t num_seqs, int32_t max_tokens, int32_t* free_count_out,
+                            int32_t* block_tables, int32_t max_blocks_per_seq,
+                            int32_t* context_lens, int32_t* query_start_loc,
+                            int64_t* slot_mapping, int32_t* positions, void* stream);
+
+/* Give back the blocks of rows seq_rows[i] (NULL: row i), which hold lens[i]
+ * tokens (device [num_seqs]), in request and table order; their entries become
+ * -1 and *free_count grows in place.  Skipped and flagged: a row out of range,
+ * named twice or already released (PKV_DEV_BAD_SEQ_ROW), a length out of range
+ * (as in pkv_tables_step), blocks past the end of the free list
+ * (PKV_DEV_BAD_BLOCK_ID). */
+PKV_API int pkv_tables_release(const pkv_device_tables* tables, const int32_t* seq_rows,
+                               const int32_t* lens, int32_t num_seqs, void* stream);
+
+/* ======================================================================== *
+ * Sparse attention over blocks that a score selects for each query.
+ *
+ * A decode step over a long context reads every block of it.  Here each (query
+ * token, KV head) reads only the blocks whose keys can matter most to it:
+ * pkv_block_bounds keeps, beside the cache, the range of the keys of every
+ * (block, KV head); pkv_select_blocks scores a sequence's blocks by them and
+ * lists the best; paged_attention_sparse attends over a list.
+ *
+ * Rows: with query_start_loc NULL there is one query token per sequence
+ * (num_query_tokens == num_seqs), its last; otherwise query_start_loc is the
+ * layout of paged_attention_varlen, and row i of a sequence sees keys
+ * 0 .. context_lens - qlen + i.  Rows behind query_start_loc[num_seqs] are left
+ * as they are, so a batch may be padded.  Caches PKV_F32 or PKV_BF16.
+ * ======================================================================== */
+
+/* Key bounds of the blocks that this step's tokens were appended to (the last
+ * qlen positions of each sequence), from all their rows that hold tokens:
+ *   hi[d] = max over the rows of k[d],  lo[d] = min over the rows of k[d],
+ *   e = the least whole number with max |k| <= 127 * 2^e, within -50 .. 50,
+ *   bounds[block][h][0][d] = clamp(ceil(hi[d] / 2^e), -127, 127),
+ *   bounds[block][h][1][d] = clamp(floor(lo[d] / 2^e), -127, 127),
+ *   exps[block][h] = e,
+ * all exact.  A (block, head) with a key that is not finite gets codes of 0 and
+ * e = 127: it scores above all others, so that attention shows it.
+ * bounds: device int8 [num_blocks][num_kv_heads][2][head_dim], 16-byte aligned;
+ * exps: device int8 [num_blocks][num_kv_heads].  Other blocks' are not touched. */
+PKV_API int pkv_block_bounds(int8_t* bounds, int8_t* exps, const void* k_cache,
+                             const pkv_cache_desc* desc, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                             const int32_t* context_lens, int32_t num_seqs,
+                             int32_t num_query_tokens, void* stream);
+
+/* Bytes of workspace pkv_select_blocks needs (0 on bad arguments). */
+PKV_API size_t pkv_select_workspace_bytes(const pkv_cache_desc* desc, int32_t num_query_tokens,
+                                          int32_t max_context_len);
+
+/* For each (query token, KV head) the blocks to attend: with q's codes
+ * c[d] = rint(q[d] / 2^f) (ties to even; f as e above, of one query head; codes
+ * of 0 for a head with values that are not finite), logical block b scores
+ *   max over the group's query heads of
+ *     2^(f + e_b) * sum_d max(c[d] * hi_b[d], c[d] * lo_b[d]),
+ * computed exactly, so the choice does not depend on how it is summed.  Listed
+ * are the first num_sink and the last num_recent blocks of the row's context
+ * (num_recent >= 1: the row's own block), and of the others those that score
+ * highest, the lower index first among equals, top_k blocks in all (all of
+ * them, if the context has no more).
+ *   selected: device int32 [num_query_tokens][num_kv_heads][top_k], logical block
+ *             indices in ascending order, -1 behind the last
+ *   q:        device [num_query_tokens][num_q_heads][head_dim] (cache dtype)
+ * num_sink >= 0, num_sink + num_recent <= top_k.  A block id outside the pool
+ * (PKV_DEV_BAD_BLOCK_ID) scores below all others; a sequence with a context out
+ * of range (PKV_DEV_BAD_CONTEXT_LEN, PKV_DEV_TABLE_TOO_NARROW) gets lists of -1.
+ * workspace: device, 256-byte aligned, not shared by concurrent calls. */
+PKV_API int pkv_select_blocks(int32_t* selected, const void* q, const int8_t* bounds,
+                              const int8_t* exps, const pkv_cache_desc* desc,
+                              const int32_t* block_tables, int32_t max_blocks_per_seq,
+                              const int32_t* query_start_loc, const int32_t* context_lens,
+                              int32_t num_seqs, int32_t num_query_tokens,
+                              int32_t max_context_len, int32_t top_k, int32_t num_sink,
+                              int32_t num_recent, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Attention over the listed blocks: for query token t and the query heads of KV
+ * head h, softmax(q . K^T * scale) V over the keys of the logical blocks
+ * selected[t][h][0 .. top_k-1] that the row sees.  Entries may come in any
+ * order; negative ones are skipped; a block that is listed twice counts twice.
+ * A list that names no key the row sees gives zeros.  An entry past the row's
+ * context or a block id outside the pool is skipped and sets
+ * PKV_DEV_BAD_BLOCK_ID; a sequence with a context out of range gives zeros.
+ * With every block listed the result is that of paged_attention_varlen.  Needs
+ * no workspace.  scale: usually 1/sqrt(head_dim). */
+PKV_API int paged_attention_sparse(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const pkv_cache_desc* desc,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* query_start_loc, const int32_t* context_lens,
+                                   const int32_t* selected, int32_t top_k, int32_t num_seqs,
+                                   int32_t num_query_tokens, float scale, void* stream);
 
 /* Read the current device's error word into *code_out (PKV_DEV_* code of the
  * first fault recorded since the last clear) and, if `clear` is non-zero,

@@ -30,6 +30,8 @@ Modules
   splitfuse    token-budget composition of one forward pass (decodes + prompt chunks)
   rope         rotate-half rotary embedding fused into the append (fp32, bf16 rounding)
   quant        8-bit KV cache: per-(token, head) symmetric int8 codes and decode over them
+  sparse       block tables served from a stack of free ids, key bounds of blocks, block
+               selection by them and attention over listed blocks
 
 Parity: every function here is pinned by ``tests/test_oracle_*.py`` against
 values the pages print, closed forms, brute force on unpaged data, or
@@ -37,4 +39,4 @@ invariants; none is marked "parity unpinned".
 """
 
 from . import (attention, block_pool, cache, kv_size, numerics, online, quant, rope,  # noqa: F401
-               sketch, splitfuse)
+               sketch, sparse, splitfuse)

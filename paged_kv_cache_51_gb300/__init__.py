@@ -35,7 +35,7 @@ PKV_INT8 = 2
 DEVICE_ERRORS = {
     0: "ok", 1: "bad block id", 2: "bad context length", 3: "bad slot", 4: "bad copy pair",
     5: "bad query layout", 6: "pipeline wait timeout", 7: "block table too narrow",
-    8: "bad rotary position",
+    8: "bad rotary position", 9: "bad table row", 10: "no free blocks",
 }
 
 # every symbol the header declares (checked by the tests)
@@ -51,6 +51,8 @@ EXPORTS = (
     "pkv_pool_create_ex", "pkv_pool_num_evictable", "pkv_pool_set_clock", "pkv_seq_add_tokens",
     "pkv_seq_append_token", "pkv_block_hash", "pkv_pool_create_window", "pkv_window_tables",
     "paged_attention_varlen_window",
+    "pkv_tables_step", "pkv_tables_release", "pkv_block_bounds", "pkv_select_workspace_bytes",
+    "pkv_select_blocks", "paged_attention_sparse",
 )
 
 PKV_POOL_PREFIX_CACHING = 1
@@ -66,6 +68,13 @@ class CacheDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("num_q_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class DeviceTablesDesc(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("free_list", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("max_seqs", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32)]
 
 
 _lib = None
@@ -123,6 +132,15 @@ def lib():
         "pkv_copy_blocks_int8": (ctypes.c_int, [p, i32, p, P(CacheDesc), p]),
         "paged_attention_decode_int8": (ctypes.c_int, [p, p, p, P(CacheDesc), p, i32, p, i32,
                                                        i32, ctypes.c_float, p, sz, p]),
+        "pkv_tables_step": (ctypes.c_int, [P(DeviceTablesDesc), p, p, p, i32, i32, p, p, i32, p,
+                                           p, p, p, p]),
+        "pkv_tables_release": (ctypes.c_int, [P(DeviceTablesDesc), p, p, i32, p]),
+        "pkv_block_bounds": (ctypes.c_int, [p, p, p, P(CacheDesc), p, i32, p, p, i32, i32, p]),
+        "pkv_select_workspace_bytes": (sz, [P(CacheDesc), i32, i32]),
+        "pkv_select_blocks": (ctypes.c_int, [p, p, p, p, P(CacheDesc), p, i32, p, p, i32, i32,
+                                             i32, i32, i32, i32, p, sz, p]),
+        "paged_attention_sparse": (ctypes.c_int, [p, p, p, p, P(CacheDesc), p, i32, p, p, p, i32,
+                                                  i32, i32, ctypes.c_float, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -646,6 +664,223 @@ def paged_attention_decode_int8(out, q, cache, block_tables, context_lens, max_c
                                              _ptr(context_lens), S, max_context_len, scale,
                                              _ptr(ws), ws.numel(), st),
            "paged_attention_decode_int8")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# block tables held on the device
+# ----------------------------------------------------------------------------
+class DeviceTables:
+    """Block tables and free list in device memory (pkv_device_tables): int32
+    tensors block_table [max_seqs, max_blocks], free_list [num_blocks] (a stack,
+    its top at entry free_count - 1) and free_count [1].  ``create`` makes those
+    of an empty pool."""
+
+    def __init__(self, block_table, free_list, free_count, block_size):
+        for t, nm in ((block_table, "block_table"), (free_list, "free_list"),
+                      (free_count, "free_count")):
+            _need(t, torch.int32, nm)
+        if block_table.dim() != 2 or free_list.dim() != 1 or free_count.numel() != 1:
+            raise ValueError("block_table [max_seqs, max_blocks], free_list [num_blocks] and "
+                             "free_count [1] expected")
+        self.block_table, self.free_list, self.free_count = block_table, free_list, free_count
+        self.block_size = block_size
+        self.desc = DeviceTablesDesc(block_table.data_ptr(), free_list.data_ptr(),
+                                     free_count.data_ptr(), block_table.shape[0],
+                                     block_table.shape[1], free_list.shape[0], block_size)
+
+    @classmethod
+    def create(cls, num_blocks, block_size, max_seqs, max_blocks, free_order=None,
+               device="cuda"):
+        """An empty pool; ``free_order`` as for BlockPool (its first entry is
+        handed out first, 0, 1, 2, ... by default)."""
+        order = np.arange(num_blocks, dtype=np.int32) if free_order is None else \
+            _host_int32(free_order, "free_order")
+        if order.shape != (num_blocks,):
+            raise ValueError(f"free_order: {order.shape[0]} entries, expected {num_blocks}")
+        return cls(torch.full((max_seqs, max_blocks), -1, dtype=torch.int32, device=device),
+                   torch.from_numpy(order[::-1].copy()).to(device),
+                   torch.tensor([num_blocks], dtype=torch.int32, device=device), block_size)
+
+
+def _need_len(t, n, name):
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({n},)")
+
+
+def pkv_tables_step(tables, seq_rows, cached_lens, new_lens, block_tables, context_lens,
+                    query_start_loc, slot_mapping, positions=None, free_count_out=None,
+                    stream=None):
+    """Build a step's block tables, lengths, slots and positions on the device from
+    the requests' lengths, taking new blocks from ``tables`` (a DeviceTables).
+
+    CUDA int32: seq_rows [n] (None: row i), cached_lens [n], new_lens [n] (None:
+    one token each); written: block_tables [n, W] (or None), context_lens [n],
+    query_start_loc [n + 1], slot_mapping (int64 [T], T the most tokens of the
+    step), positions [T] (or None), free_count_out [1] (None: in place)."""
+    n = cached_lens.shape[0]
+    T = slot_mapping.shape[0]
+    for t, nm, m in ((seq_rows, "seq_rows", n), (cached_lens, "cached_lens", n),
+                     (new_lens, "new_lens", n), (context_lens, "context_lens", n),
+                     (query_start_loc, "query_start_loc", n + 1), (positions, "positions", T),
+                     (free_count_out, "free_count_out", 1)):
+        if t is not None:
+            _need(t, torch.int32, nm)
+            _need_len(t, m, nm)
+    _need(slot_mapping, torch.int64, "slot_mapping")
+    width = 0
+    if block_tables is not None:
+        _need(block_tables, torch.int32, "block_tables")
+        if block_tables.dim() != 2 or block_tables.shape[0] != n:
+            raise ValueError(f"block_tables: shape {tuple(block_tables.shape)}, expected ({n}, W)")
+        width = block_tables.shape[1]
+    st = _stream_on_device(stream, ("block_table", tables.block_table), ("seq_rows", seq_rows),
+                           ("cached_lens", cached_lens), ("new_lens", new_lens),
+                           ("block_tables", block_tables), ("context_lens", context_lens),
+                           ("query_start_loc", query_start_loc), ("slot_mapping", slot_mapping),
+                           ("positions", positions), ("free_count_out", free_count_out))
+    _check(lib().pkv_tables_step(ctypes.byref(tables.desc), _ptr(seq_rows), _ptr(cached_lens),
+                                 _ptr(new_lens), n, T, _ptr(free_count_out), _ptr(block_tables),
+                                 width, _ptr(context_lens), _ptr(query_start_loc),
+                                 _ptr(slot_mapping), _ptr(positions), st), "pkv_tables_step")
+
+
+def pkv_tables_release(tables, seq_rows, lens, stream=None):
+    """Give back the blocks of rows ``seq_rows`` (CUDA int32 [n]; None: row i) of a
+    DeviceTables, which hold ``lens`` (CUDA int32 [n]) tokens."""
+    n = lens.shape[0]
+    _need(lens, torch.int32, "lens")
+    if seq_rows is not None:
+        _need(seq_rows, torch.int32, "seq_rows")
+        _need_len(seq_rows, n, "seq_rows")
+    st = _stream_on_device(stream, ("block_table", tables.block_table), ("seq_rows", seq_rows),
+                           ("lens", lens))
+    _check(lib().pkv_tables_release(ctypes.byref(tables.desc), _ptr(seq_rows), _ptr(lens), n, st),
+           "pkv_tables_release")
+
+
+# ----------------------------------------------------------------------------
+# sparse attention over selected blocks
+# ----------------------------------------------------------------------------
+class BlockBounds:
+    """Key bounds beside a cache: int8 codes [NB, Hkv, 2, D] and exponents
+    [NB, Hkv] (see pkv_block_bounds in include/pagedkv.h)."""
+
+    def __init__(self, num_blocks, num_kv_heads, head_dim, device="cuda"):
+        self.bounds = torch.zeros((num_blocks, num_kv_heads, 2, head_dim), dtype=torch.int8,
+                                  device=device)
+        self.exps = torch.zeros((num_blocks, num_kv_heads), dtype=torch.int8, device=device)
+
+
+def _need_shape(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+
+
+def _need_cache(t, desc, name):
+    _need(t, _TORCH_DTYPE[desc.dtype], name)
+    _need_shape(t, (desc.num_blocks, desc.num_kv_heads, desc.block_size, desc.head_dim), name)
+
+
+def _need_batch(desc, block_tables, context_lens, query_start_loc, num_tokens):
+    """Checks of the sparse entry points' batch; the number of sequences."""
+    n = context_lens.shape[0]
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError(f"block_tables: shape {tuple(block_tables.shape)}, expected ({n}, W)")
+    if query_start_loc is not None:
+        _need(query_start_loc, torch.int32, "query_start_loc")
+        _need_len(query_start_loc, n + 1, "query_start_loc")
+    elif num_tokens != n:
+        raise ValueError(f"{num_tokens} query tokens for {n} sequences need query_start_loc")
+    return n
+
+
+def pkv_block_bounds(bounds, exps, k_cache, desc, block_tables, context_lens,
+                     query_start_loc=None, num_query_tokens=None, stream=None):
+    """Bring the key bounds (CUDA int8 [NB, Hkv, 2, D], exps int8 [NB, Hkv]) of the
+    blocks that a step's tokens were appended to up to date.  One new token per
+    sequence, or query_start_loc (CUDA int32 [S + 1]) and the number of tokens."""
+    n = context_lens.shape[0]
+    tokens = n if num_query_tokens is None else num_query_tokens
+    _need_cache(k_cache, desc, "k_cache")
+    _need(bounds, torch.int8, "bounds")
+    _need(exps, torch.int8, "exps")
+    _need_shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim), "bounds")
+    _need_shape(exps, (desc.num_blocks, desc.num_kv_heads), "exps")
+    _need_batch(desc, block_tables, context_lens, query_start_loc, tokens)
+    st = _stream_on_device(stream, ("bounds", bounds), ("exps", exps), ("k_cache", k_cache),
+                           ("block_tables", block_tables), ("context_lens", context_lens),
+                           ("query_start_loc", query_start_loc))
+    _check(lib().pkv_block_bounds(_ptr(bounds), _ptr(exps), _ptr(k_cache), ctypes.byref(desc),
+                                  _ptr(block_tables), block_tables.shape[1],
+                                  _ptr(query_start_loc), _ptr(context_lens), n, tokens, st),
+           "pkv_block_bounds")
+
+
+def select_workspace_bytes(desc, num_query_tokens, max_context_len):
+    return int(lib().pkv_select_workspace_bytes(ctypes.byref(desc), num_query_tokens,
+                                                max_context_len))
+
+
+def pkv_select_blocks(selected, q, bounds, exps, desc, block_tables, context_lens,
+                      max_context_len, num_sink, num_recent, query_start_loc=None, ws=None,
+                      stream=None):
+    """List the blocks that each (query token, KV head) attends: selected CUDA int32
+    [T, Hkv, top_k], q [T, Hq, D]."""
+    T, top_k = q.shape[0], selected.shape[-1]
+    _need(q, _TORCH_DTYPE[desc.dtype], "q")
+    _need(bounds, torch.int8, "bounds")
+    _need(exps, torch.int8, "exps")
+    _need(selected, torch.int32, "selected")
+    _need_shape(q, (T, desc.num_q_heads, desc.head_dim), "q")
+    _need_shape(selected, (T, desc.num_kv_heads, top_k), "selected")
+    _need_shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim), "bounds")
+    _need_shape(exps, (desc.num_blocks, desc.num_kv_heads), "exps")
+    n = _need_batch(desc, block_tables, context_lens, query_start_loc, T)
+    st = _stream_on_device(stream, ("selected", selected), ("q", q), ("bounds", bounds),
+                           ("exps", exps), ("block_tables", block_tables),
+                           ("context_lens", context_lens), ("query_start_loc", query_start_loc),
+                           ("ws", ws))
+    if ws is None:
+        ws = workspace(select_workspace_bytes(desc, T, max_context_len), q.device)
+    _check(lib().pkv_select_blocks(_ptr(selected), _ptr(q), _ptr(bounds), _ptr(exps),
+                                   ctypes.byref(desc), _ptr(block_tables), block_tables.shape[1],
+                                   _ptr(query_start_loc), _ptr(context_lens), n, T,
+                                   max_context_len, top_k, num_sink, num_recent, _ptr(ws),
+                                   ws.numel(), st), "pkv_select_blocks")
+    return selected
+
+
+def paged_attention_sparse(out, q, k_cache, v_cache, desc, block_tables, context_lens, selected,
+                           query_start_loc=None, scale=None, stream=None):
+    """Attention of each (query token, KV head) over the blocks that ``selected``
+    (CUDA int32 [T, Hkv, top_k], logical block indices, negative ones skipped)
+    lists; out, q: CUDA [T, Hq, D]."""
+    T = q.shape[0]
+    dt = _TORCH_DTYPE[desc.dtype]
+    _need(out, dt, "out")
+    _need(q, dt, "q")
+    _need_cache(k_cache, desc, "k_cache")
+    _need_cache(v_cache, desc, "v_cache")
+    _need(selected, torch.int32, "selected")
+    top_k = selected.shape[-1]
+    _need_shape(q, (T, desc.num_q_heads, desc.head_dim), "q")
+    _need_shape(out, (T, desc.num_q_heads, desc.head_dim), "out")
+    _need_shape(selected, (T, desc.num_kv_heads, top_k), "selected")
+    n = _need_batch(desc, block_tables, context_lens, query_start_loc, T)
+    if scale is None:
+        scale = 1.0 / math.sqrt(desc.head_dim)
+    st = _stream_on_device(stream, ("out", out), ("q", q), ("k_cache", k_cache),
+                           ("v_cache", v_cache), ("block_tables", block_tables),
+                           ("context_lens", context_lens), ("selected", selected),
+                           ("query_start_loc", query_start_loc))
+    _check(lib().paged_attention_sparse(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                        ctypes.byref(desc), _ptr(block_tables),
+                                        block_tables.shape[1], _ptr(query_start_loc),
+                                        _ptr(context_lens), _ptr(selected), top_k, n, T, scale,
+                                        st), "paged_attention_sparse")
     return out
 
 

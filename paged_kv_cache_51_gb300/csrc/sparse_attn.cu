@@ -1,0 +1,417 @@
+// Attention over a list of blocks for each query row and KV head
+// (paged_attention_sparse): exact softmax(q K^T * scale) V over the keys of the
+// listed blocks that the row sees.
+//
+// Each (query row, KV head) reads top_k tiles of K and of V, scattered over the
+// pool, and nothing is read twice, so the work is bound by HBM for a batch and
+// by latency for a few rows.  A cluster of CTAs shares one (row, head): the
+// listed blocks go round the cluster's warps, every warp keeps a running
+// (max, sum, output) of its own and a ring of tiles that it fills with
+// asynchronous copies itself, so that no warp waits for another before the end;
+// the states are then merged inside the CTA and, through distributed shared
+// memory, across the cluster, in a fixed order and without a workspace.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "launch_cache.h"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "sparse_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+struct SparseParams {
+    void* out;
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* selected;       // [tokens][Hkv][top_k]
+    QueryRows rows;
+    int32_t num_blocks, num_q_heads, num_kv_heads, top_k;
+    float scale_log2;
+    int* err;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+// shared::cluster address of `addr` (this CTA's shared memory) in CTA `rank`
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <typename T, int D, int G>
+struct SparseCfg {
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kTileBytes = kBlockTokens * D * int(sizeof(T));
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kStages = sizeof(T) == 2 && D == 128 ? 3 : D == 64 ? 4 : 2;
+    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kQOff = kRingBytes;                          // q as fp32 [G][D]
+    static constexpr int kPOff = kQOff + G * D * 4;                   // weights [warp][G][16]
+    static constexpr int kRec = G * (D + 2) + 1;                      // o, m, l, keys seen
+    static constexpr int kCombOff = kPOff + kWarps * G * kBlockTokens * 4;
+    static constexpr int kMergedOff = kCombOff + kWarps * kRec * 4;   // the CTA's state
+    static constexpr int kSmem = kMergedOff + kRec * 4;
+};
+
+// 16-byte chunk c of tile row r, so that the reads of eight lanes (four rows,
+// two neighbouring chunks) fall into eight different bank groups
+__device__ __forceinline__ int chunk_at(int r, int c) { return c ^ ((r & 3) << 1); }
+
+template <typename T>
+__device__ __forceinline__ void widen16(const void* p, float* x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// Merge the CTA's warp states (records in shared memory), then the cluster's,
+// and write the outputs of the (row, head): shared by every variant.
+template <typename T, int D, int G, int kWarps, int kRec>
+__device__ __forceinline__ void merge_and_write(const SparseParams& p, const float* comb,
+                                                float* merged, int t, int h) {
+    constexpr int kThreads = kWarps * 32;
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * D; i += kThreads) {
+        const int g = i / D;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[w * kRec + G * D + g]);
+        const float Mx = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float* r = comb + w * kRec;
+            const float s = exp2f(r[G * D + g] - Mx);
+            L = fmaf(r[G * D + G + g], s, L);
+            O = fmaf(r[i], s, O);
+        }
+        merged[i] = O;
+        if (i % D == 0) {
+            merged[G * D + g] = M;
+            merged[G * D + G + g] = L;
+        }
+    }
+    if (threadIdx.x == 0) {
+        float seen = 0.f;
+        for (int w = 0; w < kWarps; ++w) seen += comb[w * kRec + G * (D + 2)];
+        merged[G * (D + 2)] = seen;
+    }
+    const uint32_t cs = cluster_size(), rank = cluster_rank();
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    const uint32_t base = smem_u32(merged);
+    T* out = static_cast<T*>(p.out) + (size_t(t) * p.num_q_heads + size_t(h) * G) * D;
+    for (int i = int(rank) * kThreads + threadIdx.x; i < G * D; i += int(cs) * kThreads) {
+        const int g = i / D;
+        float M = -INFINITY, L = 0.f, O = 0.f, seen = 0.f;
+        for (uint32_t c = 0; c < cs; ++c)
+            M = fmaxf(M, ld_cluster(map_rank(base + (G * D + g) * 4, c)));
+        const float Mx = M == -INFINITY ? 0.f : M;
+        for (uint32_t c = 0; c < cs; ++c) {
+            const uint32_t r = map_rank(base, c);
+            const float s = exp2f(ld_cluster(r + (G * D + g) * 4) - Mx);
+            L = fmaf(ld_cluster(r + (G * D + G + g) * 4), s, L);
+            O = fmaf(ld_cluster(r + i * 4), s, O);
+            seen += ld_cluster(r + G * (D + 2) * 4);
+        }
+        // a row whose list names no key it sees is 0
+        out[i] = Elem<T>::store_val(seen > 0.f ? O / L : 0.f);
+    }
+    if (cs > 1) cluster_sync();          // the others have read this CTA's state
+}
+
+// A warp's own list entries: tile j of the warp is entry first + j * stride.
+// Entry -> logical block -> physical block, 32 tiles at a time.
+struct ListCursor {
+    int phys, logical;                   // this lane's tile of the current 32
+};
+__device__ __forceinline__ ListCursor fetch_tiles(const SparseParams& p, const int32_t* list,
+                                                  int seq, int blocks, int e) {
+    ListCursor c{-1, 0};
+    if (e < p.top_k) {
+        const int b = list[e];
+        if (b >= blocks) {
+            flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
+        } else if (b >= 0) {
+            const int id = p.rows.block_tables[size_t(seq) * p.rows.table_stride + b];
+            if (id < 0 || id >= p.num_blocks) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
+            else c = ListCursor{id, b};
+        }
+    }
+    return c;
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kernel(SparseParams p) {
+    using C = SparseCfg<T, D, G>;
+    constexpr int V = 16 / int(sizeof(T));       // elements of a 16-byte chunk
+    constexpr int RC = D / V;                    // chunks of a row
+    constexpr int DL = D / 32;                   // output dimensions of a lane
+    extern __shared__ __align__(128) unsigned char smem[];
+    float* qs = reinterpret_cast<float*>(smem + C::kQOff);
+    float* comb = reinterpret_cast<float*>(smem + C::kCombOff);
+    float* merged = reinterpret_cast<float*>(smem + C::kMergedOff);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t cs = cluster_size(), rank = cluster_rank();
+    const int item = int(blockIdx.x / cs);
+    const int t = item / p.num_kv_heads, h = item % p.num_kv_heads;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    int seq;
+    const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    if (keys < 0) return;                        // the whole cluster: left as it is
+    const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
+    for (int i = threadIdx.x; i < G * D; i += C::kThreads)
+        qs[i] = float(static_cast<const T*>(p.q)[(size_t(t) * p.num_q_heads + size_t(h) * G) * D + i]);
+    __syncthreads();
+
+    const int32_t* list = p.selected + size_t(item) * p.top_k;
+    const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
+    const int tiles = p.top_k > first ? (p.top_k - first + stride - 1) / stride : 0;
+    unsigned char* ring = smem + warp * (C::kStages * C::kStageBytes);
+    const uint32_t ring_u = smem_u32(ring);
+    float* ps = reinterpret_cast<float*>(smem + C::kPOff) + warp * (G * kBlockTokens);
+
+    ListCursor next{-1, 0}, now{-1, 0};          // tiles being requested, tiles being used
+    auto request = [&](int j) {
+        if (j < tiles) {
+            if (j % 32 == 0) next = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+            const int id = __shfl_sync(kFull, next.phys, j % 32);
+            if (id >= 0) {
+                const size_t off = (size_t(id) * p.num_kv_heads + h) * (kBlockTokens * D);
+                const T* ks = static_cast<const T*>(p.k_cache) + off;
+                const T* vs = static_cast<const T*>(p.v_cache) + off;
+                const uint32_t dst = ring_u + (j % C::kStages) * C::kStageBytes;
+#pragma unroll
+                for (int i = 0; i < kBlockTokens * RC / 32; ++i) {
+                    const int idx = i * 32 + lane, r = idx / RC, c = idx % RC;
+                    const uint32_t at = dst + (r * RC + chunk_at(r, c)) * 16;
+                    cp_async16(at, ks + idx * V);
+                    cp_async16(at + C::kTileBytes, vs + idx * V);
+                }
+            }
+        }
+        cp_commit();
+    };
+    for (int j = 0; j < C::kStages - 1; ++j) request(j);
+
+    float o[G][DL], m[G], l[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        m[g] = -INFINITY;
+        l[g] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) o[g][d] = 0.f;
+    }
+    int seen = 0;
+    const int key = lane >> 1, half = lane & 1;
+    for (int j = 0; j < tiles; ++j) {
+        request(j + C::kStages - 1);
+        if (j % 32 == 0) now = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+        const int id = __shfl_sync(kFull, now.phys, j % 32);
+        const int b = __shfl_sync(kFull, now.logical, j % 32);
+        cp_wait<C::kStages - 1>();
+        __syncwarp();
+        if (id < 0) continue;
+        const unsigned char* kt = ring + (j % C::kStages) * C::kStageBytes;
+        const unsigned char* vt = kt + C::kTileBytes;
+        const int nvalid = min(kBlockTokens, keys - b * kBlockTokens);
+        seen += nvalid;
+        // scores: two lanes a key, chunks taken in turn
+        float s[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) s[g] = 0.f;
+#pragma unroll
+        for (int i = 0; i < RC / 2; ++i) {
+            const int c = 2 * i + half;
+            float x[V];
+            widen16<T>(kt + (key * RC + chunk_at(key, c)) * 16, x);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[g] = fmaf(x[e], qs[g * D + c * V + e], s[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            s[g] += __shfl_xor_sync(kFull, s[g], 1);
+            s[g] = key < nvalid ? s[g] * p.scale_log2 : -INFINITY;
+            float mx = s[g];
+#pragma unroll
+            for (int of = 2; of < 32; of <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, of));
+            const float mn = fmaxf(m[g], mx);
+            const float mz = mn == -INFINITY ? 0.f : mn;    // nothing above -inf so far
+            const float alpha = exp2f(m[g] - mz), w = exp2f(s[g] - mz);
+            m[g] = mn;
+            l[g] = l[g] * alpha + (half ? 0.f : w);
+#pragma unroll
+            for (int d = 0; d < DL; ++d) o[g][d] *= alpha;
+            if (!half) ps[g * kBlockTokens + key] = w;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kBlockTokens; ++k) {
+            float v[DL];
+            const int byte = lane * DL * int(sizeof(T));
+            const unsigned char* src = vt + (k * RC + chunk_at(k, byte / 16)) * 16 + byte % 16;
+            Elem<T>::load(reinterpret_cast<const T*>(src), v);
+#pragma unroll
+            for (int d = 0; d < DL; ++d) v[d] = k < nvalid ? v[d] : 0.f;   // 0 x NaN is NaN
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int d = 0; d < DL; ++d) o[g][d] = fmaf(ps[g * kBlockTokens + k], v[d], o[g][d]);
+        }
+        __syncwarp();
+    }
+    cp_wait<0>();
+    float* rec = comb + warp * C::kRec;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int of = 1; of < 32; of <<= 1) l[g] += __shfl_xor_sync(kFull, l[g], of);
+#pragma unroll
+        for (int d = 0; d < DL; ++d) rec[g * D + lane * DL + d] = o[g][d];
+        if (lane == 0) {
+            rec[G * D + g] = m[g];
+            rec[G * D + G + g] = l[g];
+        }
+    }
+    if (lane == 0) rec[G * (D + 2)] = float(seen);
+    merge_and_write<T, D, G, C::kWarps, C::kRec>(p, comb, merged, t, h);
+}
+
+// CTAs that share one (row, head): enough to give every SM two CTAs, but each
+// warp at least two tiles.
+int cluster_for(int64_t items, int top_k, int warps) {
+    int cs = 1;
+    while (cs < 8 && items * cs < 2 * int64_t(num_sms()) && top_k >= 4 * cs * warps) cs *= 2;
+    return cs;
+}
+
+template <typename T, int D, int G>
+int launch_sparse(const SparseParams& p, int64_t items, cudaStream_t stream) {
+    using C = SparseCfg<T, D, G>;
+    if (kernel_occupancy<sparse_attn_kernel<T, D, G>>(C::kThreads, C::kSmem) < 1)
+        return PKV_ERR_CUDA;
+    const int cs = cluster_for(items, p.top_k, C::kWarps);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(items * cs));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cs);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, sparse_attn_kernel<T, D, G>, p));
+}
+
+template <typename T, int D>
+int launch_sparse_g(const SparseParams& p, int64_t items, cudaStream_t s) {
+    switch (p.num_q_heads / p.num_kv_heads) {
+        case 1: return launch_sparse<T, D, 1>(p, items, s);
+        case 2: return launch_sparse<T, D, 2>(p, items, s);
+        case 4: return launch_sparse<T, D, 4>(p, items, s);
+        default: return launch_sparse<T, D, 8>(p, items, s);
+    }
+}
+
+bool aligned_to(const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int paged_attention_sparse(void* out, const void* q, const void* k_cache,
+                                      const void* v_cache, const pkv_cache_desc* desc,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* query_start_loc, const int32_t* context_lens,
+                                      const int32_t* selected, int32_t top_k, int32_t num_seqs,
+                                      int32_t num_query_tokens, float scale, void* stream) {
+    int st = check_desc(desc, true);
+    if (st != PKV_OK) return st;
+    if (max_blocks_per_seq < 1 || num_seqs < 0 || num_query_tokens < 0 || top_k < 1 ||
+        !(scale - scale == 0.f))
+        return PKV_ERR_INVALID;
+    if (!query_start_loc && num_query_tokens != num_seqs) return PKV_ERR_INVALID;
+    const int64_t items = int64_t(num_query_tokens) * desc->num_kv_heads;
+    if (items * 8 > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !selected ||
+        !aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(k_cache, 16) ||
+        !aligned_to(v_cache, 16) || !aligned_to(block_tables, 4) ||
+        !aligned_to(query_start_loc, 4) || !aligned_to(context_lens, 4) ||
+        !aligned_to(selected, 4))
+        return PKV_ERR_INVALID;
+    SparseParams p;
+    p.err = device_error_ptr(&st);
+    if (st != PKV_OK) return st;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.selected = selected;
+    p.rows = QueryRows{block_tables, query_start_loc, context_lens, max_blocks_per_seq, num_seqs,
+                       INT32_MAX};
+    p.num_blocks = desc->num_blocks;
+    p.num_q_heads = desc->num_q_heads;
+    p.num_kv_heads = desc->num_kv_heads;
+    p.top_k = top_k;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (desc->dtype == PKV_BF16)
+        return desc->head_dim == 128 ? launch_sparse_g<__nv_bfloat16, 128>(p, items, cs)
+                                     : launch_sparse_g<__nv_bfloat16, 64>(p, items, cs);
+    return desc->head_dim == 128 ? launch_sparse_g<float, 128>(p, items, cs)
+                                 : launch_sparse_g<float, 64>(p, items, cs);
+}
