@@ -408,6 +408,33 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
+def _launch_stream(stream):
+    """The current CUDA device's index and the handle of a launch's stream (the
+    current one by default), which has to be on that device.  The default
+    stream's handle is asked for directly: building a stream object to read it
+    from costs more than the rest of a call's checks."""
+    current = torch.cuda.current_device()
+    if stream is None:
+        return current, torch._C._cuda_getCurrentRawStream(current)
+    _devices_agree((), current, stream.device)
+    return current, stream.cuda_stream
+
+
+def _arg(t, name, dtype, current, *shape):
+    """The address of a tensor argument, after checking its type, its layout, its
+    device and (if given) its shape: one pass of cheap tests, the message apart."""
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != current or (
+            shape and t.shape != shape):
+        _need(t, dtype, name)
+        _devices_agree([(name, t.device)], current, torch.device("cuda", current))
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, current, *shape):
+    return None if t is None else _arg(t, name, dtype, current, *shape)
+
+
 def _need(t, dtype, name):
     if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype:
         raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
@@ -703,11 +730,6 @@ class DeviceTables:
                    torch.tensor([num_blocks], dtype=torch.int32, device=device), block_size)
 
 
-def _need_len(t, n, name):
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({n},)")
-
-
 def pkv_tables_step(tables, seq_rows, cached_lens, new_lens, block_tables, context_lens,
                     query_start_loc, slot_mapping, positions=None, free_count_out=None,
                     stream=None):
@@ -718,44 +740,31 @@ def pkv_tables_step(tables, seq_rows, cached_lens, new_lens, block_tables, conte
     one token each); written: block_tables [n, W] (or None), context_lens [n],
     query_start_loc [n + 1], slot_mapping (int64 [T], T the most tokens of the
     step), positions [T] (or None), free_count_out [1] (None: in place)."""
-    n = cached_lens.shape[0]
-    T = slot_mapping.shape[0]
-    for t, nm, m in ((seq_rows, "seq_rows", n), (cached_lens, "cached_lens", n),
-                     (new_lens, "new_lens", n), (context_lens, "context_lens", n),
-                     (query_start_loc, "query_start_loc", n + 1), (positions, "positions", T),
-                     (free_count_out, "free_count_out", 1)):
-        if t is not None:
-            _need(t, torch.int32, nm)
-            _need_len(t, m, nm)
-    _need(slot_mapping, torch.int64, "slot_mapping")
-    width = 0
-    if block_tables is not None:
-        _need(block_tables, torch.int32, "block_tables")
-        if block_tables.dim() != 2 or block_tables.shape[0] != n:
-            raise ValueError(f"block_tables: shape {tuple(block_tables.shape)}, expected ({n}, W)")
-        width = block_tables.shape[1]
-    st = _stream_on_device(stream, ("block_table", tables.block_table), ("seq_rows", seq_rows),
-                           ("cached_lens", cached_lens), ("new_lens", new_lens),
-                           ("block_tables", block_tables), ("context_lens", context_lens),
-                           ("query_start_loc", query_start_loc), ("slot_mapping", slot_mapping),
-                           ("positions", positions), ("free_count_out", free_count_out))
-    _check(lib().pkv_tables_step(ctypes.byref(tables.desc), _ptr(seq_rows), _ptr(cached_lens),
-                                 _ptr(new_lens), n, T, _ptr(free_count_out), _ptr(block_tables),
-                                 width, _ptr(context_lens), _ptr(query_start_loc),
-                                 _ptr(slot_mapping), _ptr(positions), st), "pkv_tables_step")
+    n, T = cached_lens.numel(), slot_mapping.numel()
+    width = 0 if block_tables is None else block_tables.shape[-1]
+    cur, st = _launch_stream(stream)
+    i32 = torch.int32
+    _arg(tables.block_table, "block_table", i32, cur)
+    _check(lib().pkv_tables_step(
+        ctypes.byref(tables.desc), _opt(seq_rows, "seq_rows", i32, cur, n),
+        _arg(cached_lens, "cached_lens", i32, cur, n), _opt(new_lens, "new_lens", i32, cur, n),
+        n, T, _opt(free_count_out, "free_count_out", i32, cur, 1),
+        _opt(block_tables, "block_tables", i32, cur, n, width), width,
+        _arg(context_lens, "context_lens", i32, cur, n),
+        _arg(query_start_loc, "query_start_loc", i32, cur, n + 1),
+        _arg(slot_mapping, "slot_mapping", torch.int64, cur, T),
+        _opt(positions, "positions", i32, cur, T), st), "pkv_tables_step")
 
 
 def pkv_tables_release(tables, seq_rows, lens, stream=None):
     """Give back the blocks of rows ``seq_rows`` (CUDA int32 [n]; None: row i) of a
     DeviceTables, which hold ``lens`` (CUDA int32 [n]) tokens."""
-    n = lens.shape[0]
-    _need(lens, torch.int32, "lens")
-    if seq_rows is not None:
-        _need(seq_rows, torch.int32, "seq_rows")
-        _need_len(seq_rows, n, "seq_rows")
-    st = _stream_on_device(stream, ("block_table", tables.block_table), ("seq_rows", seq_rows),
-                           ("lens", lens))
-    _check(lib().pkv_tables_release(ctypes.byref(tables.desc), _ptr(seq_rows), _ptr(lens), n, st),
+    n = lens.numel()
+    cur, st = _launch_stream(stream)
+    _arg(tables.block_table, "block_table", torch.int32, cur)
+    _check(lib().pkv_tables_release(ctypes.byref(tables.desc),
+                                    _opt(seq_rows, "seq_rows", torch.int32, cur, n),
+                                    _arg(lens, "lens", torch.int32, cur, n), n, st),
            "pkv_tables_release")
 
 
@@ -772,29 +781,16 @@ class BlockBounds:
         self.exps = torch.zeros((num_blocks, num_kv_heads), dtype=torch.int8, device=device)
 
 
-def _need_shape(t, shape, name):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-
-
-def _need_cache(t, desc, name):
-    _need(t, _TORCH_DTYPE[desc.dtype], name)
-    _need_shape(t, (desc.num_blocks, desc.num_kv_heads, desc.block_size, desc.head_dim), name)
-
-
-def _need_batch(desc, block_tables, context_lens, query_start_loc, num_tokens):
-    """Checks of the sparse entry points' batch; the number of sequences."""
-    n = context_lens.shape[0]
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    if block_tables.dim() != 2 or block_tables.shape[0] != n:
-        raise ValueError(f"block_tables: shape {tuple(block_tables.shape)}, expected ({n}, W)")
-    if query_start_loc is not None:
-        _need(query_start_loc, torch.int32, "query_start_loc")
-        _need_len(query_start_loc, n + 1, "query_start_loc")
-    elif num_tokens != n:
+def _batch_args(block_tables, context_lens, query_start_loc, num_tokens, cur):
+    """Addresses of a sparse entry point's batch (tables, their width, layout,
+    contexts) and its number of sequences, checked."""
+    n, width = context_lens.numel(), block_tables.shape[-1]
+    if query_start_loc is None and num_tokens != n:
         raise ValueError(f"{num_tokens} query tokens for {n} sequences need query_start_loc")
-    return n
+    i32 = torch.int32
+    return (_arg(block_tables, "block_tables", i32, cur, n, width), width,
+            _opt(query_start_loc, "query_start_loc", i32, cur, n + 1),
+            _arg(context_lens, "context_lens", i32, cur, n), n)
 
 
 def pkv_block_bounds(bounds, exps, k_cache, desc, block_tables, context_lens,
@@ -802,21 +798,16 @@ def pkv_block_bounds(bounds, exps, k_cache, desc, block_tables, context_lens,
     """Bring the key bounds (CUDA int8 [NB, Hkv, 2, D], exps int8 [NB, Hkv]) of the
     blocks that a step's tokens were appended to up to date.  One new token per
     sequence, or query_start_loc (CUDA int32 [S + 1]) and the number of tokens."""
-    n = context_lens.shape[0]
-    tokens = n if num_query_tokens is None else num_query_tokens
-    _need_cache(k_cache, desc, "k_cache")
-    _need(bounds, torch.int8, "bounds")
-    _need(exps, torch.int8, "exps")
-    _need_shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim), "bounds")
-    _need_shape(exps, (desc.num_blocks, desc.num_kv_heads), "exps")
-    _need_batch(desc, block_tables, context_lens, query_start_loc, tokens)
-    st = _stream_on_device(stream, ("bounds", bounds), ("exps", exps), ("k_cache", k_cache),
-                           ("block_tables", block_tables), ("context_lens", context_lens),
-                           ("query_start_loc", query_start_loc))
-    _check(lib().pkv_block_bounds(_ptr(bounds), _ptr(exps), _ptr(k_cache), ctypes.byref(desc),
-                                  _ptr(block_tables), block_tables.shape[1],
-                                  _ptr(query_start_loc), _ptr(context_lens), n, tokens, st),
-           "pkv_block_bounds")
+    cur, st = _launch_stream(stream)
+    nb, hkv, d = desc.num_blocks, desc.num_kv_heads, desc.head_dim
+    tokens = context_lens.numel() if num_query_tokens is None else num_query_tokens
+    t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, tokens,
+                                          cur)
+    _check(lib().pkv_block_bounds(
+        _arg(bounds, "bounds", torch.int8, cur, nb, hkv, 2, d),
+        _arg(exps, "exps", torch.int8, cur, nb, hkv),
+        _arg(k_cache, "k_cache", _TORCH_DTYPE[desc.dtype], cur, nb, hkv, desc.block_size, d),
+        ctypes.byref(desc), t, width, start, ctx, n, tokens, st), "pkv_block_bounds")
 
 
 def select_workspace_bytes(desc, num_query_tokens, max_context_len):
@@ -829,27 +820,19 @@ def pkv_select_blocks(selected, q, bounds, exps, desc, block_tables, context_len
                       stream=None):
     """List the blocks that each (query token, KV head) attends: selected CUDA int32
     [T, Hkv, top_k], q [T, Hq, D]."""
+    cur, st = _launch_stream(stream)
+    nb, hkv, d = desc.num_blocks, desc.num_kv_heads, desc.head_dim
     T, top_k = q.shape[0], selected.shape[-1]
-    _need(q, _TORCH_DTYPE[desc.dtype], "q")
-    _need(bounds, torch.int8, "bounds")
-    _need(exps, torch.int8, "exps")
-    _need(selected, torch.int32, "selected")
-    _need_shape(q, (T, desc.num_q_heads, desc.head_dim), "q")
-    _need_shape(selected, (T, desc.num_kv_heads, top_k), "selected")
-    _need_shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim), "bounds")
-    _need_shape(exps, (desc.num_blocks, desc.num_kv_heads), "exps")
-    n = _need_batch(desc, block_tables, context_lens, query_start_loc, T)
-    st = _stream_on_device(stream, ("selected", selected), ("q", q), ("bounds", bounds),
-                           ("exps", exps), ("block_tables", block_tables),
-                           ("context_lens", context_lens), ("query_start_loc", query_start_loc),
-                           ("ws", ws))
+    t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, T, cur)
     if ws is None:
         ws = workspace(select_workspace_bytes(desc, T, max_context_len), q.device)
-    _check(lib().pkv_select_blocks(_ptr(selected), _ptr(q), _ptr(bounds), _ptr(exps),
-                                   ctypes.byref(desc), _ptr(block_tables), block_tables.shape[1],
-                                   _ptr(query_start_loc), _ptr(context_lens), n, T,
-                                   max_context_len, top_k, num_sink, num_recent, _ptr(ws),
-                                   ws.numel(), st), "pkv_select_blocks")
+    _check(lib().pkv_select_blocks(
+        _arg(selected, "selected", torch.int32, cur, T, hkv, top_k),
+        _arg(q, "q", _TORCH_DTYPE[desc.dtype], cur, T, desc.num_q_heads, d),
+        _arg(bounds, "bounds", torch.int8, cur, nb, hkv, 2, d),
+        _arg(exps, "exps", torch.int8, cur, nb, hkv), ctypes.byref(desc), t, width, start, ctx,
+        n, T, max_context_len, top_k, num_sink, num_recent,
+        _arg(ws, "ws", torch.uint8, cur), ws.numel(), st), "pkv_select_blocks")
     return selected
 
 
@@ -858,29 +841,19 @@ def paged_attention_sparse(out, q, k_cache, v_cache, desc, block_tables, context
     """Attention of each (query token, KV head) over the blocks that ``selected``
     (CUDA int32 [T, Hkv, top_k], logical block indices, negative ones skipped)
     lists; out, q: CUDA [T, Hq, D]."""
-    T = q.shape[0]
-    dt = _TORCH_DTYPE[desc.dtype]
-    _need(out, dt, "out")
-    _need(q, dt, "q")
-    _need_cache(k_cache, desc, "k_cache")
-    _need_cache(v_cache, desc, "v_cache")
-    _need(selected, torch.int32, "selected")
-    top_k = selected.shape[-1]
-    _need_shape(q, (T, desc.num_q_heads, desc.head_dim), "q")
-    _need_shape(out, (T, desc.num_q_heads, desc.head_dim), "out")
-    _need_shape(selected, (T, desc.num_kv_heads, top_k), "selected")
-    n = _need_batch(desc, block_tables, context_lens, query_start_loc, T)
+    cur, st = _launch_stream(stream)
+    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    T, top_k, dt = q.shape[0], selected.shape[-1], _TORCH_DTYPE[desc.dtype]
+    pool = (desc.num_blocks, hkv, desc.block_size, d)
+    t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, T, cur)
     if scale is None:
-        scale = 1.0 / math.sqrt(desc.head_dim)
-    st = _stream_on_device(stream, ("out", out), ("q", q), ("k_cache", k_cache),
-                           ("v_cache", v_cache), ("block_tables", block_tables),
-                           ("context_lens", context_lens), ("selected", selected),
-                           ("query_start_loc", query_start_loc))
-    _check(lib().paged_attention_sparse(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                        ctypes.byref(desc), _ptr(block_tables),
-                                        block_tables.shape[1], _ptr(query_start_loc),
-                                        _ptr(context_lens), _ptr(selected), top_k, n, T, scale,
-                                        st), "paged_attention_sparse")
+        scale = 1.0 / math.sqrt(d)
+    _check(lib().paged_attention_sparse(
+        _arg(out, "out", dt, cur, T, hq, d), _arg(q, "q", dt, cur, T, hq, d),
+        _arg(k_cache, "k_cache", dt, cur, *pool), _arg(v_cache, "v_cache", dt, cur, *pool),
+        ctypes.byref(desc), t, width, start, ctx,
+        _arg(selected, "selected", torch.int32, cur, T, hkv, top_k), top_k, n, T, scale, st),
+        "paged_attention_sparse")
     return out
 
 

@@ -36,8 +36,11 @@ struct SparseParams {
     int* err;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes to shared memory, or 16 bytes of zeros without reading (`live` false)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -109,9 +112,9 @@ __device__ __forceinline__ void widen16(const void* p, float* x) {
 
 // Merge the CTA's warp states (records in shared memory), then the cluster's,
 // and write the outputs of the (row, head): shared by every variant.
-template <typename T, int D, int G, int kWarps, int kRec>
+template <typename T, int D, int kWarps, int kRec>
 __device__ __forceinline__ void merge_and_write(const SparseParams& p, const float* comb,
-                                                float* merged, int t, int h) {
+                                                float* merged, int t, int h, int G) {
     constexpr int kThreads = kWarps * 32;
     __syncthreads();
     for (int i = threadIdx.x; i < G * D; i += kThreads) {
@@ -224,12 +227,14 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
                 const T* ks = static_cast<const T*>(p.k_cache) + off;
                 const T* vs = static_cast<const T*>(p.v_cache) + off;
                 const uint32_t dst = ring_u + (j % C::kStages) * C::kStageBytes;
+                // rows past the row's keys are zero (they may hold anything; 0 x NaN is NaN)
+                const int live = keys - __shfl_sync(kFull, next.logical, j % 32) * kBlockTokens;
 #pragma unroll
                 for (int i = 0; i < kBlockTokens * RC / 32; ++i) {
                     const int idx = i * 32 + lane, r = idx / RC, c = idx % RC;
                     const uint32_t at = dst + (r * RC + chunk_at(r, c)) * 16;
-                    cp_async16(at, ks + idx * V);
-                    cp_async16(at + C::kTileBytes, vs + idx * V);
+                    cp_async16(at, ks + idx * V, r < live);
+                    cp_async16(at + C::kTileBytes, vs + idx * V, r < live);
                 }
             }
         }
@@ -297,8 +302,6 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
             const unsigned char* src = vt + (k * RC + chunk_at(k, byte / 16)) * 16 + byte % 16;
             Elem<T>::load(reinterpret_cast<const T*>(src), v);
 #pragma unroll
-            for (int d = 0; d < DL; ++d) v[d] = k < nvalid ? v[d] : 0.f;   // 0 x NaN is NaN
-#pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int d = 0; d < DL; ++d) o[g][d] = fmaf(ps[g * kBlockTokens + k], v[d], o[g][d]);
@@ -319,7 +322,208 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<T, D, G, C::kWarps, C::kRec>(p, comb, merged, t, h);
+    merge_and_write<T, D, C::kWarps, C::kRec>(p, comb, merged, t, h, G);
+}
+
+// ---- bf16 on tensor cores -------------------------------------------------------
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// d += a (16 x 16) . b (16 x 8): this lane's a0, a2 of row lane / 4, a1, a3 of row lane / 4 + 8
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 lo, __nv_bfloat16 hi) {
+    const __nv_bfloat162 v(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int D>
+struct SparseMmaCfg {
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kMaxG = 8;
+    static constexpr int kTileBytes = kBlockTokens * D * 2;
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kRec = kMaxG * (D + 2) + 1;
+    static constexpr int kSmem = kRingBytes + kRec * 4;   // the warps' records go over the ring
+    static_assert(kWarps * kRec * 4 <= kRingBytes, "records fit into the ring");
+};
+
+// The same work on warp-level tensor-core products (m16n8k16): S = q K^T with
+// the group's query heads as rows 0 .. G-1, then O += P V.  The 16-row tile has
+// eight rows to spare; the second product puts them to use: rows 0-7 carry P
+// rounded to bf16 and rows 8-15 what that rounding left, so P enters the
+// product to 2^-16 of itself at no extra instruction.
+template <int D>
+__global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_kernel(SparseParams p) {
+    using C = SparseMmaCfg<D>;
+    constexpr int RC = D / 8;                    // 16-byte chunks of a row
+    extern __shared__ __align__(128) unsigned char smem[];
+    float* comb = reinterpret_cast<float*>(smem);
+    float* merged = reinterpret_cast<float*>(smem + C::kRingBytes);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gid = lane >> 2, tig = lane & 3, mi = lane >> 3;
+    const int G = p.num_q_heads / p.num_kv_heads;
+    const uint32_t cs = cluster_size(), rank = cluster_rank();
+    const int item = int(blockIdx.x / cs);
+    const int t = item / p.num_kv_heads, h = item % p.num_kv_heads;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    int seq;
+    const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    if (keys < 0) return;                        // the whole cluster: left as it is
+    const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
+    const int32_t* list = p.selected + size_t(item) * p.top_k;
+    const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
+    const int tiles = p.top_k > first ? (p.top_k - first + stride - 1) / stride : 0;
+    const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStageBytes);
+
+    ListCursor next{-1, 0}, now{-1, 0};
+    auto request = [&](int j) {
+        if (j < tiles) {
+            if (j % 32 == 0) next = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+            const int id = __shfl_sync(kFull, next.phys, j % 32);
+            if (id >= 0) {
+                const size_t off = (size_t(id) * p.num_kv_heads + h) * (kBlockTokens * D);
+                const __nv_bfloat16* ks = static_cast<const __nv_bfloat16*>(p.k_cache) + off;
+                const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.v_cache) + off;
+                const uint32_t dst = ring + (j % C::kStages) * C::kStageBytes;
+                // rows past the row's keys are zero (they may hold anything; 0 x NaN is NaN)
+                const int live = keys - __shfl_sync(kFull, next.logical, j % 32) * kBlockTokens;
+#pragma unroll
+                for (int i = 0; i < kBlockTokens * RC / 32; ++i) {
+                    const int idx = i * 32 + lane, r = idx / RC, c = idx % RC;
+                    // chunk c of row r lies at c ^ (r % 8): ldmatrix reads without conflicts
+                    const uint32_t at = dst + (r * RC + (c ^ (r & 7))) * 16;
+                    cp_async16(at, ks + idx * 8, r < live);
+                    cp_async16(at + C::kTileBytes, vs + idx * 8, r < live);
+                }
+            }
+        }
+        cp_commit();
+    };
+    for (int j = 0; j < C::kStages - 1; ++j) request(j);
+
+    // q as the A operand: row gid is query head gid of the group
+    uint32_t q0[D / 16], q2[D / 16];
+    {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q) +
+                            (size_t(t) * p.num_q_heads + size_t(h) * G + (gid < G ? gid : 0)) * (D / 2);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            q0[ks] = gid < G ? q[ks * 8 + tig] : 0u;
+            q2[ks] = gid < G ? q[ks * 8 + 4 + tig] : 0u;
+        }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    int seen = 0;
+    for (int j = 0; j < tiles; ++j) {
+        request(j + C::kStages - 1);
+        if (j % 32 == 0) now = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+        const int id = __shfl_sync(kFull, now.phys, j % 32);
+        const int b = __shfl_sync(kFull, now.logical, j % 32);
+        cp_wait<C::kStages - 1>();
+        __syncwarp();
+        if (id < 0) continue;
+        const uint32_t kt = ring + (j % C::kStages) * C::kStageBytes, vt = kt + C::kTileBytes;
+        const int nvalid = min(kBlockTokens, keys - b * kBlockTokens);
+        seen += nvalid;
+        // S: keys 0-7 and 8-15
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+            const int r = ((mi >> 1) << 3) + (lane & 7);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t f[4];
+                ldsm_x4(kt + (r * RC + ((ks * 2 + (mi & 1)) ^ (r & 7))) * 16, f);
+                mma16816(s0, q0[ks], 0u, q2[ks], 0u, f[0], f[1]);
+                mma16816(s1, q0[ks], 0u, q2[ks], 0u, f[2], f[3]);
+            }
+        }
+        // this lane's keys of row gid: 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig
+        float v[4] = {s0[0], s0[1], s1[0], s1[1]};
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = (i >> 1) * 8 + 2 * tig + (i & 1);
+            v[i] = key < nvalid ? v[i] * p.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, v[i]);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+        const float mn = fmaxf(m, mx);
+        const float mz = mn == -INFINITY ? 0.f : mn;     // nothing above -inf so far
+        const float alpha = exp2f(m - mz);
+        __nv_bfloat16 hi[4], lo[4];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float w = exp2f(v[i] - mz);
+            sum += w;
+            hi[i] = __float2bfloat16_rn(w);
+            lo[i] = __float2bfloat16_rn(w - __bfloat162float(hi[i]));
+        }
+        l = l * alpha + sum;
+        m = mn;
+        if (__any_sync(kFull, alpha != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                o[n][0] *= alpha;
+                o[n][1] *= alpha;
+                o[n][2] *= alpha;
+                o[n][3] *= alpha;
+            }
+        }
+        const uint32_t a0 = pack2(hi[0], hi[1]), a2 = pack2(hi[2], hi[3]);
+        const uint32_t a1 = pack2(lo[0], lo[1]), a3 = pack2(lo[2], lo[3]);
+        {
+            const int r = ((mi & 1) << 3) + (lane & 7);
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                uint32_t f[4];
+                ldsm_x4_t(vt + (r * RC + ((n * 2 + (mi >> 1)) ^ (r & 7))) * 16, f);
+                mma16816(o[2 * n], a0, a1, a2, a3, f[0], f[1]);
+                mma16816(o[2 * n + 1], a0, a1, a2, a3, f[2], f[3]);
+            }
+        }
+        __syncwarp();
+    }
+    cp_wait<0>();
+    __syncthreads();                             // every warp is done with the ring
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    float* rec = comb + warp * C::kRec;
+    if (gid < G) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+            rec[gid * D + n * 8 + 2 * tig] = o[n][0] + o[n][2];
+            rec[gid * D + n * 8 + 2 * tig + 1] = o[n][1] + o[n][3];
+        }
+        if (tig == 0) {
+            rec[G * D + gid] = m;
+            rec[G * D + G + gid] = l;
+        }
+    }
+    if (lane == 0) rec[G * (D + 2)] = float(seen);
+    merge_and_write<__nv_bfloat16, D, C::kWarps, C::kRec>(p, comb, merged, t, h, G);
 }
 
 // CTAs that share one (row, head): enough to give every SM two CTAs, but each
@@ -330,11 +534,9 @@ int cluster_for(int64_t items, int top_k, int warps) {
     return cs;
 }
 
-template <typename T, int D, int G>
+template <typename C, auto Kern>
 int launch_sparse(const SparseParams& p, int64_t items, cudaStream_t stream) {
-    using C = SparseCfg<T, D, G>;
-    if (kernel_occupancy<sparse_attn_kernel<T, D, G>>(C::kThreads, C::kSmem) < 1)
-        return PKV_ERR_CUDA;
+    if (kernel_occupancy<Kern>(C::kThreads, C::kSmem) < 1) return PKV_ERR_CUDA;
     const int cs = cluster_for(items, p.top_k, C::kWarps);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(items * cs));
@@ -350,16 +552,16 @@ int launch_sparse(const SparseParams& p, int64_t items, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, sparse_attn_kernel<T, D, G>, p));
+    return cuda_status(cudaLaunchKernelEx(&cfg, Kern, p));
 }
 
 template <typename T, int D>
 int launch_sparse_g(const SparseParams& p, int64_t items, cudaStream_t s) {
     switch (p.num_q_heads / p.num_kv_heads) {
-        case 1: return launch_sparse<T, D, 1>(p, items, s);
-        case 2: return launch_sparse<T, D, 2>(p, items, s);
-        case 4: return launch_sparse<T, D, 4>(p, items, s);
-        default: return launch_sparse<T, D, 8>(p, items, s);
+        case 1: return launch_sparse<SparseCfg<T, D, 1>, sparse_attn_kernel<T, D, 1>>(p, items, s);
+        case 2: return launch_sparse<SparseCfg<T, D, 2>, sparse_attn_kernel<T, D, 2>>(p, items, s);
+        case 4: return launch_sparse<SparseCfg<T, D, 4>, sparse_attn_kernel<T, D, 4>>(p, items, s);
+        default: return launch_sparse<SparseCfg<T, D, 8>, sparse_attn_kernel<T, D, 8>>(p, items, s);
     }
 }
 
@@ -410,8 +612,9 @@ extern "C" int paged_attention_sparse(void* out, const void* q, const void* k_ca
     p.scale_log2 = scale * 1.4426950408889634f;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (desc->dtype == PKV_BF16)
-        return desc->head_dim == 128 ? launch_sparse_g<__nv_bfloat16, 128>(p, items, cs)
-                                     : launch_sparse_g<__nv_bfloat16, 64>(p, items, cs);
+        return desc->head_dim == 128
+                   ? launch_sparse<SparseMmaCfg<128>, sparse_attn_mma_kernel<128>>(p, items, cs)
+                   : launch_sparse<SparseMmaCfg<64>, sparse_attn_mma_kernel<64>>(p, items, cs);
     return desc->head_dim == 128 ? launch_sparse_g<float, 128>(p, items, cs)
                                  : launch_sparse_g<float, 64>(p, items, cs);
 }
