@@ -1,4 +1,5 @@
-// Query rows of the sparse entry points: the sequence of a row and the keys it sees.
+// Query rows of the sparse entry points (the sequence of a row and the keys it
+// sees), and thread-block clusters.
 #pragma once
 
 #include "pkv_device.cuh"
@@ -38,23 +39,65 @@ __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int
     return lo;
 }
 
+// Whether a sequence of q query rows has a context that can be read (flagged
+// where `err` is given).
+__device__ __forceinline__ bool sequence_keys(const QueryRows& r, int seq, int q, int* err) {
+    const int ctx = r.ctx[seq];
+    if (ctx < q || ctx > r.max_ctx) {
+        flag_error(err, PKV_DEV_BAD_CONTEXT_LEN);
+        return false;
+    }
+    if (ctx > int64_t(r.table_stride) * kBlockTokens) {
+        flag_error(err, PKV_DEV_TABLE_TOO_NARROW);
+        return false;
+    }
+    return true;
+}
+
 // Keys that query row `t` of sequence `seq` sees: its context up to the row's
-// own position.  0 for a sequence whose length is out of range (flagged where
-// `err` is given), -1 for a row behind the last sequence.
+// own position.  0 for a sequence whose length is out of range, -1 for a row
+// behind the last sequence.
 __device__ __forceinline__ int row_keys(const QueryRows& r, int t, int& seq, int* err) {
     int first, q;
     seq = token_seq(r.start, r.n, t, first, q, err);
     if (seq < 0) return -1;
-    const int ctx = r.ctx[seq];
-    if (ctx < q || ctx > r.max_ctx) {
-        flag_error(err, PKV_DEV_BAD_CONTEXT_LEN);
-        return 0;
-    }
-    if (ctx > int64_t(r.table_stride) * kBlockTokens) {
-        flag_error(err, PKV_DEV_TABLE_TOO_NARROW);
-        return 0;
-    }
-    return ctx - q + (t - first) + 1;
+    return sequence_keys(r, seq, q, err) ? r.ctx[seq] - q + (t - first) + 1 : 0;
+}
+
+// ---- thread-block clusters --------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// shared::cluster address of `addr` (this CTA's shared memory) in CTA `rank`
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 }  // namespace pkv

@@ -182,116 +182,20 @@ struct SelectParams {
     const int8_t* bounds;
     const int8_t* exps;
     QueryRows rows;
-    float* scores;              // [tokens][Hkv][stride]
+    uint32_t* far_keys;         // [tokens][Hkv][stride] where a row's keys do not fit on chip
     int32_t stride;             // blocks of max_context_len, a multiple of 4
     int32_t num_blocks, num_q_heads, num_kv_heads;
     int32_t top_k, sink, recent;
+    int32_t q_f32;              // q is fp32, else bf16
     int* err;
 };
 
-constexpr int kScoreWarps = 8;
-constexpr int kWarpBlocks = 32;      // blocks that a warp scores at a time
-
-// Scores of kScoreWarps * 32 blocks for one query row and KV head.  The G query
-// heads' codes, positive and negative parts, lie in shared memory; a quad of
-// lanes takes four blocks at a time, each lane 64 bytes of their 2 D, and the
-// sums run on the packed 8-bit dot product.
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(SelectParams p) {
-    constexpr int CH = 2 * D / 64;               // 64-byte chunks of a bounds row
-    __shared__ uint32_t qc[G][2 * D / 4];        // codes: positive parts, negative parts
-    __shared__ float unit[G];
-    const int t = blockIdx.z, h = blockIdx.y;
-    pdl_wait_prerequisites();
-    pdl_launch_dependents();
-    int seq;
-    const int keys = row_keys(p.rows, t, seq, nullptr);
-    const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
-    // a row whose blocks are all taken needs no scores
-    if (keys <= 0 || blocks <= p.top_k || int(blockIdx.x) * kScoreWarps * kWarpBlocks >= blocks)
-        return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b0 = (blockIdx.x * kScoreWarps + warp) * kWarpBlocks;
-    int id = -1;
-    if (b0 + lane < blocks) id = p.rows.block_tables[size_t(seq) * p.rows.table_stride + b0 + lane];
-    const bool good = id >= 0 && id < p.num_blocks;
-    const size_t tile = good ? size_t(id) * p.num_kv_heads + h : 0;
-    const int e = good ? p.exps[tile] : 0;
-    const int quad = lane >> 2, tig = lane & 3;
-    uint4 w[4][CH];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int from = quad * 4 + k;
-        const size_t tk = __shfl_sync(kFull, (unsigned long long)tile, from);
-        const bool ok = __shfl_sync(kFull, int(good), from);
-        const uint4* src = reinterpret_cast<const uint4*>(p.bounds + tk * (2 * D)) + tig;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-            w[k][c] = ok ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    // codes of the query heads: one warp a head
-    for (int g = warp; g < G; g += kScoreWarps) {
-        constexpr int PL = D / 32;               // dimensions of a lane: consecutive
-        const T* q = static_cast<const T*>(p.q) +
-                     (size_t(t) * p.num_q_heads + size_t(h) * G + g) * D + lane * PL;
-        float x[PL], amax = 0.f;
-        bool odd = false;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            x[j] = float(q[j]);
-            odd |= !(fabsf(x[j]) <= FLT_MAX);
-            amax = fmaxf(amax, fabsf(x[j]));
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-        odd = __any_sync(kFull, odd);
-        const int eq = code_exponent(amax);
-        const float u = pow2(-eq);
-        int8_t* pos = reinterpret_cast<int8_t*>(qc[g]) + lane * PL;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            // (a query with values that are not finite has codes of 0)
-            const int c = odd ? 0 : int(fminf(fmaxf(rintf(x[j] * u), -127.f), 127.f));
-            pos[j] = int8_t(max(c, 0));
-            pos[D + j] = int8_t(min(c, 0));
-        }
-        if (lane == 0) unit[g] = pow2(eq);
-    }
-    __syncthreads();
-    if (b0 >= blocks) return;
-    float best = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        int s[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const uint4 qv = *reinterpret_cast<const uint4*>(&qc[g][c * 16 + tig * 4]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[k] = __dp4a(int(w[k][c].x), int(qv.x), s[k]);
-                s[k] = __dp4a(int(w[k][c].y), int(qv.y), s[k]);
-                s[k] = __dp4a(int(w[k][c].z), int(qv.z), s[k]);
-                s[k] = __dp4a(int(w[k][c].w), int(qv.w), s[k]);
-            }
-        }
-        // the quad's four sums of four blocks: lane tig ends with block tig's
-        const bool up = tig & 2;
-        int a0 = up ? s[2] : s[0], a1 = up ? s[3] : s[1];
-        a0 += __shfl_xor_sync(kFull, up ? s[0] : s[2], 2);
-        a1 += __shfl_xor_sync(kFull, up ? s[1] : s[3], 2);
-        const bool odd = tig & 1;
-        int sum = odd ? a1 : a0;
-        sum += __shfl_xor_sync(kFull, odd ? a0 : a1, 1);
-        best = fmaxf(best, float(sum) * unit[g]);
-    }
-    const int b = b0 + lane;
-    if (b < blocks) {
-        const float score = !good ? -INFINITY : e == kUnbounded ? INFINITY : best * pow2(e);
-        p.scores[(size_t(t) * p.num_kv_heads + h) * p.stride + b] = score;
-    }
-}
-
-constexpr int kPickThreads = 256;
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kWarpBlocks = 16;      // blocks that a warp scores at a time
+constexpr int kBins = 1024;
+constexpr int kMaxCand = kSelThreads;
+constexpr int kKeyBytes = 192 << 10; // most shared memory for a CTA's keys
 
 // Floats in an order that unsigned compare keeps (no NaN among the scores).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -299,90 +203,299 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One CTA for a query row and KV head: the top_k-th largest key by four passes
-// over 8-bit digits, then the blocks above it and the first ones equal to it,
-// in ascending order.  Blocks that are always taken have a key above all scores.
-__global__ void __launch_bounds__(kPickThreads) pick_blocks_kernel(SelectParams p) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t warp_sum[2][kPickThreads / 32];
-    __shared__ uint32_t digit_s, above_s;
+struct PickScratch {
+    uint32_t hist[kBins];
+    uint32_t cand[kMaxCand];
+    uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
+    uint32_t bin, above, inside, count, cut, take;
+};
+
+// Exclusive sums over the CTA of two values per thread.
+__device__ __forceinline__ void scan_two(uint32_t& a, uint32_t& b, PickScratch& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t a0 = a, b0 = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t ua = __shfl_up_sync(kFull, a, o), ub = __shfl_up_sync(kFull, b, o);
+        if (lane >= o) a += ua, b += ub;
+    }
+    if (lane == 31) s.warp_a[warp] = a, s.warp_b[warp] = b;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) a += s.warp_a[w], b += s.warp_b[w];
+    a -= a0;
+    b -= b0;
+}
+
+// The list of one row from the keys of its blocks, by the whole CTA.  Wanted
+// are the `want` largest keys of blocks sink .. blocks - recent - 1 (the ends are
+// always taken).  A histogram over the keys' range finds the bin that holds the
+// want-th; its few keys are ranked against one another, or, while they are more
+// than a CTA ranks at once, the bin becomes the next range.  Scores of a real
+// query spread over the bins, so one histogram and one ranking is the rule.
+__device__ __forceinline__ void pick_row(const SelectParams& p, const uint32_t* keys, int blocks,
+                                         int32_t* out, PickScratch& s) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b0 = p.sink, b1 = blocks - p.recent;
+    uint32_t want = uint32_t(p.top_k - p.sink - p.recent);
+    uint32_t cut = 0xffffffffu, take = 0;        // taken: keys above `cut`, `take` equal to it
+    if (want > 0) {
+        uint32_t lo = 0xffffffffu, hi = 0;
+        for (int b = b0 + tid; b < b1; b += kSelThreads) {
+            lo = min(lo, keys[b]);
+            hi = max(hi, keys[b]);
+        }
+        lo = __reduce_min_sync(kFull, lo);
+        hi = __reduce_max_sync(kFull, hi);
+        if (lane == 0) s.warp_a[warp] = lo, s.warp_b[warp] = hi;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) {
+            lo = min(lo, s.warp_a[w]);
+            hi = max(hi, s.warp_b[w]);
+        }
+        for (;;) {                               // the range lo .. hi holds the want-th
+            int shift = 0;
+            while ((hi - lo) >> shift >= kBins) ++shift;
+            for (int i = tid; i < kBins; i += kSelThreads) s.hist[i] = 0;
+            if (tid == 0) s.count = 0;
+            __syncthreads();
+            for (int b = b0 + tid; b < b1; b += kSelThreads) {
+                const uint32_t k = keys[b];
+                if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
+            }
+            __syncthreads();
+            // bins from above, four to a thread
+            const uint4 c = *reinterpret_cast<const uint4*>(&s.hist[kBins - 4 - 4 * tid]);
+            const uint32_t four[4] = {c.w, c.z, c.y, c.x};
+            uint32_t sum = c.x + c.y + c.z + c.w, none = 0;
+            scan_two(sum, none, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (sum < want && want <= sum + four[i]) {
+                    s.bin = uint32_t(kBins - 1 - 4 * tid - i);
+                    s.above = sum;
+                    s.inside = four[i];
+                }
+                sum += four[i];
+            }
+            __syncthreads();
+            const uint32_t inside = s.inside;
+            want -= s.above;
+            const uint32_t first = lo + (s.bin << shift);
+            const uint32_t last = min(hi, first + ((1u << shift) - 1u));
+            if (want == inside) {                // the whole bin (no key is 0: -inf's is above)
+                cut = first - 1;
+                break;
+            }
+            if (first == last) {                 // equal keys: the lower indices
+                cut = first;
+                take = want;
+                break;
+            }
+            if (inside <= kMaxCand) {
+                for (int b = b0 + tid; b < b1; b += kSelThreads) {
+                    const uint32_t k = keys[b];
+                    if (k >= first && k <= last) s.cand[atomicAdd(&s.count, 1u)] = k;
+                }
+                __syncthreads();
+                if (tid < int(inside)) {
+                    const uint32_t k = s.cand[tid];
+                    uint32_t gt = 0, ge = 0;
+                    for (uint32_t i = 0; i < inside; ++i) {
+                        gt += s.cand[i] > k;
+                        ge += s.cand[i] >= k;
+                    }
+                    if (gt < want && want <= ge) {   // the same for all keys equal to the cut
+                        s.cut = k;
+                        s.take = want - gt;
+                    }
+                }
+                __syncthreads();
+                cut = s.cut;
+                take = s.take;
+                break;
+            }
+            lo = first;
+            hi = last;
+            __syncthreads();                     // (the bin was read by all)
+        }
+    }
+    // in ascending order: neighbouring blocks to a thread, so that one scan of
+    // the counts places them
+    const int per = (blocks + kSelThreads - 1) / kSelThreads;
+    const int f = min(blocks, tid * per), e = min(blocks, f + per);
+    uint32_t above = 0, equal = 0;
+    for (int b = f; b < e; ++b) {
+        const bool end = b < b0 || b >= b1;
+        above += end || keys[b] > cut;
+        equal += !end && keys[b] == cut;
+    }
+    __syncthreads();
+    scan_two(above, equal, s);
+    for (int b = f; b < e; ++b) {
+        const bool end = b < b0 || b >= b1;
+        if (end || keys[b] > cut) {
+            out[above + min(equal, take)] = b;
+            ++above;
+        } else if (keys[b] == cut) {
+            if (equal < take) out[above + equal] = b;
+            ++equal;
+        }
+    }
+    __syncthreads();
+}
+
+// Codes of one query head (one warp): positive parts, then negative parts.
+template <int D>
+__device__ __forceinline__ void query_codes(const SelectParams& p, size_t head, uint32_t* dst,
+                                            float* unit) {
+    constexpr int PL = D / 32;                   // dimensions of a lane: consecutive
+    const int lane = threadIdx.x & 31;
+    float x[PL];
+    if (p.q_f32) {
+        Elem<float>::load(static_cast<const float*>(p.q) + head * D + lane * PL, x);
+    } else {
+        Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(p.q) + head * D + lane * PL, x);
+    }
+    float amax = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        odd |= !(fabsf(x[j]) <= FLT_MAX);
+        amax = fmaxf(amax, fabsf(x[j]));
+    }
+    // (the bits of values that are not negative order as the values do)
+    amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
+    odd = __any_sync(kFull, odd);
+    const int eq = code_exponent(amax);
+    const float u = pow2(-eq);
+    int8_t* pos = reinterpret_cast<int8_t*>(dst) + lane * PL;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        // (a query with values that are not finite has codes of 0)
+        const int c = odd ? 0 : int(fminf(fmaxf(rintf(x[j] * u), -127.f), 127.f));
+        pos[j] = int8_t(max(c, 0));
+        pos[D + j] = int8_t(min(c, 0));
+    }
+    if (lane == 0) *unit = odd ? 0.f : pow2(eq);
+}
+
+// A cluster chooses the blocks of R neighbouring query rows of one sequence for
+// one KV head, R * G query heads being its columns.  Its CTAs share the
+// sequence's blocks; a quad of lanes takes two blocks at a time, each lane 64 of
+// their 2 D bytes straight from the pool, and the sums run on the packed 8-bit
+// dot product with the columns' codes from shared memory.  A score's key goes to
+// the CTA that picks the row (through distributed shared memory, or to global
+// memory where the keys of a very long context do not fit), so the scores never
+// pass through HBM and one launch does it all.
+template <int D, int G, int R>
+__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(SelectParams p) {
+    constexpr int CH = 2 * D / 64;               // 64-byte chunks of a bounds row
+    constexpr int COLS = G * R;
+    extern __shared__ __align__(16) uint32_t near_keys[];   // [rows picked here][stride]
+    __shared__ __align__(16) uint32_t qc[COLS][2 * D / 4];
+    __shared__ float unit[COLS];
+    __shared__ __align__(16) PickScratch scratch;
+    const uint32_t cs = cluster_size(), rank = cluster_rank();
+    const int item = int(blockIdx.x / cs);
+    const int h = item % p.num_kv_heads, t = item / p.num_kv_heads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (cs > 1) cluster_arrive();                // the others' shared memory is there to write to
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    const int h = blockIdx.x % p.num_kv_heads, t = blockIdx.x / p.num_kv_heads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int seq;
-    const int keys = row_keys(p.rows, t, seq, tid == 0 && h == 0 ? p.err : nullptr);
-    if (keys < 0) return;                        // behind the last sequence: left as it is
-    const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
-    int32_t* out = p.selected + size_t(blockIdx.x) * p.top_k;
-    if (blocks <= p.top_k) {
-        for (int i = tid; i < p.top_k; i += kPickThreads) out[i] = i < blocks ? i : -1;
+    int first, q;
+    int* tell = tid == 0 && h == 0 && rank == 0 ? p.err : nullptr;
+    const int seq = token_seq(p.rows.start, p.rows.n, t, first, q, tell);
+    const int rows = seq < 0 || (t - first) % R ? 0 : min(R, first + q - t);
+    if (rows == 0) {                             // another cluster's row, or behind the last one
+        if (cs > 1) cluster_wait();
         return;
     }
-    if (h == 0) {                                // ids outside the pool score below all others
-        for (int b = tid; b < blocks; b += kPickThreads) {
-            const int id = p.rows.block_tables[size_t(seq) * p.rows.table_stride + b];
-            if (id < 0 || id >= p.num_blocks) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
-        }
-    }
-    const float* sc = p.scores + size_t(blockIdx.x) * p.stride;
-    auto key_of = [&](int b) {
-        return b < p.sink || b >= blocks - p.recent ? 0xffffffffu : ordered(sc[b]);
-    };
-    uint32_t prefix = 0, want = uint32_t(p.top_k);   // the want-th largest key under the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        hist[tid] = 0;
-        __syncthreads();
-        for (int b = tid; b < blocks; b += kPickThreads) {
-            const uint32_t k = key_of(b);
-            if (shift == 24 || (k ^ prefix) >> (shift + 8) == 0)
-                atomicAdd(&hist[k >> shift & 255u], 1u);
-        }
-        __syncthreads();
-        // keys with a larger digit than tid's: a suffix sum over the 256 bins
-        const uint32_t mine = hist[255 - tid];
-        uint32_t v = mine;
+    const int keys0 = sequence_keys(p.rows, seq, q, tell) ? p.rows.ctx[seq] - q + (t - first) + 1 : 0;
+    const int blocks_end = keys0 > 0 ? (keys0 + rows - 1 + kBlockTokens - 1) / kBlockTokens : 0;
+    const bool scored = blocks_end > p.top_k;    // otherwise every row takes all its blocks
+    for (int c = warp; scored && c < rows * G; c += kSelWarps)
+        query_codes<D>(p, size_t(t + c / G) * p.num_q_heads + size_t(h) * G + c % G, qc[c], &unit[c]);
+    __syncthreads();
+    if (cs > 1) cluster_wait();
+    const uint32_t near0 = smem_u32(near_keys);
+    if (scored) {
+        const int32_t* table = p.rows.block_tables + size_t(seq) * p.rows.table_stride;
+        const int quad = lane >> 2, tig = lane & 3;
+        const int step = int(cs) * kSelWarps * kWarpBlocks;
+        // this lane's block of the 16 (the upper half of the warp repeats the lower)
+        auto block_id = [&](int b) { return b < blocks_end ? table[b] : 0; };
+        int b0 = (int(rank) * kSelWarps + warp) * kWarpBlocks;
+        int ahead = block_id(b0 + (lane & 15));
+        for (; b0 < blocks_end; b0 += step) {
+            const int id = ahead;
+            ahead = block_id(b0 + step + (lane & 15));
+            const bool good = id >= 0 && id < p.num_blocks;
+            if (!good && h == 0 && lane < 16) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
+            const size_t tile = good ? size_t(id) * p.num_kv_heads + h : 0;
+            const int e = p.exps[tile];
+            uint4 w[2][CH];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(kFull, v, o);
-            if (lane >= o) v += u;
+            for (int k = 0; k < 2; ++k) {
+                const size_t tk = __shfl_sync(kFull, (unsigned long long)tile, quad * 2 + k);
+                const uint4* src = reinterpret_cast<const uint4*>(p.bounds + tk * (2 * D)) + tig;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) w[k][c] = __ldg(src + 4 * c);
+            }
+            // after the quad's sums: lane tig holds block 2 quad + (tig >> 1)
+            const int mine = quad * 2 + (tig >> 1);
+            const float eu = pow2(__shfl_sync(kFull, e == kUnbounded ? 0 : e, mine));
+            const int em = __shfl_sync(kFull, e, mine);
+            const bool gm = __shfl_sync(kFull, int(good), mine);
+            const int bm = b0 + mine;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r >= rows) break;
+                float best = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    int s0 = 0, s1 = 0;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(&qc[r * G + g][c * 16 + tig * 4]);
+                        s0 = __dp4a(int(w[0][c].x), int(v.x), s0);
+                        s0 = __dp4a(int(w[0][c].y), int(v.y), s0);
+                        s0 = __dp4a(int(w[0][c].z), int(v.z), s0);
+                        s0 = __dp4a(int(w[0][c].w), int(v.w), s0);
+                        s1 = __dp4a(int(w[1][c].x), int(v.x), s1);
+                        s1 = __dp4a(int(w[1][c].y), int(v.y), s1);
+                        s1 = __dp4a(int(w[1][c].z), int(v.z), s1);
+                        s1 = __dp4a(int(w[1][c].w), int(v.w), s1);
+                    }
+                    const bool up = tig & 2;
+                    int sum = up ? s1 : s0;
+                    sum += __shfl_xor_sync(kFull, up ? s0 : s1, 2);
+                    sum += __shfl_xor_sync(kFull, sum, 1);
+                    best = fmaxf(best, float(sum) * unit[r * G + g]);
+                }
+                const float score = !gm ? -INFINITY : em == kUnbounded ? INFINITY : best * eu;
+                if ((tig & 1) == 0 && bm < blocks_end) {
+                    if (p.far_keys)
+                        p.far_keys[(size_t(t + r) * p.num_kv_heads + h) * p.stride + bm] = ordered(score);
+                    else
+                        st_cluster(map_rank(near0 + (uint32_t(r) / cs * p.stride + bm) * 4, r % cs),
+                                   ordered(score));
+                }
+            }
         }
-        if (lane == 31) warp_sum[0][warp] = v;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) v += warp_sum[0][w];
-        if (v >= want && v - mine < want) {      // exactly one bin
-            digit_s = uint32_t(255 - tid);
-            above_s = v - mine;
-        }
-        __syncthreads();
-        prefix |= digit_s << shift;
-        want -= above_s;
-        __syncthreads();
     }
-    // keys above `prefix` are all taken, and the first `want` equal to it
-    uint32_t n_gt = 0, n_eq = 0;
-    for (int base = 0; base < blocks; base += kPickThreads) {
-        const int b = base + tid;
-        const uint32_t k = b < blocks ? key_of(b) : 0u;
-        const bool gt = b < blocks && k > prefix, eq = b < blocks && k == prefix;
-        const uint32_t mg = __ballot_sync(kFull, gt), me = __ballot_sync(kFull, eq);
-        if (lane == 0) {
-            warp_sum[0][warp] = __popc(mg);
-            warp_sum[1][warp] = __popc(me);
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    for (int r = int(rank); r < rows; r += int(cs)) {
+        const int blocks = keys0 > 0 ? (keys0 + r + kBlockTokens - 1) / kBlockTokens : 0;
+        const size_t row = size_t(t + r) * p.num_kv_heads + h;
+        int32_t* out = p.selected + row * p.top_k;
+        if (blocks <= p.top_k) {
+            for (int i = tid; i < p.top_k; i += kSelThreads) out[i] = i < blocks ? i : -1;
+        } else {
+            pick_row(p, p.far_keys ? p.far_keys + row * p.stride : near_keys + r / int(cs) * p.stride,
+                     blocks, out, scratch);
         }
-        __syncthreads();
-        uint32_t g0 = n_gt, e0 = n_eq;
-        for (int w = 0; w < kPickThreads / 32; ++w) {
-            if (w < warp) g0 += warp_sum[0][w], e0 += warp_sum[1][w];
-            n_gt += warp_sum[0][w];
-            n_eq += warp_sum[1][w];
-        }
-        const uint32_t below = (1u << lane) - 1u;
-        g0 += __popc(mg & below);
-        e0 += __popc(me & below);
-        // place = taken blocks in front of b
-        if (gt || (eq && e0 < want)) out[g0 + min(e0, want)] = b;
-        __syncthreads();
     }
 }
 
@@ -390,18 +503,59 @@ size_t select_stride(int32_t max_ctx) {
     return align_up(size_t(ceil_div(max_ctx, kBlockTokens)), 4);
 }
 
-template <typename T, int D, int G>
-int launch_scores(const SelectParams& p, dim3 grid, cudaStream_t s) {
-    return cuda_status(launch_pdl(block_scores_kernel<T, D, G>, grid, dim3(kScoreWarps * 32), 0, s, p));
+// CTAs that share a row group: enough for two on every SM, but 128 blocks each.
+int select_cluster(int64_t items, int max_blocks) {
+    int cs = 1;
+    while (cs < 8 && items * cs < 2 * int64_t(num_sms()) && max_blocks >= 256 * cs) cs *= 2;
+    return cs;
 }
 
-template <typename T, int D>
-int launch_scores_g(const SelectParams& p, dim3 grid, cudaStream_t s) {
+// Shared memory for the keys of the rows that one CTA picks, 0 if they do not fit.
+size_t near_bytes(int rows, int cs, int32_t stride) {
+    const size_t b = size_t(ceil_div(rows, cs)) * stride * 4;
+    return b <= size_t(kKeyBytes) ? b : 0;
+}
+
+template <int D, int G, int R>
+int launch_select_r(const SelectParams& p0, int64_t tokens, uint32_t* far_keys, cudaStream_t stream) {
+    SelectParams p = p0;
+    const int64_t items = tokens * p.num_kv_heads;
+    const int cs = select_cluster(ceil_div(items, R), p.stride);
+    const size_t smem = near_bytes(R, cs, p.stride);
+    p.far_keys = smem ? nullptr : far_keys;
+    constexpr auto kern = select_blocks_kernel<D, G, R>;
+    if (kernel_occupancy<kern>(kSelThreads, kKeyBytes) < 1) return PKV_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(items * cs));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cs);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
+}
+
+// Rows of a sequence share the reads of its bounds, up to eight columns.
+template <int D, int G>
+int launch_select_g(const SelectParams& p, int64_t tokens, uint32_t* far_keys, cudaStream_t s) {
+    return p.rows.start ? launch_select_r<D, G, 8 / G>(p, tokens, far_keys, s)
+                        : launch_select_r<D, G, 1>(p, tokens, far_keys, s);
+}
+
+template <int D>
+int launch_select(const SelectParams& p, int64_t tokens, uint32_t* far_keys, cudaStream_t s) {
     switch (p.num_q_heads / p.num_kv_heads) {
-        case 1: return launch_scores<T, D, 1>(p, grid, s);
-        case 2: return launch_scores<T, D, 2>(p, grid, s);
-        case 4: return launch_scores<T, D, 4>(p, grid, s);
-        default: return launch_scores<T, D, 8>(p, grid, s);
+        case 1: return launch_select_g<D, 1>(p, tokens, far_keys, s);
+        case 2: return launch_select_g<D, 2>(p, tokens, far_keys, s);
+        case 4: return launch_select_g<D, 4>(p, tokens, far_keys, s);
+        default: return launch_select_g<D, 8>(p, tokens, far_keys, s);
     }
 }
 
@@ -463,9 +617,10 @@ extern "C" int pkv_block_bounds(int8_t* bounds, int8_t* exps, const void* k_cach
 extern "C" size_t pkv_select_workspace_bytes(const pkv_cache_desc* desc, int32_t num_query_tokens,
                                              int32_t max_context_len) {
     if (check_desc(desc, true) != PKV_OK || num_query_tokens < 0 || max_context_len < 1) return 0;
-    return align_up(size_t(num_query_tokens) * desc->num_kv_heads * select_stride(max_context_len) *
-                        sizeof(float),
-                    256);
+    // keys that fit on chip whatever the cluster need no workspace
+    const size_t stride = select_stride(max_context_len);
+    if (near_bytes(8, 1, int32_t(stride))) return 256;
+    return align_up(size_t(num_query_tokens) * desc->num_kv_heads * stride * sizeof(uint32_t), 256);
 }
 
 extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t* bounds,
@@ -482,7 +637,7 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
         num_sink < 0 || num_recent < 1 || int64_t(num_sink) + num_recent > top_k)
         return PKV_ERR_INVALID;
     if (!query_start_loc && num_query_tokens != num_seqs) return PKV_ERR_INVALID;
-    if (num_query_tokens > 65535 || desc->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (int64_t(num_query_tokens) * desc->num_kv_heads * 8 > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     if (!selected || !q || !bounds || !exps || !block_tables || !context_lens ||
         !aligned_to(selected, 4) || !aligned_to(q, 16) || !aligned_to(bounds, 16) ||
@@ -501,7 +656,7 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
     p.exps = exps;
     p.rows = QueryRows{block_tables, query_start_loc, context_lens, max_blocks_per_seq, num_seqs,
                        max_context_len};
-    p.scores = static_cast<float*>(workspace);
+    p.far_keys = nullptr;
     p.stride = int32_t(select_stride(max_context_len));
     p.num_blocks = desc->num_blocks;
     p.num_q_heads = desc->num_q_heads;
@@ -509,20 +664,9 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
     p.top_k = top_k;
     p.sink = num_sink;
     p.recent = num_recent;
+    p.q_f32 = desc->dtype == PKV_F32;
+    uint32_t* far_keys = static_cast<uint32_t*>(workspace);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const int max_blocks = ceil_div(max_context_len, kBlockTokens);
-    if (max_blocks > top_k) {
-        const dim3 grid(unsigned(ceil_div(max_blocks, kScoreWarps * kWarpBlocks)),
-                        unsigned(desc->num_kv_heads), unsigned(num_query_tokens));
-        if (desc->dtype == PKV_BF16)
-            st = desc->head_dim == 128 ? launch_scores_g<__nv_bfloat16, 128>(p, grid, cs)
-                                       : launch_scores_g<__nv_bfloat16, 64>(p, grid, cs);
-        else
-            st = desc->head_dim == 128 ? launch_scores_g<float, 128>(p, grid, cs)
-                                       : launch_scores_g<float, 64>(p, grid, cs);
-        if (st != PKV_OK) return st;
-    }
-    return cuda_status(launch_pdl(pick_blocks_kernel,
-                                  dim3(unsigned(num_query_tokens) * unsigned(desc->num_kv_heads)),
-                                  dim3(kPickThreads), 0, cs, p));
+    return desc->head_dim == 128 ? launch_select<128>(p, num_query_tokens, far_keys, cs)
+                                 : launch_select<64>(p, num_query_tokens, far_keys, cs);
 }

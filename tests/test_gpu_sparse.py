@@ -168,15 +168,44 @@ def test_selection_of_several_rows_a_sequence(pkv, dtype, hq, hkv):
     assert np.array_equal(got, ref)
 
 
-def test_selection_of_long_contexts(pkv):
-    """More blocks than any kernel handles in one pass: 20000 of them."""
-    rng = np.random.default_rng(77)
-    ctx = [20000 * 16 - 5, 4097 * 16]
-    t, nb, bounds, exps, q, start = _select_case(rng, "bf16", 8, 1, 64, ctx, [1, 1])
-    got = _run_select(pkv, "bf16", q, bounds, exps, t, ctx, start, 300, 1, 2)
+@pytest.mark.parametrize("blocks,qlen,hq,top_k", [(20000, 1, 8, 300), (70000, 1, 2, 40),
+                                                  (9000, 3, 1, 64), (60000, 2, 1, 1000)])
+def test_selection_of_long_contexts(pkv, blocks, qlen, hq, top_k):
+    """Keys of tens of thousands of blocks, on chip and (past 49152 of them, or of
+    several rows together) through the workspace."""
+    rng = np.random.default_rng(blocks)
+    ctx = [blocks * 16 - 5, 4097 * 16]
+    t, nb, bounds, exps, q, start = _select_case(rng, "bf16", hq, 1, 64, ctx, [qlen, qlen])
+    got = _run_select(pkv, "bf16", q, bounds, exps, t, ctx, start, top_k, 1, 2,
+                      layout=qlen > 1)
     assert pkv.device_error() == 0
-    ref = sparse.select(q, bounds, exps, t, start, ctx, 16, 300, 1, 2, "bf16")
+    ref = sparse.select(q, bounds, exps, t, start, ctx, 16, top_k, 1, 2, "bf16")
     assert np.array_equal(got, ref)
+
+
+@pytest.mark.parametrize("kind", ["equal", "near", "spread"])
+def test_selection_from_keys_in_few_bins(pkv, kind):
+    """Scores that fall into one bin of the key histogram: all equal, a few units
+    apart beside an outlier, or spread over the whole range of exponents."""
+    rng = np.random.default_rng(3)
+    n, d = 3000, 64
+    bounds = np.zeros((n, 1, 2, d), np.int8)
+    exps = np.zeros((n, 1), np.int8)
+    bounds[:, 0, 0, 0] = 64
+    if kind == "near":
+        bounds[:, 0, 0, 0] = rng.integers(60, 64, n)
+        exps[[17, 2000]] = 50
+    elif kind == "spread":
+        bounds[:, 0, :, 0] = rng.integers(-127, 128, (n, 1))
+        exps[:, 0] = rng.integers(-50, 51, n)
+    q = np.zeros((1, 1, d), np.float32)
+    q[0, 0, 0] = 1.0
+    t = rng.permutation(n).astype(np.int32)[None, :]
+    for top_k in (3, 700, 2999):
+        got = _run_select(pkv, "f32", q, bounds, exps, t, [n * 16], [0, 1], top_k, 1, 1)
+        assert pkv.device_error() == 0
+        ref = sparse.select(q, bounds, exps, t, [0, 1], [n * 16], 16, top_k, 1, 1, "f32")
+        assert np.array_equal(got, ref)
 
 
 def test_selection_with_values_that_are_not_finite(pkv):
