@@ -36,18 +36,6 @@ struct SparseParams {
     int* err;
 };
 
-// 16 bytes to shared memory, or 16 bytes of zeros without reading (`live` false)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <typename T, int D, int G>
 struct SparseCfg {
     static constexpr int kWarps = 4;

@@ -10,6 +10,7 @@
 // of D of them stays below 128 * 127 * 127 < 2^24, and the units only move the
 // exponent: every score is exact in single precision.  The choice is thus a
 // function of the inputs alone, whatever order the sums are taken in.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -182,20 +183,18 @@ struct SelectParams {
     const int8_t* bounds;
     const int8_t* exps;
     QueryRows rows;
-    uint32_t* far_keys;         // [tokens][Hkv][stride] where a row's keys do not fit on chip
+    uint32_t* keys;             // [tokens][Hkv][stride]: scores in an order unsigned compare keeps
     int32_t stride;             // blocks of max_context_len, a multiple of 4
-    int32_t num_blocks, num_q_heads, num_kv_heads;
+    int32_t tokens, num_blocks, num_q_heads, num_kv_heads;
     int32_t top_k, sink, recent;
     int32_t q_f32;              // q is fp32, else bf16
+    int32_t chunk_tiles, chunks;   // tiles that one warp scores, and such chunks of a row
     int* err;
 };
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kWarpBlocks = 16;      // blocks that a warp scores at a time
-constexpr int kBins = 1024;
-constexpr int kMaxCand = kSelThreads;
-constexpr int kKeyBytes = 192 << 10; // most shared memory for a CTA's keys
+constexpr int kScoreWarps = 4;
+constexpr int kTileBlocks = 16;      // blocks of a product tile
+constexpr int kScoreStages = 3;      // tiles in flight per warp
 
 // Floats in an order that unsigned compare keeps (no NaN among the scores).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -203,80 +202,389 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Four 8-bit codes as two pairs of halves, bytes 0 and 2 and bytes 1 and 3, each
+// raised by kBias: a code with its sign bit flipped, below the byte 0x64, is the
+// half 1024 + 128 + code.
+constexpr float kBias = 1152.f;
+__device__ __forceinline__ void raise_codes(uint32_t w, uint32_t& even, uint32_t& odd) {
+    even = (w & 0x00ff00ffu) ^ 0x64806480u;
+    odd = (w >> 8 & 0x00ff00ffu) ^ 0x64806480u;
+}
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// d = c + a . b, the sums of two columns starting from c0 and c1
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], float c0, float c1, float c2, float c3,
+                                             const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+          "f"(c3));
+}
+
+// Sixteen consecutive values of a query head.
+__device__ __forceinline__ void load16(const SelectParams& p, size_t at, float (&x)[16]) {
+    if (p.q_f32) {
+        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = __ldg(s + i);
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
+    } else {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = __ldg(s + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+                x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+        }
+    }
+}
+
+// Keys of the blocks of up to R neighbouring query rows of one sequence for one
+// KV head.  The rows' R * G <= 8 query heads are the columns of a product whose
+// rows are blocks: scores = bounds (16 blocks x 2 D) . codes (2 D x 8), on
+// m16n8k16 half-precision products with single-precision sums, in which whole
+// numbers below 2^24 stay exact.  (The packed 8-bit dot product and the 8-bit
+// tensor products run at a quarter of that rate on this GPU: 491 against 1915
+// multiply-adds per ns and SM.)  The bounds enter raised by 1152, which three
+// instructions on four packed codes do, and each 64-byte chunk's sum starts from
+// -1152 times the chunk's codes: all sums of a chunk stay below
+// 64 * 127 * 1279 < 2^24.
+//
+// Every warp works alone on a chunk of a row's tiles: it makes the codes in the
+// registers that the product takes them from, and every lane copies the bounds
+// that it will use itself (two rows' 16 bytes of each 64) into places of its own
+// in shared memory, a few tiles ahead.  Nothing waits for another lane or warp,
+// and the SM's other warps hide the start of each (context, ids, bounds: three
+// dependent loads).
+template <int D, int G, int R>
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(SelectParams p) {
+    __shared__ __align__(128) uint4 ring_all[kScoreWarps][kScoreStages][2 * D / 32][32];
+    constexpr int CH = 2 * D / 64;               // 64-byte chunks: four product steps each
+    constexpr int NP = D / 64;                   // ... of which the first half meet positive parts
+    constexpr int LR = G > 2 ? G / 2 : 1;        // lanes of a quad that hold a row's columns
+    constexpr int NR = G == 1 ? 2 : 1;           // rows of a lane's two columns
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gid = lane >> 2, tig = lane & 3;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    // neighbouring warps take neighbouring heads: their bounds lie side by side
+    const uint32_t unit = blockIdx.x * kScoreWarps + warp;
+    const int chunk = int(unit / uint32_t(p.num_kv_heads));
+    const int h = int(unit % uint32_t(p.num_kv_heads));
+    const int t = int(blockIdx.z * gridDim.y + blockIdx.y);
+    if (t >= p.tokens || chunk >= p.chunks) return;
+    int first, q;
+    const int seq = token_seq(p.rows.start, p.rows.n, t, first, q, nullptr);
+    const int rows = seq < 0 || (t - first) % R ? 0 : min(R, first + q - t);
+    if (rows == 0) return;                       // another warp's row, or behind the last one
+    // asked for at once, before the context is known: the first tile's ids and
+    // the values of this lane's query head (column gid)
+    const int32_t* table = p.rows.block_tables + size_t(seq) * p.rows.table_stride;
+    const int base = chunk * p.chunk_tiles * kTileBlocks;
+    const int last = p.rows.table_stride - 1;
+    int id0 = table[min(base + gid, last)], id1 = table[min(base + gid + 8, last)];
+    float x[NP][16];
+    const bool column = gid < rows * G;
+    if (column) {
+        const size_t head = size_t(t + gid / G) * p.num_q_heads + size_t(h) * G + gid % G;
+#pragma unroll
+        for (int c = 0; c < NP; ++c) load16(p, head * D + c * 64 + tig * 16, x[c]);
+    }
+    if (!sequence_keys(p.rows, seq, q, nullptr)) return;
+    const int keys_end = p.rows.ctx[seq] - q + (t - first) + rows;
+    const int blocks = (keys_end + kBlockTokens - 1) / kBlockTokens;
+    // (a row whose blocks are all taken needs no scores)
+    if (blocks <= p.top_k || base >= blocks) return;
+    const int end = min(blocks, base + p.chunk_tiles * kTileBlocks);
+
+    // this lane's two rows of a tile are blocks gid and gid + 8
+    constexpr int kBadId = 1000;                 // exponent of an id outside the pool
+    uint4* ring = &ring_all[warp][0][0][lane];
+    const uint32_t ring_u = smem_u32(ring);
+    int e0[kScoreStages], e1[kScoreStages];
+    auto request = [&](int b, int js) {          // the tile at block b, into stage js
+        if (b < end) {
+            const bool good0 = id0 >= 0 && id0 < p.num_blocks, good1 = id1 >= 0 && id1 < p.num_blocks;
+            const size_t tile0 = size_t(good0 ? id0 : 0) * p.num_kv_heads + h;
+            const size_t tile1 = size_t(good1 ? id1 : 0) * p.num_kv_heads + h;
+            const int8_t* src0 = p.bounds + tile0 * (2 * D) + tig * 16;
+            const int8_t* src1 = p.bounds + tile1 * (2 * D) + tig * 16;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                cp_async16(ring_u + (js * 2 * CH + 2 * c) * 512, src0 + 64 * c, true);
+                cp_async16(ring_u + (js * 2 * CH + 2 * c + 1) * 512, src1 + 64 * c, true);
+            }
+            e0[js] = p.exps[tile0];
+            e1[js] = p.exps[tile1];
+            if (!good0 || !good1) {
+                if ((!good0 && b + gid < end) || (!good1 && b + gid + 8 < end))
+                    if (h == 0) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
+                if (!good0) e0[js] = kBadId;
+                if (!good1) e1[js] = kBadId;
+            }
+            // (entries behind the row's blocks may hold anything: clamped, then not used)
+            id0 = table[min(b + kTileBlocks + gid, end - 1)];
+            id1 = table[min(b + kTileBlocks + gid + 8, end - 1)];
+        }
+        cp_commit();
+    };
+    if (base + gid >= end) id0 = 0;
+    if (base + gid + 8 >= end) id1 = 0;
+#pragma unroll
+    for (int js = 0; js < kScoreStages - 1; ++js) request(base + js * kTileBlocks, js);
+
+    // codes of column gid as the product's second operand, in the order in which
+    // the bounds are read: of each 64-byte chunk this lane's 16 dimensions
+    uint32_t bq[CH][4][2];
+    float unit_q, start[CH][2];
+    {
+        float amax = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (!column) x[c][i] = 0.f;
+                odd |= !(fabsf(x[c][i]) <= FLT_MAX);
+                amax = fmaxf(amax, fabsf(x[c][i]));
+            }
+        odd = __ballot_sync(kFull, odd) >> (lane & 28) & 15u;
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+        const int eq = code_exponent(amax);
+        // (a query with values that are not finite has codes of 0)
+        const float u = odd ? 0.f : pow2(-eq);
+        unit_q = odd ? 0.f : pow2(eq);
+#pragma unroll
+        for (int c = 0; c < NP; ++c) {
+            float up = 0.f, down = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float a = odd ? 0.f : fminf(fmaxf(rintf(x[c][i] * u), -127.f), 127.f);
+                up += fmaxf(a, 0.f);
+                down += fminf(a, 0.f);
+                x[c][i] = a;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {    // bytes 0 and 2, then 1 and 3
+                    const float a = x[c][4 * i + k], b = x[c][4 * i + k + 2];
+                    bq[c][i][k] = half_pair(fmaxf(a, 0.f), fmaxf(b, 0.f));
+                    bq[NP + c][i][k] = half_pair(fminf(a, 0.f), fminf(b, 0.f));
+                }
+            up += __shfl_xor_sync(kFull, up, 1);
+            up += __shfl_xor_sync(kFull, up, 2);
+            down += __shfl_xor_sync(kFull, down, 1);
+            down += __shfl_xor_sync(kFull, down, 2);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                start[c][k] = -kBias * __shfl_sync(kFull, up, 8 * tig + 4 * k);
+                start[NP + c][k] = -kBias * __shfl_sync(kFull, down, 8 * tig + 4 * k);
+            }
+        }
+    }
+    const float u0 = __shfl_sync(kFull, unit_q, 8 * tig), u1 = __shfl_sync(kFull, unit_q, 8 * tig + 4);
+    uint32_t* out[NR];
+    bool mine[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int r = (2 * tig + n) / G;
+        mine[n] = r < rows;
+        out[n] = p.keys + (size_t(t + (mine[n] ? r : 0)) * p.num_kv_heads + h) * p.stride;
+    }
+    for (int tile = base; tile < end; tile += kScoreStages * kTileBlocks) {
+#pragma unroll
+        for (int js = 0; js < kScoreStages; ++js) {
+            const int b0 = tile + js * kTileBlocks;
+            if (b0 >= end) break;
+            request(b0 + (kScoreStages - 1) * kTileBlocks, (js + kScoreStages - 1) % kScoreStages);
+            cp_wait<kScoreStages - 1>();
+            float d[CH][4];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint4 v = ring[(js * 2 * CH + 2 * c) * 32], w = ring[(js * 2 * CH + 2 * c + 1) * 32];
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t a[4];
+                    raise_codes(vw[k], a[0], a[2]);
+                    raise_codes(ww[k], a[1], a[3]);
+                    if (k == 0)
+                        mma16816_f16(d[c], start[c][0], start[c][1], start[c][0], start[c][1], a,
+                                     bq[c][k][0], bq[c][k][1]);
+                    else
+                        mma16816_f16(d[c], d[c][0], d[c][1], d[c][2], d[c][3], a, bq[c][k][0],
+                                     bq[c][k][1]);
+                }
+            }
+            // this lane: blocks gid and gid + 8, columns 2 tig and 2 tig + 1
+            float s[2][NR];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float x0 = d[0][2 * half], x1 = d[0][2 * half + 1];
+#pragma unroll
+                for (int c = 1; c < CH; ++c) x0 += d[c][2 * half], x1 += d[c][2 * half + 1];
+                s[half][0] = x0 * u0;
+                if (NR == 2) s[half][NR - 1] = x1 * u1;
+                else s[half][0] = fmaxf(s[half][0], x1 * u1);
+                if (G > 4) s[half][0] = fmaxf(s[half][0], __shfl_xor_sync(kFull, s[half][0], 2));
+            }
+            int e = e0[js], f = e1[js], b = b0 + gid;
+            bool writes0 = true, writes1 = LR == 1;
+            if (LR > 1) {                        // a block each for lanes that share a row's columns
+                const bool up = tig & 1;
+                const float mine_s = up ? s[1][0] : s[0][0], other = up ? s[0][0] : s[1][0];
+                s[0][0] = fmaxf(mine_s, __shfl_xor_sync(kFull, other, 1));
+                if (up) e = f, b += 8;
+                writes0 = tig % LR < 2;
+            }
+            auto put = [&](int at, int ex, const float (&sc)[NR]) {
+                const float eu = pow2(ex > 50 ? 0 : ex);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    float x = sc[n] * eu;
+                    if (ex > 50) x = ex == kBadId ? -INFINITY : ex == kUnbounded ? INFINITY : x;
+                    if (mine[n]) out[n][at] = ordered(x);
+                }
+            };
+            if (writes0 && b < end) put(b, e, s[0]);
+            if (writes1 && b + 8 < end) put(b + 8, f, s[1]);
+        }
+    }
+    cp_wait<0>();
+}
+
+// ---- the lists ------------------------------------------------------------------
+
+template <int NT>
 struct PickScratch {
+    static constexpr int kWarps = NT / 32;
+    static constexpr int kBins = 4 * NT;
     uint32_t hist[kBins];
-    uint32_t cand[kMaxCand];
-    uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
+    uint32_t cand[NT];
+    uint32_t warp_a[kWarps], warp_b[kWarps];
     uint32_t bin, above, inside, count, cut, take;
 };
 
-// Exclusive sums over the CTA of two values per thread.
-__device__ __forceinline__ void scan_two(uint32_t& a, uint32_t& b, PickScratch& s) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t a0 = a, b0 = b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t ua = __shfl_up_sync(kFull, a, o), ub = __shfl_up_sync(kFull, b, o);
-        if (lane >= o) a += ua, b += ub;
-    }
-    if (lane == 31) s.warp_a[warp] = a, s.warp_b[warp] = b;
+// Sums of two values over the warps in front of this one (each value is the
+// same for a warp's lanes).
+template <int NT>
+__device__ __forceinline__ void warps_before(uint32_t& a, uint32_t& b, PickScratch<NT>& s) {
+    const int warp = threadIdx.x >> 5;
+    s.warp_a[warp] = a;
+    s.warp_b[warp] = b;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) a += s.warp_a[w], b += s.warp_b[w];
-    a -= a0;
-    b -= b0;
+    a = b = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32 - 1; ++w) {
+        a += w < warp ? s.warp_a[w] : 0u;
+        b += w < warp ? s.warp_b[w] : 0u;
+    }
 }
 
-// The list of one row from the keys of its blocks, by the whole CTA.  Wanted
-// are the `want` largest keys of blocks sink .. blocks - recent - 1 (the ends are
-// always taken).  A histogram over the keys' range finds the bin that holds the
-// want-th; its few keys are ranked against one another, or, while they are more
-// than a CTA ranks at once, the bin becomes the next range.  Scores of a real
-// query spread over the bins, so one histogram and one ranking is the rule.
-__device__ __forceinline__ void pick_row(const SelectParams& p, const uint32_t* keys, int blocks,
-                                         int32_t* out, PickScratch& s) {
+// One CTA of NT threads for the list of a (query row, KV head).  Wanted are the
+// `want` largest keys of blocks sink .. blocks - recent - 1 (the ends are always
+// taken).  A histogram over the keys' range finds the bin that holds the want-th;
+// its few keys are ranked against one another, or, while they are more than the
+// CTA ranks at once, the bin becomes the next range.  Scores of a real query
+// spread over the bins, so one histogram and one ranking is the rule.  A row's
+// keys stay in registers, kHeld to a thread, asked for before the row's context
+// is known; with kHeld 0 (rows longer than that) every pass reads them again.
+template <int NT, int kHeld>
+__global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
+    using S = PickScratch<NT>;
+    constexpr bool Held = kHeld > 0;
+    __shared__ __align__(16) S s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.hist[i * NT + tid] = 0;
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    const int h = int(blockIdx.x % uint32_t(p.num_kv_heads));
+    const int t = int(blockIdx.x / uint32_t(p.num_kv_heads));
+    const uint32_t* far = p.keys + size_t(blockIdx.x) * p.stride;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    const int mine = Held ? warp * 32 * kHeld + lane : 0;
+    uint32_t held[Held ? kHeld : 1];
+    if (Held) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            held[i] = mine + 32 * i < p.stride ? far[mine + 32 * i] : 0u;
+    }
+    int seq;
+    const int row_sees = row_keys(p.rows, t, seq, tid == 0 && h == 0 ? p.err : nullptr);
+    if (row_sees < 0) return;                    // behind the last sequence: left as it is
+    const int blocks = (row_sees + kBlockTokens - 1) / kBlockTokens;
+    int32_t* out = p.selected + size_t(blockIdx.x) * p.top_k;
+    if (blocks <= p.top_k) {
+        for (int i = tid; i < p.top_k; i += NT) out[i] = i < blocks ? i : -1;
+        return;
+    }
     const int b0 = p.sink, b1 = blocks - p.recent;
+    // f(key) for each of this thread's keys of blocks b0 .. b1 - 1
+    auto each = [&](auto f) {
+        if (Held) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                if (mine + 32 * i >= b0 && mine + 32 * i < b1) f(held[i]);
+        } else {
+            for (int b = b0 + tid; b < b1; b += NT) f(far[b]);
+        }
+    };
     uint32_t want = uint32_t(p.top_k - p.sink - p.recent);
     uint32_t cut = 0xffffffffu, take = 0;        // taken: keys above `cut`, `take` equal to it
     if (want > 0) {
         uint32_t lo = 0xffffffffu, hi = 0;
-        for (int b = b0 + tid; b < b1; b += kSelThreads) {
-            lo = min(lo, keys[b]);
-            hi = max(hi, keys[b]);
-        }
+        each([&](uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
         lo = __reduce_min_sync(kFull, lo);
         hi = __reduce_max_sync(kFull, hi);
         if (lane == 0) s.warp_a[warp] = lo, s.warp_b[warp] = hi;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) {
-            lo = min(lo, s.warp_a[w]);
-            hi = max(hi, s.warp_b[w]);
-        }
+        lo = __reduce_min_sync(kFull, s.warp_a[lane % S::kWarps]);
+        hi = __reduce_max_sync(kFull, s.warp_b[lane % S::kWarps]);
         for (;;) {                               // the range lo .. hi holds the want-th
-            int shift = 0;
-            while ((hi - lo) >> shift >= kBins) ++shift;
-            for (int i = tid; i < kBins; i += kSelThreads) s.hist[i] = 0;
-            if (tid == 0) s.count = 0;
-            __syncthreads();
-            for (int b = b0 + tid; b < b1; b += kSelThreads) {
-                const uint32_t k = keys[b];
+            const int shift = max(0, 32 - __clz(hi - lo) - (31 - __clz(S::kBins)));
+            each([&](uint32_t k) {
                 if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
-            }
+            });
             __syncthreads();
             // bins from above, four to a thread
-            const uint4 c = *reinterpret_cast<const uint4*>(&s.hist[kBins - 4 - 4 * tid]);
+            const uint4 c = *reinterpret_cast<const uint4*>(&s.hist[S::kBins - 4 - 4 * tid]);
             const uint32_t four[4] = {c.w, c.z, c.y, c.x};
-            uint32_t sum = c.x + c.y + c.z + c.w, none = 0;
-            scan_two(sum, none, s);
+            const uint32_t own = c.x + c.y + c.z + c.w;
+            uint32_t sum = own;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (sum < want && want <= sum + four[i]) {
-                    s.bin = uint32_t(kBins - 1 - 4 * tid - i);
-                    s.above = sum;
-                    s.inside = four[i];
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(kFull, sum, o);
+                if (lane >= o) sum += u;
+            }
+            uint32_t before = __shfl_sync(kFull, sum, 31), none = 0;
+            warps_before<NT>(before, none, s);
+            sum += before - own;
+            if (sum < want && want <= sum + own) {   // exactly one thread
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (sum < want && want <= sum + four[i]) {
+                        s.bin = uint32_t(S::kBins - 1 - 4 * tid - i);
+                        s.above = sum;
+                        s.inside = four[i];
+                    }
+                    sum += four[i];
                 }
-                sum += four[i];
             }
             __syncthreads();
             const uint32_t inside = s.inside;
@@ -292,18 +600,17 @@ __device__ __forceinline__ void pick_row(const SelectParams& p, const uint32_t* 
                 take = want;
                 break;
             }
-            if (inside <= kMaxCand) {
-                for (int b = b0 + tid; b < b1; b += kSelThreads) {
-                    const uint32_t k = keys[b];
+            if (inside <= uint32_t(NT)) {
+                each([&](uint32_t k) {
                     if (k >= first && k <= last) s.cand[atomicAdd(&s.count, 1u)] = k;
-                }
+                });
                 __syncthreads();
                 if (tid < int(inside)) {
                     const uint32_t k = s.cand[tid];
                     uint32_t gt = 0, ge = 0;
-                    for (uint32_t i = 0; i < inside; ++i) {
-                        gt += s.cand[i] > k;
-                        ge += s.cand[i] >= k;
+                    for (uint32_t j = 0; j < inside; ++j) {
+                        gt += s.cand[j] > k;
+                        ge += s.cand[j] >= k;
                     }
                     if (gt < want && want <= ge) {   // the same for all keys equal to the cut
                         s.cut = k;
@@ -318,245 +625,94 @@ __device__ __forceinline__ void pick_row(const SelectParams& p, const uint32_t* 
             lo = first;
             hi = last;
             __syncthreads();                     // (the bin was read by all)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.hist[i * NT + tid] = 0;
+            __syncthreads();
         }
     }
-    // in ascending order: neighbouring blocks to a thread, so that one scan of
-    // the counts places them
-    const int per = (blocks + kSelThreads - 1) / kSelThreads;
-    const int f = min(blocks, tid * per), e = min(blocks, f + per);
-    uint32_t above = 0, equal = 0;
-    for (int b = f; b < e; ++b) {
-        const bool end = b < b0 || b >= b1;
-        above += end || keys[b] > cut;
-        equal += !end && keys[b] == cut;
-    }
-    __syncthreads();
-    scan_two(above, equal, s);
-    for (int b = f; b < e; ++b) {
-        const bool end = b < b0 || b >= b1;
-        if (end || keys[b] > cut) {
-            out[above + min(equal, take)] = b;
-            ++above;
-        } else if (keys[b] == cut) {
-            if (equal < take) out[above + equal] = b;
-            ++equal;
-        }
-    }
-    __syncthreads();
-}
-
-// Codes of one query head (one warp): positive parts, then negative parts.
-template <int D>
-__device__ __forceinline__ void query_codes(const SelectParams& p, size_t head, uint32_t* dst,
-                                            float* unit) {
-    constexpr int PL = D / 32;                   // dimensions of a lane: consecutive
-    const int lane = threadIdx.x & 31;
-    float x[PL];
-    if (p.q_f32) {
-        Elem<float>::load(static_cast<const float*>(p.q) + head * D + lane * PL, x);
-    } else {
-        Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(p.q) + head * D + lane * PL, x);
-    }
-    float amax = 0.f;
-    bool odd = false;
+    // in ascending order: a stretch of blocks to a warp, whose counts are summed
+    // first; within a warp 32 blocks at a time by ballot
+    const int stretch = Held ? 32 * kHeld : ((blocks + S::kWarps - 1) / S::kWarps + 31) & ~31;
+    const int f = min(blocks, warp * stretch), e = min(blocks, f + stretch);
+    auto walk = [&](auto use) {                  // use(block, above the cut, equal to it)
+        auto one = [&](int b, uint32_t k) {
+            const bool in = b < e, end = b < b0 || b >= b1;
+            use(b, in && (end || k > cut), in && !end && k == cut);
+        };
+        if (Held) {
 #pragma unroll
-    for (int j = 0; j < PL; ++j) {
-        odd |= !(fabsf(x[j]) <= FLT_MAX);
-        amax = fmaxf(amax, fabsf(x[j]));
-    }
-    // (the bits of values that are not negative order as the values do)
-    amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
-    odd = __any_sync(kFull, odd);
-    const int eq = code_exponent(amax);
-    const float u = pow2(-eq);
-    int8_t* pos = reinterpret_cast<int8_t*>(dst) + lane * PL;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) {
-        // (a query with values that are not finite has codes of 0)
-        const int c = odd ? 0 : int(fminf(fmaxf(rintf(x[j] * u), -127.f), 127.f));
-        pos[j] = int8_t(max(c, 0));
-        pos[D + j] = int8_t(min(c, 0));
-    }
-    if (lane == 0) *unit = odd ? 0.f : pow2(eq);
-}
-
-// A cluster chooses the blocks of R neighbouring query rows of one sequence for
-// one KV head, R * G query heads being its columns.  Its CTAs share the
-// sequence's blocks; a quad of lanes takes two blocks at a time, each lane 64 of
-// their 2 D bytes straight from the pool, and the sums run on the packed 8-bit
-// dot product with the columns' codes from shared memory.  A score's key goes to
-// the CTA that picks the row (through distributed shared memory, or to global
-// memory where the keys of a very long context do not fit), so the scores never
-// pass through HBM and one launch does it all.
-template <int D, int G, int R>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(SelectParams p) {
-    constexpr int CH = 2 * D / 64;               // 64-byte chunks of a bounds row
-    constexpr int COLS = G * R;
-    extern __shared__ __align__(16) uint32_t near_keys[];   // [rows picked here][stride]
-    __shared__ __align__(16) uint32_t qc[COLS][2 * D / 4];
-    __shared__ float unit[COLS];
-    __shared__ __align__(16) PickScratch scratch;
-    const uint32_t cs = cluster_size(), rank = cluster_rank();
-    const int item = int(blockIdx.x / cs);
-    const int h = item % p.num_kv_heads, t = item / p.num_kv_heads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (cs > 1) cluster_arrive();                // the others' shared memory is there to write to
-    pdl_wait_prerequisites();
-    pdl_launch_dependents();
-    int first, q;
-    int* tell = tid == 0 && h == 0 && rank == 0 ? p.err : nullptr;
-    const int seq = token_seq(p.rows.start, p.rows.n, t, first, q, tell);
-    const int rows = seq < 0 || (t - first) % R ? 0 : min(R, first + q - t);
-    if (rows == 0) {                             // another cluster's row, or behind the last one
-        if (cs > 1) cluster_wait();
-        return;
-    }
-    const int keys0 = sequence_keys(p.rows, seq, q, tell) ? p.rows.ctx[seq] - q + (t - first) + 1 : 0;
-    const int blocks_end = keys0 > 0 ? (keys0 + rows - 1 + kBlockTokens - 1) / kBlockTokens : 0;
-    const bool scored = blocks_end > p.top_k;    // otherwise every row takes all its blocks
-    for (int c = warp; scored && c < rows * G; c += kSelWarps)
-        query_codes<D>(p, size_t(t + c / G) * p.num_q_heads + size_t(h) * G + c % G, qc[c], &unit[c]);
-    __syncthreads();
-    if (cs > 1) cluster_wait();
-    const uint32_t near0 = smem_u32(near_keys);
-    if (scored) {
-        const int32_t* table = p.rows.block_tables + size_t(seq) * p.rows.table_stride;
-        const int quad = lane >> 2, tig = lane & 3;
-        const int step = int(cs) * kSelWarps * kWarpBlocks;
-        // this lane's block of the 16 (the upper half of the warp repeats the lower)
-        auto block_id = [&](int b) { return b < blocks_end ? table[b] : 0; };
-        int b0 = (int(rank) * kSelWarps + warp) * kWarpBlocks;
-        int ahead = block_id(b0 + (lane & 15));
-        for (; b0 < blocks_end; b0 += step) {
-            const int id = ahead;
-            ahead = block_id(b0 + step + (lane & 15));
-            const bool good = id >= 0 && id < p.num_blocks;
-            if (!good && h == 0 && lane < 16) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
-            const size_t tile = good ? size_t(id) * p.num_kv_heads + h : 0;
-            const int e = p.exps[tile];
-            uint4 w[2][CH];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const size_t tk = __shfl_sync(kFull, (unsigned long long)tile, quad * 2 + k);
-                const uint4* src = reinterpret_cast<const uint4*>(p.bounds + tk * (2 * D)) + tig;
-#pragma unroll
-                for (int c = 0; c < CH; ++c) w[k][c] = __ldg(src + 4 * c);
-            }
-            // after the quad's sums: lane tig holds block 2 quad + (tig >> 1)
-            const int mine = quad * 2 + (tig >> 1);
-            const float eu = pow2(__shfl_sync(kFull, e == kUnbounded ? 0 : e, mine));
-            const int em = __shfl_sync(kFull, e, mine);
-            const bool gm = __shfl_sync(kFull, int(good), mine);
-            const int bm = b0 + mine;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (r >= rows) break;
-                float best = -INFINITY;
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    int s0 = 0, s1 = 0;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(&qc[r * G + g][c * 16 + tig * 4]);
-                        s0 = __dp4a(int(w[0][c].x), int(v.x), s0);
-                        s0 = __dp4a(int(w[0][c].y), int(v.y), s0);
-                        s0 = __dp4a(int(w[0][c].z), int(v.z), s0);
-                        s0 = __dp4a(int(w[0][c].w), int(v.w), s0);
-                        s1 = __dp4a(int(w[1][c].x), int(v.x), s1);
-                        s1 = __dp4a(int(w[1][c].y), int(v.y), s1);
-                        s1 = __dp4a(int(w[1][c].z), int(v.z), s1);
-                        s1 = __dp4a(int(w[1][c].w), int(v.w), s1);
-                    }
-                    const bool up = tig & 2;
-                    int sum = up ? s1 : s0;
-                    sum += __shfl_xor_sync(kFull, up ? s0 : s1, 2);
-                    sum += __shfl_xor_sync(kFull, sum, 1);
-                    best = fmaxf(best, float(sum) * unit[r * G + g]);
-                }
-                const float score = !gm ? -INFINITY : em == kUnbounded ? INFINITY : best * eu;
-                if ((tig & 1) == 0 && bm < blocks_end) {
-                    if (p.far_keys)
-                        p.far_keys[(size_t(t + r) * p.num_kv_heads + h) * p.stride + bm] = ordered(score);
-                    else
-                        st_cluster(map_rank(near0 + (uint32_t(r) / cs * p.stride + bm) * 4, r % cs),
-                                   ordered(score));
-                }
-            }
-        }
-    }
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
-    for (int r = int(rank); r < rows; r += int(cs)) {
-        const int blocks = keys0 > 0 ? (keys0 + r + kBlockTokens - 1) / kBlockTokens : 0;
-        const size_t row = size_t(t + r) * p.num_kv_heads + h;
-        int32_t* out = p.selected + row * p.top_k;
-        if (blocks <= p.top_k) {
-            for (int i = tid; i < p.top_k; i += kSelThreads) out[i] = i < blocks ? i : -1;
+            for (int i = 0; i < kHeld; ++i)
+                if (f + 32 * i < e) one(mine + 32 * i, held[i]);
         } else {
-            pick_row(p, p.far_keys ? p.far_keys + row * p.stride : near_keys + r / int(cs) * p.stride,
-                     blocks, out, scratch);
+            for (int b = f; b < e; b += 32) one(b + lane, b + lane < e ? far[b + lane] : 0u);
         }
-    }
+    };
+    uint32_t n_above = 0, n_equal = 0;
+    walk([&](int, bool above, bool equal) {
+        n_above += __popc(__ballot_sync(kFull, above));
+        n_equal += __popc(__ballot_sync(kFull, equal));
+    });
+    warps_before<NT>(n_above, n_equal, s);
+    const uint32_t below = (1u << lane) - 1u;
+    walk([&](int b, bool above, bool equal) {
+        const uint32_t ma = __ballot_sync(kFull, above), me = __ballot_sync(kFull, equal);
+        const uint32_t at = n_above + __popc(ma & below), nth = n_equal + __popc(me & below);
+        if (above || (equal && nth < take)) out[at + min(nth, take)] = b;
+        n_above += __popc(ma);
+        n_equal += __popc(me);
+    });
 }
 
 size_t select_stride(int32_t max_ctx) {
     return align_up(size_t(ceil_div(max_ctx, kBlockTokens)), 4);
 }
 
-// CTAs that share a row group: enough for two on every SM, but 128 blocks each.
-int select_cluster(int64_t items, int max_blocks) {
-    int cs = 1;
-    while (cs < 8 && items * cs < 2 * int64_t(num_sms()) && max_blocks >= 256 * cs) cs *= 2;
-    return cs;
-}
-
-// Shared memory for the keys of the rows that one CTA picks, 0 if they do not fit.
-size_t near_bytes(int rows, int cs, int32_t stride) {
-    const size_t b = size_t(ceil_div(rows, cs)) * stride * 4;
-    return b <= size_t(kKeyBytes) ? b : 0;
-}
-
 template <int D, int G, int R>
-int launch_select_r(const SelectParams& p0, int64_t tokens, uint32_t* far_keys, cudaStream_t stream) {
-    SelectParams p = p0;
-    const int64_t items = tokens * p.num_kv_heads;
-    const int cs = select_cluster(ceil_div(items, R), p.stride);
-    const size_t smem = near_bytes(R, cs, p.stride);
-    p.far_keys = smem ? nullptr : far_keys;
-    constexpr auto kern = select_blocks_kernel<D, G, R>;
-    if (kernel_occupancy<kern>(kSelThreads, kKeyBytes) < 1) return PKV_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(items * cs));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(cs);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
+int launch_scores_r(SelectParams p, cudaStream_t stream) {
+    // chunks that give every SM some tens of warps, of 2 to 16 tiles each
+    const int64_t items = ceil_div(int64_t(p.tokens), R) * int64_t(p.num_kv_heads);
+    const int tiles = ceil_div(p.stride, kTileBlocks);
+    p.chunk_tiles = 16;
+    while (p.chunk_tiles > 2 && items * ceil_div(tiles, p.chunk_tiles) < 32 * int64_t(num_sms()))
+        p.chunk_tiles /= 2;
+    p.chunks = ceil_div(tiles, p.chunk_tiles);
+    const int64_t units = int64_t(p.chunks) * p.num_kv_heads;
+    const unsigned gy = unsigned(std::min(p.tokens, 65535));
+    return cuda_status(launch_pdl(block_scores_kernel<D, G, R>,
+                                  dim3(unsigned((units + kScoreWarps - 1) / kScoreWarps), gy,
+                                       unsigned(ceil_div(p.tokens, gy))),
+                                  dim3(kScoreWarps * 32), 0, stream, p));
 }
 
 // Rows of a sequence share the reads of its bounds, up to eight columns.
 template <int D, int G>
-int launch_select_g(const SelectParams& p, int64_t tokens, uint32_t* far_keys, cudaStream_t s) {
-    return p.rows.start ? launch_select_r<D, G, 8 / G>(p, tokens, far_keys, s)
-                        : launch_select_r<D, G, 1>(p, tokens, far_keys, s);
+int launch_scores_g(const SelectParams& p, cudaStream_t s) {
+    return p.rows.start ? launch_scores_r<D, G, 8 / G>(p, s) : launch_scores_r<D, G, 1>(p, s);
 }
 
 template <int D>
-int launch_select(const SelectParams& p, int64_t tokens, uint32_t* far_keys, cudaStream_t s) {
+int launch_scores(const SelectParams& p, cudaStream_t s) {
     switch (p.num_q_heads / p.num_kv_heads) {
-        case 1: return launch_select_g<D, 1>(p, tokens, far_keys, s);
-        case 2: return launch_select_g<D, 2>(p, tokens, far_keys, s);
-        case 4: return launch_select_g<D, 4>(p, tokens, far_keys, s);
-        default: return launch_select_g<D, 8>(p, tokens, far_keys, s);
+        case 1: return launch_scores_g<D, 1>(p, s);
+        case 2: return launch_scores_g<D, 2>(p, s);
+        case 4: return launch_scores_g<D, 4>(p, s);
+        default: return launch_scores_g<D, 8>(p, s);
     }
+}
+
+template <int NT, int kHeld>
+int launch_pick_t(const SelectParams& p, cudaStream_t s) {
+    return cuda_status(launch_pdl(pick_blocks_kernel<NT, kHeld>,
+                                  dim3(unsigned(p.tokens) * unsigned(p.num_kv_heads)), dim3(NT), 0,
+                                  s, p));
+}
+
+// The least threads that hold a row's keys.  (2048 rows of up to 512 blocks, the
+// kernel alone: 7.1 us with two warps to a row, 21 us with one.)
+int launch_pick(const SelectParams& p, cudaStream_t s) {
+    if (p.stride <= 64 * 8) return launch_pick_t<64, 8>(p, s);
+    if (p.stride <= 256 * 8) return launch_pick_t<256, 8>(p, s);
+    return launch_pick_t<512, 0>(p, s);
 }
 
 bool aligned_to(const void* p, uintptr_t a) {
@@ -617,10 +773,9 @@ extern "C" int pkv_block_bounds(int8_t* bounds, int8_t* exps, const void* k_cach
 extern "C" size_t pkv_select_workspace_bytes(const pkv_cache_desc* desc, int32_t num_query_tokens,
                                              int32_t max_context_len) {
     if (check_desc(desc, true) != PKV_OK || num_query_tokens < 0 || max_context_len < 1) return 0;
-    // keys that fit on chip whatever the cluster need no workspace
-    const size_t stride = select_stride(max_context_len);
-    if (near_bytes(8, 1, int32_t(stride))) return 256;
-    return align_up(size_t(num_query_tokens) * desc->num_kv_heads * stride * sizeof(uint32_t), 256);
+    return align_up(size_t(num_query_tokens) * desc->num_kv_heads * select_stride(max_context_len) *
+                        sizeof(uint32_t),
+                    256);
 }
 
 extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t* bounds,
@@ -637,7 +792,9 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
         num_sink < 0 || num_recent < 1 || int64_t(num_sink) + num_recent > top_k)
         return PKV_ERR_INVALID;
     if (!query_start_loc && num_query_tokens != num_seqs) return PKV_ERR_INVALID;
-    if (int64_t(num_query_tokens) * desc->num_kv_heads * 8 > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (int64_t(num_query_tokens) * desc->num_kv_heads * ceil_div(max_context_len, kBlockTokens) >
+        (int64_t(1) << 36))
+        return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     if (!selected || !q || !bounds || !exps || !block_tables || !context_lens ||
         !aligned_to(selected, 4) || !aligned_to(q, 16) || !aligned_to(bounds, 16) ||
@@ -656,8 +813,9 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
     p.exps = exps;
     p.rows = QueryRows{block_tables, query_start_loc, context_lens, max_blocks_per_seq, num_seqs,
                        max_context_len};
-    p.far_keys = nullptr;
+    p.keys = static_cast<uint32_t*>(workspace);
     p.stride = int32_t(select_stride(max_context_len));
+    p.tokens = num_query_tokens;
     p.num_blocks = desc->num_blocks;
     p.num_q_heads = desc->num_q_heads;
     p.num_kv_heads = desc->num_kv_heads;
@@ -665,8 +823,11 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
     p.sink = num_sink;
     p.recent = num_recent;
     p.q_f32 = desc->dtype == PKV_F32;
-    uint32_t* far_keys = static_cast<uint32_t*>(workspace);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return desc->head_dim == 128 ? launch_select<128>(p, num_query_tokens, far_keys, cs)
-                                 : launch_select<64>(p, num_query_tokens, far_keys, cs);
+    // (a batch whose lists hold every block needs no scores)
+    if (ceil_div(max_context_len, kBlockTokens) > top_k) {
+        st = desc->head_dim == 128 ? launch_scores<128>(p, cs) : launch_scores<64>(p, cs);
+        if (st != PKV_OK) return st;
+    }
+    return launch_pick(p, cs);
 }

@@ -129,12 +129,12 @@ def test_select_and_attend_scalars(lib):
     assert _attend(lib, d, scale=float("inf")) == bad
 
 
-def test_select_workspace_is_for_contexts_that_do_not_fit_on_chip(lib):
+def test_select_workspace_grows_with_rows_and_context(lib):
     d = _desc(lib)
-    assert lib.select_workspace_bytes(d, 64, 32768) == 256
-    a = lib.select_workspace_bytes(d, 64, 1 << 20)
-    assert a >= 64 * 8 * 65536 * 4 and a % 256 == 0
-    assert lib.select_workspace_bytes(d, 65, 1 << 20) > a
+    a = lib.select_workspace_bytes(d, 64, 32768)
+    assert a >= 64 * 8 * 2048 * 4 and a % 256 == 0
+    assert lib.select_workspace_bytes(d, 64, 4096) < a
+    assert lib.select_workspace_bytes(d, 65, 32768) > a
     assert lib.select_workspace_bytes(_desc(lib, dtype=2), 64, 4096) == 0
     assert lib.select_workspace_bytes(d, -1, 4096) == 0
 
