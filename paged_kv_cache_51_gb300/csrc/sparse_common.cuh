@@ -13,9 +13,11 @@ struct QueryRows {
     int32_t table_stride, n, max_ctx;
 };
 
-// Sequence of query token t: t itself without query_start_loc, else by
-// bisection; -1 for a token behind the last sequence.  `first` is the
-// sequence's first token, `count` its number of tokens.
+// Sequence of query token t, found by a whole warp: t itself without
+// query_start_loc, else the last one that starts at or before t; -1 for a token
+// behind the last sequence.  `first` is the sequence's first token, `count` its
+// number of tokens.  A batch of single tokens is answered by one look, others by
+// one more for every factor of 32 in the number of sequences.
 __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int& first,
                                          int& count, int* err) {
     if (!start) {
@@ -23,19 +25,31 @@ __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int
         count = 1;
         return t < n ? t : -1;
     }
-    if (t >= start[n]) return -1;
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
-    }
+    const int lane = threadIdx.x & 31;
+    const int total = start[n];
+    int lo = min(t, n - 1);
     first = start[lo];
-    count = start[lo + 1] - first;
-    if (first < 0 || t < first || t >= first + count) {   // offsets that are not in order
-        flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
-        return -1;
+    int next = start[lo + 1];
+    if (t >= total) return -1;
+    if (t < first || t >= next) {
+        lo = 0;
+        for (int width = n; width > 1;) {        // the sequence is one of lo .. lo + width - 1
+            const int step = (width + 31) / 32;
+            const int at = lo + lane * step;
+            const bool before = lane == 0 || (lane * step < width && start[at] <= t);
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
+            lo += k * step;
+            width = min(step, width - k * step);
+        }
+        // (of several that start there, those before the last are empty)
+        first = start[lo];
+        next = start[lo + 1];
+        if (first < 0 || t < first || t >= next) {   // offsets that are not in order
+            flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
+            return -1;
+        }
     }
+    count = next - first;
     return lo;
 }
 

@@ -47,130 +47,194 @@ struct BoundsParams {
     const int32_t* start;       // [n + 1] or null
     const int32_t* ctx;
     int32_t table_stride, n, tokens, num_blocks, num_kv_heads;
-    int span;                   // tokens that one CTA looks at
+    int span;                   // tokens that one warp looks at
     int* err;
 };
 
-constexpr int kBoundsWarps = 8;
-constexpr int kMaxSpan = 16;
+constexpr int kBoundsWarps = 4;
 
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[V]);
+// Largest and smallest of 16 bytes of values each, element by element; NaN if
+// either is.
+template <typename T>
+struct Extent;
 template <>
-__device__ __forceinline__ void load_vec<float, 4>(const float* p, float (&x)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-template <>
-__device__ __forceinline__ void load_vec<__nv_bfloat16, 8>(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Extent<float> {
+    static constexpr int V = 4;
+    float hi[4], lo[4];
+    __device__ __forceinline__ static float max_nan(float a, float b) {
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+        return r;
     }
-}
+    __device__ __forceinline__ void start(uint4 v) {
+        hi[0] = lo[0] = __uint_as_float(v.x);
+        hi[1] = lo[1] = __uint_as_float(v.y);
+        hi[2] = lo[2] = __uint_as_float(v.z);
+        hi[3] = lo[3] = __uint_as_float(v.w);
+    }
+    __device__ __forceinline__ void add(const float (&h)[4], const float (&l)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = max_nan(hi[i], h[i]);
+            lo[i] = -max_nan(-lo[i], -l[i]);
+        }
+    }
+    __device__ __forceinline__ void add(uint4 v) {
+        const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                            __uint_as_float(v.w)};
+        add(x, x);
+    }
+    __device__ __forceinline__ void fold(int lanes) {
+        float h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = __shfl_xor_sync(kFull, hi[i], lanes);
+            l[i] = __shfl_xor_sync(kFull, lo[i], lanes);
+        }
+        add(h, l);
+    }
+    __device__ __forceinline__ float top(int i) const { return hi[i]; }
+    __device__ __forceinline__ float low(int i) const { return lo[i]; }
+};
+template <>
+struct Extent<__nv_bfloat16> {
+    static constexpr int V = 8;
+    __nv_bfloat162 hi[4], lo[4];                 // two values at a time
+    __device__ __forceinline__ static __nv_bfloat162 two(uint32_t w) {
+        return *reinterpret_cast<const __nv_bfloat162*>(&w);
+    }
+    __device__ __forceinline__ void start(uint4 v) {
+        hi[0] = lo[0] = two(v.x);
+        hi[1] = lo[1] = two(v.y);
+        hi[2] = lo[2] = two(v.z);
+        hi[3] = lo[3] = two(v.w);
+    }
+    __device__ __forceinline__ void add(uint4 v) {
+        const __nv_bfloat162 x[4] = {two(v.x), two(v.y), two(v.z), two(v.w)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = __hmax2_nan(hi[i], x[i]);
+            lo[i] = __hmin2_nan(lo[i], x[i]);
+        }
+    }
+    __device__ __forceinline__ void fold(int lanes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(kFull, hi[i], lanes));
+            lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(kFull, lo[i], lanes));
+        }
+    }
+    __device__ __forceinline__ static float part(__nv_bfloat162 v, int i) {
+        return i & 1 ? __high2float(v) : __low2float(v);
+    }
+    __device__ __forceinline__ float top(int i) const { return part(hi[i / 2], i); }
+    __device__ __forceinline__ float low(int i) const { return part(lo[i / 2], i); }
+};
 
-// A CTA looks at `span` query tokens; a token that is the first of its sequence
-// in the step, or the first row of its block, stands for that block.  Each of
-// the blocks found, times the KV heads, is one warp's tile: the warp reads the
-// rows that hold tokens, keeps the largest and the smallest value of each
-// dimension, and writes codes rounded outwards.
+// A warp looks at `span` query tokens for one KV head; a token that is the first
+// of its sequence in the step, or the first row of its block, stands for that
+// block.  For each block found the warp reads the rows that hold tokens, all of
+// them asked for at once, keeps the largest and the smallest value of each
+// dimension, and writes codes rounded outwards, half the warp the upper ends and
+// half the lower.  One pass over the keys: bound by HBM for prompts and by the
+// chain of lookups in front of the tile for a decode step.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(BoundsParams p) {
-    constexpr int V = 16 / int(sizeof(T));       // elements of a 16-byte load
+    constexpr int V = Extent<T>::V;              // elements of a 16-byte load
     constexpr int LPR = D / V;                   // lanes of a row
     constexpr int RPI = 32 / LPR;                // rows of a load
-    __shared__ int32_t blk[kMaxSpan], rows[kMaxSpan];
-    __shared__ int count;
+    const int lane = threadIdx.x & 31;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    if (threadIdx.x == 0) count = 0;
-    __syncthreads();
-    const int t = blockIdx.x * p.span + threadIdx.x;
-    if (int(threadIdx.x) < p.span && t < p.tokens) {
-        int first, q;
-        const int s = token_seq(p.start, p.n, t, first, q, p.err);
-        if (s >= 0) {
+    const uint32_t unit = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
+    const int h = int(unit % uint32_t(p.num_kv_heads));
+    const int64_t t0 = int64_t(unit / uint32_t(p.num_kv_heads)) * p.span;
+    if (t0 >= p.tokens) return;
+    int* const tell = h == 0 ? p.err : nullptr;
+    int first, q, id = -1, nrow = 0;
+    int s = token_seq(p.start, p.n, int(t0), first, q, lane == 0 ? tell : nullptr);
+    const int64_t t = t0 + lane;
+    if (lane < p.span && t < p.tokens && s >= 0) {
+        // the lane's own token: a later sequence than the first token's, perhaps
+        while (t >= int64_t(first) + q && s + 1 < p.n) {
+            ++s;
+            first = p.start[s];
+            q = p.start[s + 1] - first;
+        }
+        if (t >= first && t < int64_t(first) + q) {
             const int ctx = p.ctx[s];
-            const int pos = ctx - q + (t - first);
+            const int pos = ctx - q + int(t - first);
             if (ctx < q) {
-                if (t == first) flag_error(p.err, PKV_DEV_BAD_CONTEXT_LEN);
+                if (t == first) flag_error(tell, PKV_DEV_BAD_CONTEXT_LEN);
             } else if (t == first || pos % kBlockTokens == 0) {
                 const int b = pos / kBlockTokens;
                 if (b >= p.table_stride) {
-                    flag_error(p.err, PKV_DEV_TABLE_TOO_NARROW);
+                    flag_error(tell, PKV_DEV_TABLE_TOO_NARROW);
                 } else {
-                    const int id = p.block_tables[size_t(s) * p.table_stride + b];
+                    id = p.block_tables[size_t(s) * p.table_stride + b];
+                    nrow = min(kBlockTokens, ctx - b * kBlockTokens);
                     if (id < 0 || id >= p.num_blocks) {
-                        flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
-                    } else {
-                        const int at = atomicAdd(&count, 1);
-                        blk[at] = id;
-                        rows[at] = min(kBlockTokens, ctx - b * kBlockTokens);
+                        flag_error(tell, PKV_DEV_BAD_BLOCK_ID);
+                        nrow = 0;
                     }
                 }
             }
         }
     }
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    const int tiles = count * p.num_kv_heads;
-    for (int i = threadIdx.x >> 5; i < tiles; i += kBoundsWarps) {
-        const int a = i / p.num_kv_heads, h = i % p.num_kv_heads;
-        const size_t tile = size_t(blk[a]) * p.num_kv_heads + h;
-        const int nrow = rows[a];
-        const T* k = static_cast<const T*>(p.k_cache) + tile * (kBlockTokens * D) +
-                     (lane / LPR) * D + (lane % LPR) * V;
-        float hi[V], lo[V];
+    for (uint32_t found = __ballot_sync(kFull, nrow > 0); found; found &= found - 1) {
+        const int from = __ffs(found) - 1;
+        const int rows = __shfl_sync(kFull, nrow, from);
+        const size_t tile = size_t(__shfl_sync(kFull, id, from)) * p.num_kv_heads + h;
+        const uint4* k = reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_cache) +
+                                                        tile * (kBlockTokens * D)) + lane;
+        uint4 x[kBlockTokens / RPI];
+#pragma unroll
+        for (int i = 0; i < kBlockTokens / RPI; ++i) {
+            // (a lane whose row holds no token repeats row 0)
+            const bool in = i * RPI + lane / LPR < rows;
+            x[i] = __ldg(k + (in ? i * 32 : -(lane / LPR) * LPR));
+        }
+        Extent<T> ex;
+        ex.start(x[0]);
+#pragma unroll
+        for (int i = 1; i < kBlockTokens / RPI; ++i) ex.add(x[i]);
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) ex.fold(o);
+        float amax = 0.f;
         bool odd = false;                        // a value that is not finite
 #pragma unroll
-        for (int j = 0; j < V; ++j) hi[j] = -INFINITY, lo[j] = INFINITY;
-#pragma unroll
-        for (int r = 0; r < kBlockTokens; r += RPI) {
-            if (r + lane / LPR < nrow) {
-                float x[V];
-                load_vec<T, V>(k + r * D, x);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    odd |= !(fabsf(x[j]) <= FLT_MAX);
-                    hi[j] = fmaxf(hi[j], x[j]);
-                    lo[j] = fminf(lo[j], x[j]);
-                }
-            }
+        for (int j = 0; j < V; ++j) {
+            const float a = fmaxf(fabsf(ex.top(j)), fabsf(ex.low(j)));
+            odd |= !(fabsf(ex.top(j)) <= FLT_MAX) || !(fabsf(ex.low(j)) <= FLT_MAX);
+            amax = fmaxf(amax, a);
         }
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                hi[j] = fmaxf(hi[j], __shfl_xor_sync(kFull, hi[j], o));
-                lo[j] = fminf(lo[j], __shfl_xor_sync(kFull, lo[j], o));
-            }
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) amax = fmaxf(amax, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+        // (the bits of values that are not negative order as the values do)
+        amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
         odd = __any_sync(kFull, odd);
         const int e = code_exponent(amax);
-        const float unit = odd ? 0.f : pow2(-e);
-        if (lane < LPR) {
-            alignas(8) int8_t ch[V], cl[V];
+        const float unit_inv = pow2(-e);
+        int8_t* dst = p.bounds + tile * (2 * D) + (lane % LPR) * V;
+        auto write = [&](bool lower) {           // floor(x) = -ceil(-x)
+            uint32_t w[V / 4];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                // (a block with values that are not finite has codes of 0)
-                ch[j] = odd ? 0 : int8_t(fminf(fmaxf(ceilf(hi[j] * unit), -127.f), 127.f));
-                cl[j] = odd ? 0 : int8_t(fminf(fmaxf(floorf(lo[j] * unit), -127.f), 127.f));
+            for (int j = 0; j < V; j += 4) {
+                w[j / 4] = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y = lower ? -ex.low(j + i) : ex.top(j + i);
+                    const int c = int(fminf(fmaxf(ceilf(y * unit_inv), -127.f), 127.f));
+                    w[j / 4] |= uint32_t((lower ? -c : c) & 0xff) << (8 * i);
+                }
+                if (odd) w[j / 4] = 0u;          // (such a block has codes of 0)
             }
-            int8_t* dst = p.bounds + tile * (2 * D) + lane * V;
-            if constexpr (V == 8) {
-                *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(ch);
-                *reinterpret_cast<uint2*>(dst + D) = *reinterpret_cast<const uint2*>(cl);
-            } else {
-                *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(ch);
-                *reinterpret_cast<uint32_t*>(dst + D) = *reinterpret_cast<const uint32_t*>(cl);
-            }
+            if constexpr (V == 8) *reinterpret_cast<uint2*>(dst + lower * D) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(dst + lower * D) = w[0];
+        };
+        if (RPI > 1) {
+            if (lane < 2 * LPR) write(lane >= LPR);
+        } else {
+            write(false);
+            write(true);
         }
         if (lane == 0) p.exps[tile] = int8_t(odd ? kUnbounded : e);
     }
@@ -720,8 +784,11 @@ bool aligned_to(const void* p, uintptr_t a) {
 }
 
 template <typename T, int D>
-int launch_bounds(const BoundsParams& p, unsigned ctas, cudaStream_t s) {
-    return cuda_status(launch_pdl(block_bounds_kernel<T, D>, dim3(ctas), dim3(kBoundsWarps * 32), 0, s, p));
+int launch_bounds(const BoundsParams& p, cudaStream_t s) {
+    const int64_t units = ceil_div(p.tokens, p.span) * int64_t(p.num_kv_heads);
+    return cuda_status(launch_pdl(block_bounds_kernel<T, D>,
+                                  dim3(unsigned((units + kBoundsWarps - 1) / kBoundsWarps)),
+                                  dim3(kBoundsWarps * 32), 0, s, p));
 }
 
 }  // namespace
@@ -738,6 +805,7 @@ extern "C" int pkv_block_bounds(int8_t* bounds, int8_t* exps, const void* k_cach
     if (st != PKV_OK) return st;
     if (max_blocks_per_seq < 1 || num_seqs < 0 || num_query_tokens < 0) return PKV_ERR_INVALID;
     if (!query_start_loc && num_query_tokens != num_seqs) return PKV_ERR_INVALID;
+    if (int64_t(num_query_tokens) * desc->num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     if (!bounds || !exps || !k_cache || !block_tables || !context_lens ||
         !aligned_to(bounds, 16) || !aligned_to(k_cache, 16) || !aligned_to(block_tables, 4) ||
@@ -757,17 +825,17 @@ extern "C" int pkv_block_bounds(int8_t* bounds, int8_t* exps, const void* k_cach
     p.tokens = num_query_tokens;
     p.num_blocks = desc->num_blocks;
     p.num_kv_heads = desc->num_kv_heads;
-    // few tokens: one to a CTA, so that their tiles spread over the GPU; many:
-    // a block's worth, of which one or two stand for a block
+    // few tokens: one to a warp; many: a block's worth, of which one or two stand
+    // for a block
     p.span = 1;
-    while (p.span < kMaxSpan && num_query_tokens / p.span > 4 * num_sms()) p.span *= 2;
-    const unsigned ctas = unsigned(ceil_div(num_query_tokens, p.span));
+    while (p.span < kBlockTokens &&
+           int64_t(num_query_tokens) * desc->num_kv_heads / p.span > 64 * int64_t(num_sms()))
+        p.span *= 2;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (desc->dtype == PKV_BF16)
-        return desc->head_dim == 128 ? launch_bounds<__nv_bfloat16, 128>(p, ctas, cs)
-                                     : launch_bounds<__nv_bfloat16, 64>(p, ctas, cs);
-    return desc->head_dim == 128 ? launch_bounds<float, 128>(p, ctas, cs)
-                                 : launch_bounds<float, 64>(p, ctas, cs);
+        return desc->head_dim == 128 ? launch_bounds<__nv_bfloat16, 128>(p, cs)
+                                     : launch_bounds<__nv_bfloat16, 64>(p, cs);
+    return desc->head_dim == 128 ? launch_bounds<float, 128>(p, cs) : launch_bounds<float, 64>(p, cs);
 }
 
 extern "C" size_t pkv_select_workspace_bytes(const pkv_cache_desc* desc, int32_t num_query_tokens,
