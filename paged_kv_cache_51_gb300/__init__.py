@@ -420,19 +420,20 @@ def _launch_stream(stream):
     return current, stream.cuda_stream
 
 
-def _arg(t, name, dtype, current, *shape):
+def _arg(t, name, dtype, current, numel):
     """The address of a tensor argument, after checking its type, its layout, its
-    device and (if given) its shape: one pass of cheap tests, the message apart."""
+    device and its number of elements (-1: any): one pass of cheap tests, the
+    message apart."""
     if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != current or (
-            shape and t.shape != shape):
+            t.numel() != numel and numel >= 0):
         _need(t, dtype, name)
         _devices_agree([(name, t.device)], current, torch.device("cuda", current))
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        raise ValueError(f"{name}: {t.numel()} elements {tuple(t.shape)}, expected {numel}")
     return t.data_ptr()
 
 
-def _opt(t, name, dtype, current, *shape):
-    return None if t is None else _arg(t, name, dtype, current, *shape)
+def _opt(t, name, dtype, current, numel):
+    return None if t is None else _arg(t, name, dtype, current, numel)
 
 
 def _need(t, dtype, name):
@@ -744,12 +745,12 @@ def pkv_tables_step(tables, seq_rows, cached_lens, new_lens, block_tables, conte
     width = 0 if block_tables is None else block_tables.shape[-1]
     cur, st = _launch_stream(stream)
     i32 = torch.int32
-    _arg(tables.block_table, "block_table", i32, cur)
+    _arg(tables.block_table, "block_table", i32, cur, -1)
     _check(lib().pkv_tables_step(
         ctypes.byref(tables.desc), _opt(seq_rows, "seq_rows", i32, cur, n),
         _arg(cached_lens, "cached_lens", i32, cur, n), _opt(new_lens, "new_lens", i32, cur, n),
         n, T, _opt(free_count_out, "free_count_out", i32, cur, 1),
-        _opt(block_tables, "block_tables", i32, cur, n, width), width,
+        _opt(block_tables, "block_tables", i32, cur, n * width), width,
         _arg(context_lens, "context_lens", i32, cur, n),
         _arg(query_start_loc, "query_start_loc", i32, cur, n + 1),
         _arg(slot_mapping, "slot_mapping", torch.int64, cur, T),
@@ -761,7 +762,7 @@ def pkv_tables_release(tables, seq_rows, lens, stream=None):
     DeviceTables, which hold ``lens`` (CUDA int32 [n]) tokens."""
     n = lens.numel()
     cur, st = _launch_stream(stream)
-    _arg(tables.block_table, "block_table", torch.int32, cur)
+    _arg(tables.block_table, "block_table", torch.int32, cur, -1)
     _check(lib().pkv_tables_release(ctypes.byref(tables.desc),
                                     _opt(seq_rows, "seq_rows", torch.int32, cur, n),
                                     _arg(lens, "lens", torch.int32, cur, n), n, st),
@@ -788,7 +789,7 @@ def _batch_args(block_tables, context_lens, query_start_loc, num_tokens, cur):
     if query_start_loc is None and num_tokens != n:
         raise ValueError(f"{num_tokens} query tokens for {n} sequences need query_start_loc")
     i32 = torch.int32
-    return (_arg(block_tables, "block_tables", i32, cur, n, width), width,
+    return (_arg(block_tables, "block_tables", i32, cur, n * width), width,
             _opt(query_start_loc, "query_start_loc", i32, cur, n + 1),
             _arg(context_lens, "context_lens", i32, cur, n), n)
 
@@ -804,9 +805,9 @@ def pkv_block_bounds(bounds, exps, k_cache, desc, block_tables, context_lens,
     t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, tokens,
                                           cur)
     _check(lib().pkv_block_bounds(
-        _arg(bounds, "bounds", torch.int8, cur, nb, hkv, 2, d),
-        _arg(exps, "exps", torch.int8, cur, nb, hkv),
-        _arg(k_cache, "k_cache", _TORCH_DTYPE[desc.dtype], cur, nb, hkv, desc.block_size, d),
+        _arg(bounds, "bounds", torch.int8, cur, 2 * nb * hkv * d),
+        _arg(exps, "exps", torch.int8, cur, nb * hkv),
+        _arg(k_cache, "k_cache", _TORCH_DTYPE[desc.dtype], cur, nb * hkv * desc.block_size * d),
         ctypes.byref(desc), t, width, start, ctx, n, tokens, st), "pkv_block_bounds")
 
 
@@ -827,12 +828,12 @@ def pkv_select_blocks(selected, q, bounds, exps, desc, block_tables, context_len
     if ws is None:
         ws = workspace(select_workspace_bytes(desc, T, max_context_len), q.device)
     _check(lib().pkv_select_blocks(
-        _arg(selected, "selected", torch.int32, cur, T, hkv, top_k),
-        _arg(q, "q", _TORCH_DTYPE[desc.dtype], cur, T, desc.num_q_heads, d),
-        _arg(bounds, "bounds", torch.int8, cur, nb, hkv, 2, d),
-        _arg(exps, "exps", torch.int8, cur, nb, hkv), ctypes.byref(desc), t, width, start, ctx,
+        _arg(selected, "selected", torch.int32, cur, T * hkv * top_k),
+        _arg(q, "q", _TORCH_DTYPE[desc.dtype], cur, T * desc.num_q_heads * d),
+        _arg(bounds, "bounds", torch.int8, cur, 2 * nb * hkv * d),
+        _arg(exps, "exps", torch.int8, cur, nb * hkv), ctypes.byref(desc), t, width, start, ctx,
         n, T, max_context_len, top_k, num_sink, num_recent,
-        _arg(ws, "ws", torch.uint8, cur), ws.numel(), st), "pkv_select_blocks")
+        _arg(ws, "ws", torch.uint8, cur, -1), ws.numel(), st), "pkv_select_blocks")
     return selected
 
 
@@ -844,15 +845,15 @@ def paged_attention_sparse(out, q, k_cache, v_cache, desc, block_tables, context
     cur, st = _launch_stream(stream)
     hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
     T, top_k, dt = q.shape[0], selected.shape[-1], _TORCH_DTYPE[desc.dtype]
-    pool = (desc.num_blocks, hkv, desc.block_size, d)
+    rows, pool = T * hq * d, desc.num_blocks * hkv * desc.block_size * d
     t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, T, cur)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     _check(lib().paged_attention_sparse(
-        _arg(out, "out", dt, cur, T, hq, d), _arg(q, "q", dt, cur, T, hq, d),
-        _arg(k_cache, "k_cache", dt, cur, *pool), _arg(v_cache, "v_cache", dt, cur, *pool),
+        _arg(out, "out", dt, cur, rows), _arg(q, "q", dt, cur, rows),
+        _arg(k_cache, "k_cache", dt, cur, pool), _arg(v_cache, "v_cache", dt, cur, pool),
         ctypes.byref(desc), t, width, start, ctx,
-        _arg(selected, "selected", torch.int32, cur, T, hkv, top_k), top_k, n, T, scale, st),
+        _arg(selected, "selected", torch.int32, cur, T * hkv * top_k), top_k, n, T, scale, st),
         "paged_attention_sparse")
     return out
 

@@ -10,11 +10,12 @@
 // before it, at position cached_i + j, slot table[position / bs] * bs +
 // position % bs.
 //
-// Two launches.  tables_plan_kernel (one CTA) does what is sequential by
-// nature: the checks, both prefix sums and the few new table entries.
-// tables_fill_kernel spreads the rest over the GPU: rows of tables copied out
-// and padded, slots and positions of the tokens.  The step moves a few hundred
-// KB to a few MB, so it is bound by the latency of the two launches.
+// The step moves a few hundred KB to a few MB, so it is bound by latency.  A
+// small step is one launch of one cluster (tables_small_kernel): every CTA of it
+// makes the prefix sums for itself and then fills its share of the outputs from
+// them.  A large one takes two: tables_plan_kernel (one CTA) does what is
+// sequential by nature, the checks, both sums and the few new table entries;
+// tables_fill_kernel spreads the copies over the GPU.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,6 +23,7 @@
 #include "launch_cache.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "sparse_common.cuh"
 
 namespace pkv {
 namespace {
@@ -108,6 +110,82 @@ __device__ __forceinline__ int64_t blocks_of(int64_t tokens, int bs) {
     return (tokens + bs - 1) / bs;
 }
 
+// What a step hands out: running sums over the passes of kPlanThreads requests.
+struct StepSums {
+    uint32_t need_base = 0, tok_base = 0;         // of the requests before this pass
+    uint32_t used = 0, placed = 0;                // of the served ones
+};
+struct Request {
+    int row, cached, fresh;
+    uint32_t need_in, tok_in;                     // sums that include it
+    uint32_t need_sum, tok_sum;                   // of the whole pass
+    bool ok, served;
+};
+
+// One pass: request `i` of this thread, checked and summed.  Served in order up
+// to the first request that does not fit: both sums only grow, so no later
+// request fits either.
+__device__ __forceinline__ Request plan_pass(const TablesParams& p, int i, const uint32_t* twice,
+                                             uint32_t have, int64_t limit, uint32_t* warp_sums,
+                                             StepSums& s, int* tell) {
+    Request r{-1, 0, 0, 0, 0, 0, 0, false, false};
+    uint32_t need = 0;
+    if (i < p.n) {
+        r.row = row_of(p.seq_rows, i, p.max_seqs, twice);
+        r.cached = p.cached[i];
+        r.fresh = p.fresh ? p.fresh[i] : 1;
+        if (r.row < 0) {
+            flag_error(tell, PKV_DEV_BAD_SEQ_ROW);
+        } else if (r.cached < 0 || r.fresh < 0) {
+            flag_error(tell, PKV_DEV_BAD_CONTEXT_LEN);
+        } else if (int64_t(r.cached) + r.fresh > limit) {
+            flag_error(tell, PKV_DEV_TABLE_TOO_NARROW);
+        } else {
+            r.ok = true;
+            need = uint32_t(blocks_of(int64_t(r.cached) + r.fresh, p.block_size) -
+                            blocks_of(r.cached, p.block_size));
+        }
+    }
+    const uint32_t tok = r.ok ? min(uint32_t(r.fresh), kSat) : 0u;
+    r.need_in = sat_add(s.need_base, scan_inclusive(need, warp_sums, r.need_sum));
+    r.tok_in = sat_add(s.tok_base, scan_inclusive(tok, warp_sums, r.tok_sum));
+    const bool fits = r.need_in <= have && r.tok_in <= uint32_t(p.max_tokens);
+    r.served = r.ok && fits;
+    if (r.ok && !fits)
+        flag_error(tell, r.need_in > have ? PKV_DEV_NO_FREE_BLOCKS : PKV_DEV_BAD_QUERY_LAYOUT);
+    // the sums of served requests: the largest, over the CTA
+    const uint32_t u = __reduce_max_sync(kFull, r.served ? r.need_in : 0u);
+    const uint32_t q = __reduce_max_sync(kFull, r.served ? r.tok_in : 0u);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) warp_sums[warp] = u;
+    __syncthreads();
+    s.used = max(s.used, __reduce_max_sync(kFull, warp_sums[lane]));
+    __syncthreads();
+    if (lane == 0) warp_sums[warp] = q;
+    __syncthreads();
+    s.placed = max(s.placed, __reduce_max_sync(kFull, warp_sums[lane]));
+    __syncthreads();
+    return r;
+}
+
+// The free blocks that a step may take; a count out of range gives none.
+__device__ __forceinline__ uint32_t free_blocks(const TablesParams& p, int count, bool& ok) {
+    ok = count >= 0 && count <= p.num_blocks;
+    return ok ? uint32_t(count) : 0u;
+}
+
+// Entry `k` from the top of the free stack: the id, or -1 if it is none.
+__device__ __forceinline__ int take_block(const TablesParams& p, uint32_t have, uint32_t k, int* tell) {
+    const int blk = p.free_list[have - 1 - k];
+    if (blk >= 0 && blk < p.num_blocks) return blk;
+    flag_error(tell, PKV_DEV_BAD_BLOCK_ID);
+    return -1;
+}
+
+__device__ __forceinline__ int64_t token_limit(const TablesParams& p) {
+    return int64_t(min(p.max_blocks, p.out_tables ? p.width : p.max_blocks)) * p.block_size;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(TablesParams p) {
     extern __shared__ uint32_t bits[];            // two planes of max_seqs bits
     __shared__ uint32_t warp_sums[kPlanWarps];
@@ -120,70 +198,26 @@ __global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(TablesParams 
     if (p.seq_rows)
         mark_rows(p.seq_rows, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
     const int free0 = *p.free_count;
-    const bool free_ok = free0 >= 0 && free0 <= p.num_blocks;
-    const uint32_t have = free_ok ? uint32_t(free0) : 0u;
+    bool free_ok;
+    const uint32_t have = free_blocks(p, free0, free_ok);
     if (!free_ok && threadIdx.x == 0) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
     __syncthreads();                              // everyone read the count before it is written
-    const int64_t limit = int64_t(min(p.max_blocks, p.out_tables ? p.width : p.max_blocks)) *
-                          p.block_size;
-    uint32_t need_base = 0, tok_base = 0;         // of the requests before this pass
-    uint32_t used = 0, placed = 0;                // of the served ones
+    const int64_t limit = token_limit(p);
+    StepSums s;
     for (int base = 0; base < p.n; base += kPlanThreads) {
         const int i = base + threadIdx.x;
-        int row = -1, cached = 0, fresh = 0;
-        uint32_t need = 0;
-        bool ok = false;
+        const Request r = plan_pass(p, i, twice, have, limit, warp_sums, s, p.err);
         if (i < p.n) {
-            row = row_of(p.seq_rows, i, p.max_seqs, twice);
-            cached = p.cached[i];
-            fresh = p.fresh ? p.fresh[i] : 1;
-            if (row < 0) {
-                flag_error(p.err, PKV_DEV_BAD_SEQ_ROW);
-            } else if (cached < 0 || fresh < 0) {
-                flag_error(p.err, PKV_DEV_BAD_CONTEXT_LEN);
-            } else if (int64_t(cached) + fresh > limit) {
-                flag_error(p.err, PKV_DEV_TABLE_TOO_NARROW);
-            } else {
-                ok = true;
-                need = uint32_t(blocks_of(int64_t(cached) + fresh, p.block_size) -
-                                blocks_of(cached, p.block_size));
-            }
+            p.ctx[i] = r.ok ? r.cached + (r.served ? r.fresh : 0) : 0;
+            p.start[i + 1] = int32_t(min(r.tok_in, s.placed));
         }
-        const uint32_t tok = ok ? min(uint32_t(fresh), kSat) : 0u;
-        uint32_t need_sum, tok_sum;
-        const uint32_t need_in = sat_add(need_base, scan_inclusive(need, warp_sums, need_sum));
-        const uint32_t tok_in = sat_add(tok_base, scan_inclusive(tok, warp_sums, tok_sum));
-        // served in order up to the first request that does not fit: both sums
-        // only grow, so no later request fits either
-        const bool fits = need_in <= have && tok_in <= uint32_t(p.max_tokens);
-        const bool served = ok && fits;
-        if (ok && !fits)
-            flag_error(p.err, need_in > have ? PKV_DEV_NO_FREE_BLOCKS : PKV_DEV_BAD_QUERY_LAYOUT);
-        // the sums of served requests: those in front of the first that does not fit
-        const uint32_t need_got = served ? need_in : 0u, tok_got = served ? tok_in : 0u;
-        used = max(used, __reduce_max_sync(kFull, need_got));
-        placed = max(placed, __reduce_max_sync(kFull, tok_got));
-        if ((threadIdx.x & 31) == 0) need_end[threadIdx.x >> 5] = used;
-        if ((threadIdx.x & 31) == 0) dest[threadIdx.x >> 5] = int32_t(placed);
-        __syncthreads();
-        used = need_end[0];
-        placed = uint32_t(dest[0]);
-        for (int w = 1; w < kPlanWarps; ++w) {
-            used = max(used, need_end[w]);
-            placed = max(placed, uint32_t(dest[w]));
-        }
-        __syncthreads();
-        if (i < p.n) {
-            p.ctx[i] = ok ? cached + (served ? fresh : 0) : 0;
-            p.start[i + 1] = int32_t(min(tok_in, placed));
-        }
-        need_end[threadIdx.x] = min(need_in, used);
-        dest[threadIdx.x] = ok ? int32_t(blocks_of(cached, p.block_size)) : 0;
-        dest_row[threadIdx.x] = row;
+        need_end[threadIdx.x] = min(r.need_in, s.used);
+        dest[threadIdx.x] = r.ok ? int32_t(blocks_of(r.cached, p.block_size)) : 0;
+        dest_row[threadIdx.x] = r.row;
         __syncthreads();
         // new entries of the pass, one thread each: the request by bisection
-        const uint32_t first = min(need_base, used);
-        for (uint32_t b = first + threadIdx.x; b < used; b += kPlanThreads) {
+        const uint32_t first = min(s.need_base, s.used);
+        for (uint32_t b = first + threadIdx.x; b < s.used; b += kPlanThreads) {
             int lo = 0, hi = kPlanThreads - 1;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
@@ -191,20 +225,16 @@ __global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(TablesParams 
                 else lo = mid + 1;
             }
             const uint32_t before = lo ? need_end[lo - 1] : first;
-            int blk = p.free_list[have - 1 - b];
-            if (blk < 0 || blk >= p.num_blocks) {
-                flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
-                blk = -1;
-            }
-            p.table[size_t(dest_row[lo]) * p.max_blocks + dest[lo] + (b - before)] = blk;
+            p.table[size_t(dest_row[lo]) * p.max_blocks + dest[lo] + (b - before)] =
+                take_block(p, have, b, p.err);
         }
         __syncthreads();
-        need_base = sat_add(need_base, need_sum);
-        tok_base = sat_add(tok_base, tok_sum);
+        s.need_base = sat_add(s.need_base, r.need_sum);
+        s.tok_base = sat_add(s.tok_base, r.tok_sum);
     }
     if (threadIdx.x == 0) {
         p.start[0] = 0;
-        *p.free_count_out = free_ok ? int32_t(have - used) : free0;
+        *p.free_count_out = free_ok ? int32_t(have - s.used) : free0;
     }
 }
 
@@ -264,6 +294,112 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(TablesParams 
                      ? -1
                      : int64_t(blk) * p.block_size + pos % p.block_size;
     if (p.positions) p.positions[t] = pos;
+}
+
+constexpr int kSmallSeqs = 2048;  // requests of a step in one launch
+constexpr int kSmallCtas = 8;     // CTAs of its cluster
+constexpr int64_t kSmallWork = 1 << 18;   // most table entries and tokens of one launch
+
+// A step in one launch of one cluster.  Every CTA checks and sums all requests
+// and keeps what the outputs are made of in shared memory; then the CTAs fill the
+// outputs side by side.  Inputs may be outputs too (lengths and count in place):
+// they are written once every CTA of the cluster has read them.
+__global__ void __launch_bounds__(kPlanThreads) tables_small_kernel(TablesParams p, int segments,
+                                                                    int copy_warps) {
+    extern __shared__ uint32_t bits[];            // two planes of max_seqs bits
+    __shared__ uint32_t warp_sums[kPlanWarps];
+    __shared__ int32_t row[kSmallSeqs];           // -1: refused
+    __shared__ int32_t old_blocks[kSmallSeqs];    // blocks held, and with the new ones
+    __shared__ int32_t now_blocks[kSmallSeqs];
+    __shared__ uint32_t before[kSmallSeqs];       // new blocks of the requests in front
+    __shared__ int32_t start[kSmallSeqs + 1], ctx[kSmallSeqs];
+    const uint32_t* twice = bits + (p.max_seqs + 31) / 32;
+    const int rank = int(cluster_rank());
+    int* const tell = rank == 0 ? p.err : nullptr;
+    const int lane = threadIdx.x & 31;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    if (p.seq_rows)
+        mark_rows(p.seq_rows, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
+    const int free0 = *p.free_count;
+    bool free_ok;
+    const uint32_t have = free_blocks(p, free0, free_ok);
+    if (!free_ok && threadIdx.x == 0) flag_error(tell, PKV_DEV_BAD_BLOCK_ID);
+    const int64_t limit = token_limit(p);
+    StepSums s;
+    if (threadIdx.x == 0) start[0] = 0;
+    for (int base = 0; base < p.n; base += kPlanThreads) {
+        const int i = base + threadIdx.x;
+        const Request r = plan_pass(p, i, twice, have, limit, warp_sums, s, tell);
+        if (i < p.n) {
+            const int held = r.ok ? int(blocks_of(r.cached, p.block_size)) : 0;
+            ctx[i] = r.ok ? r.cached + (r.served ? r.fresh : 0) : 0;
+            row[i] = r.ok ? r.row : -1;
+            old_blocks[i] = held;
+            now_blocks[i] = r.ok ? int(blocks_of(ctx[i], p.block_size)) : 0;
+            before[i] = r.need_in - (now_blocks[i] - held);
+            start[i + 1] = int32_t(min(r.tok_in, s.placed));
+        }
+        s.need_base = sat_add(s.need_base, r.need_sum);
+        s.tok_base = sat_add(s.tok_base, r.tok_sum);
+    }
+    cluster_sync();                               // (all inputs are read; shared memory is filled)
+    if (rank == 0) {
+        for (int i = threadIdx.x; i < p.n; i += kPlanThreads) p.ctx[i] = ctx[i];
+        for (int i = threadIdx.x; i <= p.n; i += kPlanThreads) p.start[i] = start[i];
+        if (threadIdx.x == 0) *p.free_count_out = free_ok ? int32_t(have - s.used) : free0;
+    }
+    // block j of request i, as the step leaves it
+    auto block = [&](int i, int j, int* flag) {
+        if (j >= old_blocks[i]) return take_block(p, have, before[i] + (j - old_blocks[i]), flag);
+        return p.table[size_t(row[i]) * p.max_blocks + j];
+    };
+    // new entries of the state, one thread each: the request by bisection
+    for (uint32_t b = rank * kPlanThreads + threadIdx.x; b < s.used; b += kSmallCtas * kPlanThreads) {
+        int lo = 0, hi = p.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] + (now_blocks[mid] - old_blocks[mid]) > b) hi = mid;
+            else lo = mid + 1;
+        }
+        p.table[size_t(row[lo]) * p.max_blocks + old_blocks[lo] + (b - before[lo])] =
+            take_block(p, have, b, p.err);
+    }
+    const int warps = kSmallCtas * kPlanWarps;
+    for (int w = rank * kPlanWarps + (threadIdx.x >> 5); w < copy_warps; w += warps) {
+        const int i = w / segments, j0 = (w % segments) * kSegment;
+        int32_t* dst = p.out_tables + size_t(i) * p.width + j0;
+        int32_t v[kSegment / 32];
+#pragma unroll
+        for (int k = 0; k < kSegment / 32; ++k) {
+            const int j = j0 + lane + 32 * k;
+            v[k] = j < now_blocks[i] ? block(i, j, nullptr) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kSegment / 32; ++k) {
+            const int j = lane + 32 * k;
+            if (j0 + j < p.width) dst[j] = v[k];
+        }
+    }
+    const int total = p.n ? start[p.n] : 0;
+    for (int t = rank * kPlanThreads + threadIdx.x; t < p.max_tokens; t += kSmallCtas * kPlanThreads) {
+        int64_t slot = -1;
+        int pos = 0;
+        if (t < total) {
+            int lo = 0, hi = p.n - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (start[mid + 1] > t) hi = mid;
+                else lo = mid + 1;
+            }
+            pos = ctx[lo] - (start[lo + 1] - t);
+            const int blk = block(lo, pos / p.block_size, nullptr);
+            if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
+            else slot = int64_t(blk) * p.block_size + pos % p.block_size;
+        }
+        p.slots[t] = slot;
+        if (p.positions) p.positions[t] = pos;
+    }
 }
 
 struct ReleaseParams {
@@ -419,6 +555,26 @@ extern "C" int pkv_tables_step(const pkv_device_tables* tables, const int32_t* s
     p.width = max_blocks_per_seq;
     p.max_tokens = max_tokens;
     const int smem = seq_rows ? plane_bytes(p.max_seqs) : 0;
+    if (num_seqs <= kSmallSeqs && copy_warps * kSegment + max_tokens <= kSmallWork) {
+        if (kernel_occupancy<tables_small_kernel>(kPlanThreads, plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
+            return PKV_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSmallCtas);
+        cfg.blockDim = dim3(kPlanThreads);
+        cfg.dynamicSmemBytes = size_t(smem);
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kSmallCtas;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cuda_status(
+            cudaLaunchKernelEx(&cfg, tables_small_kernel, p, segments, int(copy_warps)));
+    }
     if (kernel_occupancy<tables_plan_kernel>(kPlanThreads, plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
         return PKV_ERR_CUDA;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
