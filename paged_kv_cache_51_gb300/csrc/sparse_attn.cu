@@ -36,6 +36,15 @@ struct SparseParams {
     int* err;
 };
 
+// Where a CTA of a cluster finds what the others send it: from each its part of
+// the outputs (G * D / cluster floats) and its (max, sum) per head and keys seen.
+template <int D, int kMaxG>
+struct Inbox {
+    static constexpr int kStats = 2 * kMaxG + 1;
+    static constexpr int kMaxCluster = 8;
+    static constexpr int kFloats = kMaxG * D + kMaxCluster * kStats;
+};
+
 template <typename T, int D, int G>
 struct SparseCfg {
     static constexpr int kWarps = 4;
@@ -48,8 +57,8 @@ struct SparseCfg {
     static constexpr int kPOff = kQOff + G * D * 4;                   // weights [warp][G][16]
     static constexpr int kRec = G * (D + 2) + 1;                      // o, m, l, keys seen
     static constexpr int kCombOff = kPOff + kWarps * G * kBlockTokens * 4;
-    static constexpr int kMergedOff = kCombOff + kWarps * kRec * 4;   // the CTA's state
-    static constexpr int kSmem = kMergedOff + kRec * 4;
+    static constexpr int kInboxOff = kCombOff + kWarps * kRec * 4;
+    static constexpr int kSmem = kInboxOff + Inbox<D, G>::kFloats * 4;
 };
 
 // 16-byte chunk c of tile row r, so that the reads of eight lanes (four rows,
@@ -73,12 +82,23 @@ __device__ __forceinline__ void widen16(const void* p, float* x) {
 }
 
 // Merge the CTA's warp states (records in shared memory), then the cluster's,
-// and write the outputs of the (row, head): shared by every variant.
-template <typename T, int D, int kWarps, int kRec>
+// and write the outputs of the (row, head): shared by every variant.  Each CTA
+// owns a part of the outputs; the others send it theirs, so that one cluster
+// barrier stands between the merges and none behind them.
+template <typename T, int D, int kMaxG, int kWarps, int kRec>
 __device__ __forceinline__ void merge_and_write(const SparseParams& p, const float* comb,
-                                                float* merged, int t, int h, int G) {
+                                                float* inbox, int t, int h, int G) {
     constexpr int kThreads = kWarps * 32;
+    constexpr int kStats = Inbox<D, kMaxG>::kStats;
+    const uint32_t cs = cluster_size(), rank = cluster_rank();
+    const int part = G * D / int(cs);                // (a power of two: at most 8 parts)
+    const uint32_t in_u = smem_u32(inbox), stats_u = in_u + kMaxG * D * 4;
+    T* out = static_cast<T*>(p.out) + (size_t(t) * p.num_q_heads + size_t(h) * G) * D;
     __syncthreads();
+    float seen = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) seen += comb[w * kRec + G * (D + 2)];
+    if (cs > 1) cluster_wait();                      // the others have started
     for (int i = threadIdx.x; i < G * D; i += kThreads) {
         const int g = i / D;
         float M = -INFINITY, L = 0.f, O = 0.f;
@@ -92,51 +112,47 @@ __device__ __forceinline__ void merge_and_write(const SparseParams& p, const flo
             L = fmaf(r[G * D + G + g], s, L);
             O = fmaf(r[i], s, O);
         }
-        merged[i] = O;
-        if (i % D == 0) {
-            merged[G * D + g] = M;
-            merged[G * D + G + g] = L;
+        if (cs == 1) {
+            // a row whose list names no key it sees is 0
+            out[i] = Elem<T>::store_val(seen > 0.f ? O / L : 0.f);
+            continue;
+        }
+        st_cluster(map_rank(in_u + (rank * part + i % part) * 4, i / part), __float_as_uint(O));
+        if (i % D < int(cs)) {                       // the statistics to CTA i % D
+            const uint32_t s = map_rank(stats_u + rank * (kStats * 4), i % D);
+            st_cluster(s + g * 4, __float_as_uint(M));
+            st_cluster(s + (G + g) * 4, __float_as_uint(L));
+            if (g == 0) st_cluster(s + 2 * G * 4, __float_as_uint(seen));
         }
     }
-    if (threadIdx.x == 0) {
-        float seen = 0.f;
-        for (int w = 0; w < kWarps; ++w) seen += comb[w * kRec + G * (D + 2)];
-        merged[G * (D + 2)] = seen;
-    }
-    const uint32_t cs = cluster_size(), rank = cluster_rank();
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
-    const uint32_t base = smem_u32(merged);
-    T* out = static_cast<T*>(p.out) + (size_t(t) * p.num_q_heads + size_t(h) * G) * D;
-    for (int i = int(rank) * kThreads + threadIdx.x; i < G * D; i += int(cs) * kThreads) {
-        const int g = i / D;
-        float M = -INFINITY, L = 0.f, O = 0.f, seen = 0.f;
-        for (uint32_t c = 0; c < cs; ++c)
-            M = fmaxf(M, ld_cluster(map_rank(base + (G * D + g) * 4, c)));
+    if (cs == 1) return;
+    cluster_sync();
+    const float* stats = inbox + kMaxG * D;
+    for (int i = threadIdx.x; i < part; i += kThreads) {
+        const int at = int(rank) * part + i, g = at / D;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+        seen = 0.f;
+        for (uint32_t c = 0; c < cs; ++c) M = fmaxf(M, stats[c * kStats + g]);
         const float Mx = M == -INFINITY ? 0.f : M;
         for (uint32_t c = 0; c < cs; ++c) {
-            const uint32_t r = map_rank(base, c);
-            const float s = exp2f(ld_cluster(r + (G * D + g) * 4) - Mx);
-            L = fmaf(ld_cluster(r + (G * D + G + g) * 4), s, L);
-            O = fmaf(ld_cluster(r + i * 4), s, O);
-            seen += ld_cluster(r + G * (D + 2) * 4);
+            const float s = exp2f(stats[c * kStats + g] - Mx);
+            L = fmaf(stats[c * kStats + G + g], s, L);
+            O = fmaf(inbox[c * part + i], s, O);
+            seen += stats[c * kStats + 2 * G];
         }
-        // a row whose list names no key it sees is 0
-        out[i] = Elem<T>::store_val(seen > 0.f ? O / L : 0.f);
+        out[at] = Elem<T>::store_val(seen > 0.f ? O / L : 0.f);
     }
-    if (cs > 1) cluster_sync();          // the others have read this CTA's state
 }
 
 // A warp's own list entries: tile j of the warp is entry first + j * stride.
-// Entry -> logical block -> physical block, 32 tiles at a time.
+// Entry `e`, block b -> physical block, 32 tiles at a time.
 struct ListCursor {
     int phys, logical;                   // this lane's tile of the current 32
 };
-__device__ __forceinline__ ListCursor fetch_tiles(const SparseParams& p, const int32_t* list,
-                                                  int seq, int blocks, int e) {
+__device__ __forceinline__ ListCursor fetch_tiles(const SparseParams& p, int b, int seq,
+                                                  int blocks, int e) {
     ListCursor c{-1, 0};
     if (e < p.top_k) {
-        const int b = list[e];
         if (b >= blocks) {
             flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
         } else if (b >= 0) {
@@ -157,32 +173,42 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
     extern __shared__ __align__(128) unsigned char smem[];
     float* qs = reinterpret_cast<float*>(smem + C::kQOff);
     float* comb = reinterpret_cast<float*>(smem + C::kCombOff);
-    float* merged = reinterpret_cast<float*>(smem + C::kMergedOff);
+    float* inbox = reinterpret_cast<float*>(smem + C::kInboxOff);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t cs = cluster_size(), rank = cluster_rank();
     const int item = int(blockIdx.x / cs);
     const int t = item / p.num_kv_heads, h = item % p.num_kv_heads;
+    if (cs > 1) cluster_arrive();                // (waited for before the others are written to)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
+    const int32_t* list = p.selected + size_t(item) * p.top_k;
+    const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
+    // the first entries, asked for before the row's context is known
+    const int entry0 = first + lane * stride < p.top_k ? list[first + lane * stride] : -1;
     int seq;
     const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
-    if (keys < 0) return;                        // the whole cluster: left as it is
+    if (keys < 0) {                              // the whole cluster: left as it is
+        if (cs > 1) cluster_wait();
+        return;
+    }
     const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
     for (int i = threadIdx.x; i < G * D; i += C::kThreads)
         qs[i] = float(static_cast<const T*>(p.q)[(size_t(t) * p.num_q_heads + size_t(h) * G) * D + i]);
     __syncthreads();
 
-    const int32_t* list = p.selected + size_t(item) * p.top_k;
-    const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
     const int tiles = p.top_k > first ? (p.top_k - first + stride - 1) / stride : 0;
     unsigned char* ring = smem + warp * (C::kStages * C::kStageBytes);
     const uint32_t ring_u = smem_u32(ring);
     float* ps = reinterpret_cast<float*>(smem + C::kPOff) + warp * (G * kBlockTokens);
 
+    auto fetch = [&](int j) {
+        const int e = first + (j + lane) * stride;
+        return fetch_tiles(p, j ? (e < p.top_k ? list[e] : -1) : entry0, seq, blocks, e);
+    };
     ListCursor next{-1, 0}, now{-1, 0};          // tiles being requested, tiles being used
     auto request = [&](int j) {
         if (j < tiles) {
-            if (j % 32 == 0) next = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+            if (j % 32 == 0) next = fetch(j);
             const int id = __shfl_sync(kFull, next.phys, j % 32);
             if (id >= 0) {
                 const size_t off = (size_t(id) * p.num_kv_heads + h) * (kBlockTokens * D);
@@ -203,6 +229,7 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
         cp_commit();
     };
     for (int j = 0; j < C::kStages - 1; ++j) request(j);
+    const ListCursor now0 = next;
 
     float o[G][DL], m[G], l[G];
 #pragma unroll
@@ -216,7 +243,7 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
     const int key = lane >> 1, half = lane & 1;
     for (int j = 0; j < tiles; ++j) {
         request(j + C::kStages - 1);
-        if (j % 32 == 0) now = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+        if (j % 32 == 0) now = j ? fetch(j) : now0;
         const int id = __shfl_sync(kFull, now.phys, j % 32);
         const int b = __shfl_sync(kFull, now.logical, j % 32);
         cp_wait<C::kStages - 1>();
@@ -284,7 +311,7 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<T, D, C::kWarps, C::kRec>(p, comb, merged, t, h, G);
+    merge_and_write<T, D, G, C::kWarps, C::kRec>(p, comb, inbox, t, h, G);
 }
 
 // ---- bf16 on tensor cores -------------------------------------------------------
@@ -322,7 +349,8 @@ struct SparseMmaCfg {
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kRec = kMaxG * (D + 2) + 1;
-    static constexpr int kSmem = kRingBytes + kRec * 4;   // the warps' records go over the ring
+    // (the warps' records go over the ring)
+    static constexpr int kSmem = kRingBytes + Inbox<D, kMaxG>::kFloats * 4;
     static_assert(kWarps * kRec * 4 <= kRingBytes, "records fit into the ring");
 };
 
@@ -337,28 +365,38 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
     constexpr int RC = D / 8;                    // 16-byte chunks of a row
     extern __shared__ __align__(128) unsigned char smem[];
     float* comb = reinterpret_cast<float*>(smem);
-    float* merged = reinterpret_cast<float*>(smem + C::kRingBytes);
+    float* inbox = reinterpret_cast<float*>(smem + C::kRingBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3, mi = lane >> 3;
     const int G = p.num_q_heads / p.num_kv_heads;
     const uint32_t cs = cluster_size(), rank = cluster_rank();
     const int item = int(blockIdx.x / cs);
     const int t = item / p.num_kv_heads, h = item % p.num_kv_heads;
+    if (cs > 1) cluster_arrive();                // (waited for before the others are written to)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    int seq;
-    const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
-    if (keys < 0) return;                        // the whole cluster: left as it is
-    const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
     const int32_t* list = p.selected + size_t(item) * p.top_k;
     const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
+    // the first entries, asked for before the row's context is known
+    const int entry0 = first + lane * stride < p.top_k ? list[first + lane * stride] : -1;
+    int seq;
+    const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    if (keys < 0) {                              // the whole cluster: left as it is
+        if (cs > 1) cluster_wait();
+        return;
+    }
+    const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
     const int tiles = p.top_k > first ? (p.top_k - first + stride - 1) / stride : 0;
     const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStageBytes);
 
+    auto fetch = [&](int j) {
+        const int e = first + (j + lane) * stride;
+        return fetch_tiles(p, j ? (e < p.top_k ? list[e] : -1) : entry0, seq, blocks, e);
+    };
     ListCursor next{-1, 0}, now{-1, 0};
     auto request = [&](int j) {
         if (j < tiles) {
-            if (j % 32 == 0) next = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+            if (j % 32 == 0) next = fetch(j);
             const int id = __shfl_sync(kFull, next.phys, j % 32);
             if (id >= 0) {
                 const size_t off = (size_t(id) * p.num_kv_heads + h) * (kBlockTokens * D);
@@ -380,6 +418,7 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
         cp_commit();
     };
     for (int j = 0; j < C::kStages - 1; ++j) request(j);
+    const ListCursor now0 = next;
 
     // q as the A operand: row gid is query head gid of the group
     uint32_t q0[D / 16], q2[D / 16];
@@ -399,7 +438,7 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
     int seen = 0;
     for (int j = 0; j < tiles; ++j) {
         request(j + C::kStages - 1);
-        if (j % 32 == 0) now = fetch_tiles(p, list, seq, blocks, first + (j + lane) * stride);
+        if (j % 32 == 0) now = j ? fetch(j) : now0;
         const int id = __shfl_sync(kFull, now.phys, j % 32);
         const int b = __shfl_sync(kFull, now.logical, j % 32);
         cp_wait<C::kStages - 1>();
@@ -485,7 +524,7 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<__nv_bfloat16, D, C::kWarps, C::kRec>(p, comb, merged, t, h, G);
+    merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps, C::kRec>(p, comb, inbox, t, h, G);
 }
 
 // CTAs that share one (row, head): enough to give every SM two CTAs, but each
