@@ -36,6 +36,9 @@ struct SparseParams {
     int* err;
 };
 
+// Floats of a warp's record: outputs [G][D], max [G], sum [G], keys seen.
+constexpr int record_floats(int g, int d) { return (g * (d + 2) + 1 + 3) & ~3; }
+
 // Where a CTA of a cluster finds what the others send it: from each its part of
 // the outputs (G * D / cluster floats) and its (max, sum) per head and keys seen.
 template <int D, int kMaxG>
@@ -55,7 +58,7 @@ struct SparseCfg {
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kQOff = kRingBytes;                          // q as fp32 [G][D]
     static constexpr int kPOff = kQOff + G * D * 4;                   // weights [warp][G][16]
-    static constexpr int kRec = G * (D + 2) + 1;                      // o, m, l, keys seen
+    static constexpr int kRec = record_floats(G, D);
     static constexpr int kCombOff = kPOff + kWarps * G * kBlockTokens * 4;
     static constexpr int kInboxOff = kCombOff + kWarps * kRec * 4;
     static constexpr int kSmem = kInboxOff + Inbox<D, G>::kFloats * 4;
@@ -84,45 +87,68 @@ __device__ __forceinline__ void widen16(const void* p, float* x) {
 // Merge the CTA's warp states (records in shared memory), then the cluster's,
 // and write the outputs of the (row, head): shared by every variant.  Each CTA
 // owns a part of the outputs; the others send it theirs, so that one cluster
-// barrier stands between the merges and none behind them.
-template <typename T, int D, int kMaxG, int kWarps, int kRec>
-__device__ __forceinline__ void merge_and_write(const SparseParams& p, const float* comb,
-                                                float* inbox, int t, int h, int G) {
+// barrier stands between the merges and none behind them.  The factors of a head
+// are made once, not by every output.
+template <typename T, int D, int kMaxG, int kWarps>
+__device__ __forceinline__ void merge_and_write(const SparseParams& p, float* comb, float* inbox,
+                                                int t, int h, int G) {
     constexpr int kThreads = kWarps * 32;
+    constexpr int kRec = record_floats(kMaxG, D);
     constexpr int kStats = Inbox<D, kMaxG>::kStats;
     const uint32_t cs = cluster_size(), rank = cluster_rank();
-    const int part = G * D / int(cs);                // (a power of two: at most 8 parts)
+    const int part_log2 = 31 - __clz(G * D) - (31 - __clz(int(cs)));   // all powers of two
+    const int part = 1 << part_log2;
     const uint32_t in_u = smem_u32(inbox), stats_u = in_u + kMaxG * D * 4;
     T* out = static_cast<T*>(p.out) + (size_t(t) * p.num_q_heads + size_t(h) * G) * D;
     __syncthreads();
-    float seen = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) seen += comb[w * kRec + G * (D + 2)];
     if (cs > 1) cluster_wait();                      // the others have started
-    for (int i = threadIdx.x; i < G * D; i += kThreads) {
-        const int g = i / D;
-        float M = -INFINITY, L = 0.f, O = 0.f;
+    // one head each: the warps' factors over the maxima, and the CTA's statistics
+    if (int(threadIdx.x) < G) {
+        const int g = threadIdx.x;
+        float M = -INFINITY, L = 0.f, seen = 0.f, s[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[w * kRec + G * D + g]);
         const float Mx = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float* r = comb + w * kRec;
-            const float s = exp2f(r[G * D + g] - Mx);
-            L = fmaf(r[G * D + G + g], s, L);
-            O = fmaf(r[i], s, O);
+            s[w] = exp2f(comb[w * kRec + G * D + g] - Mx);
+            L = fmaf(comb[w * kRec + G * D + G + g], s[w], L);
+            seen += comb[w * kRec + 2 * G + G * D];
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) comb[w * kRec + G * D + g] = s[w];
+        // (a row whose list names no key it sees is 0)
+        if (cs == 1) comb[G * D + G + g] = seen > 0.f ? L : INFINITY;
+        for (uint32_t c = 0; cs > 1 && c < cs; ++c) {
+            const uint32_t at = map_rank(stats_u + rank * (kStats * 4), c);
+            st_cluster(at + g * 4, __float_as_uint(M));
+            st_cluster(at + (G + g) * 4, __float_as_uint(L));
+            if (g == 0) st_cluster(at + 2 * G * 4, __float_as_uint(seen));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < (kMaxG * D / 4 + kThreads - 1) / kThreads; ++k) {
+        const int i = (k * kThreads + threadIdx.x) * 4;
+        if (i >= G * D) break;
+        const int g = i / D;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 o = *reinterpret_cast<const float4*>(comb + w * kRec + i);
+            const float s = comb[w * kRec + G * D + g];
+            O.x = fmaf(o.x, s, O.x);
+            O.y = fmaf(o.y, s, O.y);
+            O.z = fmaf(o.z, s, O.z);
+            O.w = fmaf(o.w, s, O.w);
         }
         if (cs == 1) {
-            // a row whose list names no key it sees is 0
-            out[i] = Elem<T>::store_val(seen > 0.f ? O / L : 0.f);
-            continue;
-        }
-        st_cluster(map_rank(in_u + (rank * part + i % part) * 4, i / part), __float_as_uint(O));
-        if (i % D < int(cs)) {                       // the statistics to CTA i % D
-            const uint32_t s = map_rank(stats_u + rank * (kStats * 4), i % D);
-            st_cluster(s + g * 4, __float_as_uint(M));
-            st_cluster(s + (G + g) * 4, __float_as_uint(L));
-            if (g == 0) st_cluster(s + 2 * G * 4, __float_as_uint(seen));
+            const float L = comb[G * D + G + g];
+            const float v[4] = {O.x / L, O.y / L, O.z / L, O.w / L};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[i + e] = Elem<T>::store_val(v[e]);
+        } else {
+            st_cluster(map_rank(in_u + (rank * part + (i & (part - 1))) * 4, i >> part_log2), O);
         }
     }
     if (cs == 1) return;
@@ -130,8 +156,7 @@ __device__ __forceinline__ void merge_and_write(const SparseParams& p, const flo
     const float* stats = inbox + kMaxG * D;
     for (int i = threadIdx.x; i < part; i += kThreads) {
         const int at = int(rank) * part + i, g = at / D;
-        float M = -INFINITY, L = 0.f, O = 0.f;
-        seen = 0.f;
+        float M = -INFINITY, L = 0.f, O = 0.f, seen = 0.f;
         for (uint32_t c = 0; c < cs; ++c) M = fmaxf(M, stats[c * kStats + g]);
         const float Mx = M == -INFINITY ? 0.f : M;
         for (uint32_t c = 0; c < cs; ++c) {
@@ -311,7 +336,7 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<T, D, G, C::kWarps, C::kRec>(p, comb, inbox, t, h, G);
+    merge_and_write<T, D, G, C::kWarps>(p, comb, inbox, t, h, G);
 }
 
 // ---- bf16 on tensor cores -------------------------------------------------------
@@ -348,7 +373,7 @@ struct SparseMmaCfg {
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-    static constexpr int kRec = kMaxG * (D + 2) + 1;
+    static constexpr int kRec = record_floats(kMaxG, D);
     // (the warps' records go over the ring)
     static constexpr int kSmem = kRingBytes + Inbox<D, kMaxG>::kFloats * 4;
     static_assert(kWarps * kRec * 4 <= kRingBytes, "records fit into the ring");
@@ -524,7 +549,7 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps, C::kRec>(p, comb, inbox, t, h, G);
+    merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps>(p, comb, inbox, t, h, G);
 }
 
 // CTAs that share one (row, head): enough to give every SM two CTAs, but each
