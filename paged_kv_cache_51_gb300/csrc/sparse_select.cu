@@ -621,6 +621,11 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
         lo = __reduce_min_sync(kFull, s.warp_a[lane % S::kWarps]);
         hi = __reduce_max_sync(kFull, s.warp_b[lane % S::kWarps]);
         for (;;) {                               // the range lo .. hi holds the want-th
+            if (lo == hi) {                      // equal keys (a query of zeros): the lower indices
+                cut = lo;
+                take = want;
+                break;
+            }
             const int shift = max(0, 32 - __clz(hi - lo) - (31 - __clz(S::kBins)));
             each([&](uint32_t k) {
                 if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
@@ -657,11 +662,6 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
             const uint32_t last = min(hi, first + ((1u << shift) - 1u));
             if (want == inside) {                // the whole bin (no key is 0: -inf's is above)
                 cut = first - 1;
-                break;
-            }
-            if (first == last) {                 // equal keys: the lower indices
-                cut = first;
-                take = want;
                 break;
             }
             if (inside <= uint32_t(NT)) {
@@ -771,10 +771,11 @@ int launch_pick_t(const SelectParams& p, cudaStream_t s) {
                                   s, p));
 }
 
-// The least threads that hold a row's keys.  (2048 rows of up to 512 blocks, the
-// kernel alone: 7.1 us with two warps to a row, 21 us with one.)
+// The least threads that hold a row's keys, four to eight each.  (2048 rows of up
+// to 512 blocks, the whole call: 39.3 us with four warps to a row, 40.9 with two;
+// one alone takes 21 us where two take 7.)
 int launch_pick(const SelectParams& p, cudaStream_t s) {
-    if (p.stride <= 64 * 8) return launch_pick_t<64, 8>(p, s);
+    if (p.stride <= 128 * 4) return launch_pick_t<128, 4>(p, s);
     if (p.stride <= 256 * 8) return launch_pick_t<256, 8>(p, s);
     return launch_pick_t<512, 0>(p, s);
 }

@@ -201,7 +201,7 @@ def test_selection_from_keys_in_few_bins(pkv, kind):
     q = np.zeros((1, 1, d), np.float32)
     q[0, 0, 0] = 1.0
     t = rng.permutation(n).astype(np.int32)[None, :]
-    for top_k in (3, 700, 2999):
+    for top_k in (3, 4, 700, 2999):
         got = _run_select(pkv, "f32", q, bounds, exps, t, [n * 16], [0, 1], top_k, 1, 1)
         assert pkv.device_error() == 0
         ref = sparse.select(q, bounds, exps, t, [0, 1], [n * 16], 16, top_k, 1, 1, "f32")
