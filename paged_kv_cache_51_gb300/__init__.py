@@ -2,8 +2,10 @@
 
 Every function here only marshals arguments (tensor data pointers, sizes and
 the current CUDA stream) into the C ABI declared in include/pagedkv.h; all work
-runs in the library's CUDA kernels or its C++ block pool.  There is no fallback:
-if the library is missing or was built for another machine, calls raise.
+runs in the library's CUDA kernels or its C++ block pool.  The calls of the
+shortest kernels (device tables, sparse attention) are marshalled by the extension
+module _hotcalls, the others through ctypes.  There is no fallback: if the library
+is missing or was built for another machine, calls raise.
 
 PyTorch supplies device memory and streams only.
 """
@@ -408,32 +410,26 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
-def _launch_stream(stream):
-    """The current CUDA device's index and the handle of a launch's stream (the
-    current one by default), which has to be on that device.  The default
-    stream's handle is asked for directly: building a stream object to read it
-    from costs more than the rest of a call's checks."""
-    current = torch.cuda.current_device()
+_hot = None
+
+
+def _native():
+    """The extension module that marshals the shortest calls (built with the library)."""
+    global _hot
+    if _hot is None:
+        lib()                      # loads the library the module is linked to, or says what is missing
+        from . import _hotcalls as module
+        _hot = module
+    return _hot
+
+
+def _handle(stream):
+    """A stream argument for the extension module: None (the current stream) or the
+    handle of a stream on the current CUDA device."""
     if stream is None:
-        return current, torch._C._cuda_getCurrentRawStream(current)
-    _devices_agree((), current, stream.device)
-    return current, stream.cuda_stream
-
-
-def _arg(t, name, dtype, current, numel):
-    """The address of a tensor argument, after checking its type, its layout, its
-    device and its number of elements (-1: any): one pass of cheap tests, the
-    message apart."""
-    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != current or (
-            t.numel() != numel and numel >= 0):
-        _need(t, dtype, name)
-        _devices_agree([(name, t.device)], current, torch.device("cuda", current))
-        raise ValueError(f"{name}: {t.numel()} elements {tuple(t.shape)}, expected {numel}")
-    return t.data_ptr()
-
-
-def _opt(t, name, dtype, current, numel):
-    return None if t is None else _arg(t, name, dtype, current, numel)
+        return None
+    _devices_agree((), torch.cuda.current_device(), stream.device)
+    return stream.cuda_stream
 
 
 def _need(t, dtype, name):
@@ -741,32 +737,17 @@ def pkv_tables_step(tables, seq_rows, cached_lens, new_lens, block_tables, conte
     one token each); written: block_tables [n, W] (or None), context_lens [n],
     query_start_loc [n + 1], slot_mapping (int64 [T], T the most tokens of the
     step), positions [T] (or None), free_count_out [1] (None: in place)."""
-    n, T = cached_lens.numel(), slot_mapping.numel()
-    width = 0 if block_tables is None else block_tables.shape[-1]
-    cur, st = _launch_stream(stream)
-    i32 = torch.int32
-    _arg(tables.block_table, "block_table", i32, cur, -1)
-    _check(lib().pkv_tables_step(
-        ctypes.byref(tables.desc), _opt(seq_rows, "seq_rows", i32, cur, n),
-        _arg(cached_lens, "cached_lens", i32, cur, n), _opt(new_lens, "new_lens", i32, cur, n),
-        n, T, _opt(free_count_out, "free_count_out", i32, cur, 1),
-        _opt(block_tables, "block_tables", i32, cur, n * width), width,
-        _arg(context_lens, "context_lens", i32, cur, n),
-        _arg(query_start_loc, "query_start_loc", i32, cur, n + 1),
-        _arg(slot_mapping, "slot_mapping", torch.int64, cur, T),
-        _opt(positions, "positions", i32, cur, T), st), "pkv_tables_step")
+    _check(_native().tables_step(tables.desc, tables.block_table, seq_rows, cached_lens,
+                                   new_lens, block_tables, context_lens, query_start_loc,
+                                   slot_mapping, positions, free_count_out, _handle(stream)),
+           "pkv_tables_step")
 
 
 def pkv_tables_release(tables, seq_rows, lens, stream=None):
     """Give back the blocks of rows ``seq_rows`` (CUDA int32 [n]; None: row i) of a
     DeviceTables, which hold ``lens`` (CUDA int32 [n]) tokens."""
-    n = lens.numel()
-    cur, st = _launch_stream(stream)
-    _arg(tables.block_table, "block_table", torch.int32, cur, -1)
-    _check(lib().pkv_tables_release(ctypes.byref(tables.desc),
-                                    _opt(seq_rows, "seq_rows", torch.int32, cur, n),
-                                    _arg(lens, "lens", torch.int32, cur, n), n, st),
-           "pkv_tables_release")
+    _check(_native().tables_release(tables.desc, tables.block_table, seq_rows, lens,
+                                      _handle(stream)), "pkv_tables_release")
 
 
 # ----------------------------------------------------------------------------
@@ -782,33 +763,14 @@ class BlockBounds:
         self.exps = torch.zeros((num_blocks, num_kv_heads), dtype=torch.int8, device=device)
 
 
-def _batch_args(block_tables, context_lens, query_start_loc, num_tokens, cur):
-    """Addresses of a sparse entry point's batch (tables, their width, layout,
-    contexts) and its number of sequences, checked."""
-    n, width = context_lens.numel(), block_tables.shape[-1]
-    if query_start_loc is None and num_tokens != n:
-        raise ValueError(f"{num_tokens} query tokens for {n} sequences need query_start_loc")
-    i32 = torch.int32
-    return (_arg(block_tables, "block_tables", i32, cur, n * width), width,
-            _opt(query_start_loc, "query_start_loc", i32, cur, n + 1),
-            _arg(context_lens, "context_lens", i32, cur, n), n)
-
-
 def pkv_block_bounds(bounds, exps, k_cache, desc, block_tables, context_lens,
                      query_start_loc=None, num_query_tokens=None, stream=None):
     """Bring the key bounds (CUDA int8 [NB, Hkv, 2, D], exps int8 [NB, Hkv]) of the
     blocks that a step's tokens were appended to up to date.  One new token per
     sequence, or query_start_loc (CUDA int32 [S + 1]) and the number of tokens."""
-    cur, st = _launch_stream(stream)
-    nb, hkv, d = desc.num_blocks, desc.num_kv_heads, desc.head_dim
-    tokens = context_lens.numel() if num_query_tokens is None else num_query_tokens
-    t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, tokens,
-                                          cur)
-    _check(lib().pkv_block_bounds(
-        _arg(bounds, "bounds", torch.int8, cur, 2 * nb * hkv * d),
-        _arg(exps, "exps", torch.int8, cur, nb * hkv),
-        _arg(k_cache, "k_cache", _TORCH_DTYPE[desc.dtype], cur, nb * hkv * desc.block_size * d),
-        ctypes.byref(desc), t, width, start, ctx, n, tokens, st), "pkv_block_bounds")
+    _check(_native().block_bounds(bounds, exps, k_cache, desc, block_tables, context_lens,
+                                    query_start_loc, num_query_tokens, _handle(stream)),
+           "pkv_block_bounds")
 
 
 def select_workspace_bytes(desc, num_query_tokens, max_context_len):
@@ -821,19 +783,11 @@ def pkv_select_blocks(selected, q, bounds, exps, desc, block_tables, context_len
                       stream=None):
     """List the blocks that each (query token, KV head) attends: selected CUDA int32
     [T, Hkv, top_k], q [T, Hq, D]."""
-    cur, st = _launch_stream(stream)
-    nb, hkv, d = desc.num_blocks, desc.num_kv_heads, desc.head_dim
-    T, top_k = q.shape[0], selected.shape[-1]
-    t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, T, cur)
     if ws is None:
-        ws = workspace(select_workspace_bytes(desc, T, max_context_len), q.device)
-    _check(lib().pkv_select_blocks(
-        _arg(selected, "selected", torch.int32, cur, T * hkv * top_k),
-        _arg(q, "q", _TORCH_DTYPE[desc.dtype], cur, T * desc.num_q_heads * d),
-        _arg(bounds, "bounds", torch.int8, cur, 2 * nb * hkv * d),
-        _arg(exps, "exps", torch.int8, cur, nb * hkv), ctypes.byref(desc), t, width, start, ctx,
-        n, T, max_context_len, top_k, num_sink, num_recent,
-        _arg(ws, "ws", torch.uint8, cur, -1), ws.numel(), st), "pkv_select_blocks")
+        ws = workspace(select_workspace_bytes(desc, q.shape[0], max_context_len), q.device)
+    _check(_native().select_blocks(selected, q, bounds, exps, desc, block_tables, context_lens,
+                                     max_context_len, num_sink, num_recent, query_start_loc, ws,
+                                     _handle(stream)), "pkv_select_blocks")
     return selected
 
 
@@ -842,19 +796,9 @@ def paged_attention_sparse(out, q, k_cache, v_cache, desc, block_tables, context
     """Attention of each (query token, KV head) over the blocks that ``selected``
     (CUDA int32 [T, Hkv, top_k], logical block indices, negative ones skipped)
     lists; out, q: CUDA [T, Hq, D]."""
-    cur, st = _launch_stream(stream)
-    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
-    T, top_k, dt = q.shape[0], selected.shape[-1], _TORCH_DTYPE[desc.dtype]
-    rows, pool = T * hq * d, desc.num_blocks * hkv * desc.block_size * d
-    t, width, start, ctx, n = _batch_args(block_tables, context_lens, query_start_loc, T, cur)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    _check(lib().paged_attention_sparse(
-        _arg(out, "out", dt, cur, rows), _arg(q, "q", dt, cur, rows),
-        _arg(k_cache, "k_cache", dt, cur, pool), _arg(v_cache, "v_cache", dt, cur, pool),
-        ctypes.byref(desc), t, width, start, ctx,
-        _arg(selected, "selected", torch.int32, cur, T * hkv * top_k), top_k, n, T, scale, st),
-        "paged_attention_sparse")
+    _check(_native().attention_sparse(out, q, k_cache, v_cache, desc, block_tables,
+                                        context_lens, selected, query_start_loc, scale,
+                                        _handle(stream)), "paged_attention_sparse")
     return out
 
 

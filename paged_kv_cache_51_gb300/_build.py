@@ -1,8 +1,10 @@
-"""Build libpagedkv.so in-tree with nvcc for sm_103a (GB300).
+"""Build libpagedkv.so in-tree with nvcc for sm_103a (GB300), and _hotcalls.so.
 
 Every translation unit under csrc/ is compiled in parallel, then linked into
-one shared library next to this file.  A stamp of the sources and flags skips
-the build when nothing changed.
+one shared library next to this file.  _hotcalls.so (binding/hotcalls.cpp) is the
+Python extension that marshals the calls of the shortest kernels; it is compiled
+beside the library, against the installed torch, and linked to it.  A stamp of the
+sources and flags skips the build when nothing changed.
 """
 
 import hashlib
@@ -16,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
+BINDING_SRC = os.path.join(HERE, "binding", "hotcalls.cpp")
+BINDING = os.path.join(HERE, "_hotcalls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -85,9 +89,63 @@ def build(force=False, verbose=False):
     with open(LIB + ".lock", "w") as lock:
         fcntl.flock(lock, fcntl.LOCK_EX)
         try:
-            return _build_locked(force, verbose)
+            with ThreadPoolExecutor(max_workers=1) as ex:
+                binding = ex.submit(_compile_binding, force)
+                lib = _build_locked(force, verbose)
+                _link_binding(*binding.result())
+            return lib
         finally:
             fcntl.flock(lock, fcntl.LOCK_UN)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(force):
+    """The binding's object file and the stamp of what it was made from; the object
+    is None when the module in place is up to date."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    flags = (["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+             + [f"-I{d}" for d in (os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
+                                   os.path.join(root, "include"),
+                                   os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                                   os.path.join(cuda, "include"))])
+    h = hashlib.sha256(repr((flags, torch.__version__)).encode())
+    for path in (BINDING_SRC, os.path.join(ROOT, "include", "pagedkv.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    stamp = h.hexdigest()
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING + ".stamp"):
+        with open(BINDING + ".stamp") as f:
+            if f.read().strip() == stamp:
+                return None, stamp
+    os.makedirs(BUILD, exist_ok=True)
+    obj = os.path.join(BUILD, "hotcalls.cpp.o")
+    _run(["g++"] + flags + ["-c", BINDING_SRC, "-o", obj], "compile")
+    return obj, stamp
+
+
+def _link_binding(obj, stamp):
+    if obj is None:
+        return
+    import torch
+
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", obj, "-o", tmp,
+          "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda",
+          "-ltorch_python", "-L" + HERE, "-lpagedkv", "-Wl,-rpath,$ORIGIN"], "link")
+    os.replace(tmp, BINDING)
+    with open(BINDING + ".stamp", "w") as f:
+        f.write(stamp)
 
 
 def _build_locked(force, verbose, lib=LIB, build_dir=BUILD, extra=()):

@@ -145,3 +145,18 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
         lib.DeviceTables(t, t[0], t[0, :1], 16)
     with pytest.raises(ValueError):
         lib.DeviceTables.create(4, 16, 2, 2, free_order=[0, 1], device="cpu")
+    d = lib.CacheDesc(lib.PKV_F32, 4, 16, 1, 1, 64)
+    q, k = torch.zeros(1, 1, 64), torch.zeros(4, 1, 16, 64)
+    b, e = torch.zeros((4, 1, 2, 64), dtype=torch.int8), torch.zeros((4, 1), dtype=torch.int8)
+    ctx, sel = torch.ones(1, dtype=torch.int32), torch.zeros((1, 1, 1), dtype=torch.int32)
+    with pytest.raises(TypeError, match="bounds must be a contiguous CUDA"):
+        lib.pkv_block_bounds(b, e, k, d, t[:1], ctx)
+    with pytest.raises(TypeError, match="selected must be a contiguous CUDA"):
+        lib.pkv_select_blocks(sel, q, b, e, d, t[:1], ctx, 16, 0, 1, ws=b)
+    with pytest.raises(TypeError, match="out must be a contiguous CUDA"):
+        lib.paged_attention_sparse(q, q, k, k, d, t[:1], ctx, sel)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        lib.paged_attention_sparse(None, q, k, k, d, t[:1], ctx, sel)
+    hot = lib._native()
+    with pytest.raises(TypeError, match="arguments expected"):
+        hot.attention_sparse(q)
