@@ -177,7 +177,7 @@ struct ListCursor {
 __device__ __forceinline__ ListCursor fetch_tiles(const SparseParams& p, int b, int seq,
                                                   int blocks, int e) {
     ListCursor c{-1, 0};
-    if (e < p.top_k) {
+    if (e < p.top_k && blocks > 0) {             // (a context out of range is flagged as such)
         if (b >= blocks) {
             flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
         } else if (b >= 0) {

@@ -16,8 +16,8 @@ struct QueryRows {
 // Sequence of query token t, found by a whole warp: t itself without
 // query_start_loc, else the last one that starts at or before t; -1 for a token
 // behind the last sequence.  `first` is the sequence's first token, `count` its
-// number of tokens.  A batch of single tokens is answered by one look, others by
-// one more for every factor of 32 in the number of sequences.
+// number of tokens.  A batch of single tokens or of up to 32 sequences is answered
+// by one round of loads, others by one more for every factor of 32 in their number.
 __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int& first,
                                          int& count, int* err) {
     if (!start) {
@@ -26,24 +26,32 @@ __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int
         return t < n ? t : -1;
     }
     const int lane = threadIdx.x & 31;
+    int step = (n + 31) / 32;
+    const int coarse = lane * step < n ? start[lane * step] : INT32_MAX;
     const int total = start[n];
     int lo = min(t, n - 1);
     first = start[lo];
     int next = start[lo + 1];
     if (t >= total) return -1;
     if (t < first || t >= next) {
-        lo = 0;
-        for (int width = n; width > 1;) {        // the sequence is one of lo .. lo + width - 1
-            const int step = (width + 31) / 32;
-            const int at = lo + lane * step;
-            const bool before = lane == 0 || (lane * step < width && start[at] <= t);
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
-            lo += k * step;
-            width = min(step, width - k * step);
+        // (of several sequences that start there, those before the last are empty)
+        lo = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || coarse <= t));
+        first = __shfl_sync(0xffffffffu, coarse, lo);
+        next = __shfl_sync(0xffffffffu, coarse, min(lo + 1, 31));
+        if (lo + 1 >= min(n, 32)) next = total;
+        if (step > 1) {
+            int width = min(step, n - lo * step);
+            lo *= step;
+            while (width > 1) {                  // the sequence is one of lo .. lo + width - 1
+                step = (width + 31) / 32;
+                const bool before = lane == 0 || (lane * step < width && start[lo + lane * step] <= t);
+                const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
+                lo += k * step;
+                width = min(step, width - k * step);
+            }
+            first = start[lo];
+            next = start[lo + 1];
         }
-        // (of several that start there, those before the last are empty)
-        first = start[lo];
-        next = start[lo + 1];
         if (first < 0 || t < first || t >= next) {   // offsets that are not in order
             flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
             return -1;

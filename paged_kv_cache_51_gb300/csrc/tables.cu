@@ -10,12 +10,13 @@
 // before it, at position cached_i + j, slot table[position / bs] * bs +
 // position % bs.
 //
-// The step moves a few hundred KB to a few MB, so it is bound by latency.  A
-// small step is one launch of one cluster (tables_small_kernel): every CTA of it
-// makes the prefix sums for itself and then fills its share of the outputs from
-// them.  A large one takes two: tables_plan_kernel (one CTA) does what is
-// sequential by nature, the checks, both sums and the few new table entries;
-// tables_fill_kernel spreads the copies over the GPU.
+// The step moves a few hundred KB to a few MB, so it is bound by latency.  Where
+// the outputs are not the inputs it is one launch (tables_step_kernel): every CTA
+// makes the prefix sums for itself, so that nothing has to be waited for, and
+// fills its share of the outputs from them.  A step in place, or of very many
+// requests, takes two: tables_plan_kernel (one CTA) does what is sequential by
+// nature, the checks, both sums and the few new table entries; tables_fill_kernel
+// spreads the copies over the GPU.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,13 +24,11 @@
 #include "launch_cache.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
-#include "sparse_common.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr uint32_t kFull = 0xffffffffu;
 // Sums saturate here: needs and tokens of a batch may pass 32 bits, the
 // capacities they are compared with may not.
@@ -54,43 +53,49 @@ struct TablesParams {
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSat); }
 
-// Inclusive saturating scan of one value per thread; `total` is the CTA's sum.
-// (min(a + b, cap) is associative on values of 0 .. cap.)
-__device__ __forceinline__ uint32_t scan_inclusive(uint32_t v, uint32_t* warp_sums,
-                                                   uint32_t& total) {
+// Inclusive saturating scans of two values per thread over a CTA of NT threads;
+// `total_*` are the CTA's sums.  (min(a + b, cap) is associative on 0 .. cap.)
+template <int NT>
+struct ScanScratch {
+    uint32_t a[NT / 32], b[NT / 32];
+};
+template <int NT>
+__device__ __forceinline__ void scan_inclusive(uint32_t& a, uint32_t& b, ScanScratch<NT>& s,
+                                               uint32_t& total_a, uint32_t& total_b) {
+    constexpr int kWarps = NT / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v = sat_add(v, u);
+        const uint32_t u = __shfl_up_sync(kFull, a, o), v = __shfl_up_sync(kFull, b, o);
+        if (lane >= o) a = sat_add(a, u), b = sat_add(b, v);
     }
-    if (lane == 31) warp_sums[warp] = v;
+    if (lane == 31) s.a[warp] = a, s.b[warp] = b;
     __syncthreads();
-    if (warp == 0) {
-        uint32_t w = lane < kPlanWarps ? warp_sums[lane] : 0u;
+    // every warp sums the warps for itself
+    uint32_t wa = lane < kWarps ? s.a[lane] : 0u, wb = lane < kWarps ? s.b[lane] : 0u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(kFull, w, o);
-            if (lane >= o) w = sat_add(w, u);
-        }
-        if (lane < kPlanWarps) warp_sums[lane] = w;
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(kFull, wa, o), v = __shfl_up_sync(kFull, wb, o);
+        if (lane >= o) wa = sat_add(wa, u), wb = sat_add(wb, v);
     }
-    __syncthreads();
-    if (warp > 0) v = sat_add(v, warp_sums[warp - 1]);
-    total = warp_sums[kPlanWarps - 1];
-    __syncthreads();
-    return v;
+    total_a = __shfl_sync(kFull, wa, kWarps - 1);
+    total_b = __shfl_sync(kFull, wb, kWarps - 1);
+    const uint32_t pa = __shfl_sync(kFull, wa, max(warp - 1, 0)), pb = __shfl_sync(kFull, wb, max(warp - 1, 0));
+    if (warp > 0) a = sat_add(a, pa), b = sat_add(b, pb);
+    __syncthreads();                              // (the scratch may be written again)
 }
 
 // Marks the rows that the batch names more than once: two bit planes over
-// max_seqs rows in shared memory, `seen` and `twice`.
-__device__ __forceinline__ void mark_rows(const int32_t* rows, int n, int max_seqs,
+// max_seqs rows in shared memory, `seen` and `twice`.  `mine` is this thread's
+// first row, which it has loaded already.
+template <int NT>
+__device__ __forceinline__ void mark_rows(const int32_t* rows, int mine, int n, int max_seqs,
                                           uint32_t* seen, uint32_t* twice) {
     const int words = (max_seqs + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += kPlanThreads) seen[i] = twice[i] = 0u;
+    for (int i = threadIdx.x; i < words; i += NT) seen[i] = twice[i] = 0u;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-        const int r = rows[i];
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const int r = i < NT ? mine : rows[i];
         if (r < 0 || r >= max_seqs) continue;
         const uint32_t bit = 1u << (r & 31);
         if (atomicOr(seen + (r >> 5), bit) & bit) atomicOr(twice + (r >> 5), bit);
@@ -98,12 +103,10 @@ __device__ __forceinline__ void mark_rows(const int32_t* rows, int n, int max_se
     __syncthreads();
 }
 
-__device__ __forceinline__ int row_of(const int32_t* rows, int i, int max_seqs,
-                                      const uint32_t* twice) {
-    if (!rows) return i < max_seqs ? i : -1;
-    const int r = rows[i];
+// The row that request i names, if it is one and named once; else -1.
+__device__ __forceinline__ int checked_row(int r, bool listed, int max_seqs, const uint32_t* twice) {
     if (r < 0 || r >= max_seqs) return -1;
-    return twice[r >> 5] >> (r & 31) & 1u ? -1 : r;
+    return listed && (twice[r >> 5] >> (r & 31) & 1u) ? -1 : r;
 }
 
 __device__ __forceinline__ int64_t blocks_of(int64_t tokens, int bs) {
@@ -115,6 +118,19 @@ struct StepSums {
     uint32_t need_base = 0, tok_base = 0;         // of the requests before this pass
     uint32_t used = 0, placed = 0;                // of the served ones
 };
+// Request i as the caller gave it.
+struct Given {
+    int row, cached, fresh;
+};
+__device__ __forceinline__ Given load_request(const TablesParams& p, int i) {
+    Given g{-1, 0, 0};
+    if (i < p.n) {
+        g.row = p.seq_rows ? p.seq_rows[i] : i;
+        g.cached = p.cached[i];
+        g.fresh = p.fresh ? p.fresh[i] : 1;
+    }
+    return g;
+}
 struct Request {
     int row, cached, fresh;
     uint32_t need_in, tok_in;                     // sums that include it
@@ -125,15 +141,17 @@ struct Request {
 // One pass: request `i` of this thread, checked and summed.  Served in order up
 // to the first request that does not fit: both sums only grow, so no later
 // request fits either.
-__device__ __forceinline__ Request plan_pass(const TablesParams& p, int i, const uint32_t* twice,
-                                             uint32_t have, int64_t limit, uint32_t* warp_sums,
+template <int NT>
+__device__ __forceinline__ Request plan_pass(const TablesParams& p, int i, Given g,
+                                             const uint32_t* twice,
+                                             uint32_t have, int64_t limit, ScanScratch<NT>& scratch,
                                              StepSums& s, int* tell) {
     Request r{-1, 0, 0, 0, 0, 0, 0, false, false};
-    uint32_t need = 0;
+    uint32_t need = 0, tok = 0;
     if (i < p.n) {
-        r.row = row_of(p.seq_rows, i, p.max_seqs, twice);
-        r.cached = p.cached[i];
-        r.fresh = p.fresh ? p.fresh[i] : 1;
+        r.row = checked_row(g.row, p.seq_rows != nullptr, p.max_seqs, twice);
+        r.cached = g.cached;
+        r.fresh = g.fresh;
         if (r.row < 0) {
             flag_error(tell, PKV_DEV_BAD_SEQ_ROW);
         } else if (r.cached < 0 || r.fresh < 0) {
@@ -144,26 +162,24 @@ __device__ __forceinline__ Request plan_pass(const TablesParams& p, int i, const
             r.ok = true;
             need = uint32_t(blocks_of(int64_t(r.cached) + r.fresh, p.block_size) -
                             blocks_of(r.cached, p.block_size));
+            tok = min(uint32_t(r.fresh), kSat);
         }
     }
-    const uint32_t tok = r.ok ? min(uint32_t(r.fresh), kSat) : 0u;
-    r.need_in = sat_add(s.need_base, scan_inclusive(need, warp_sums, r.need_sum));
-    r.tok_in = sat_add(s.tok_base, scan_inclusive(tok, warp_sums, r.tok_sum));
+    scan_inclusive<NT>(need, tok, scratch, r.need_sum, r.tok_sum);
+    r.need_in = sat_add(s.need_base, need);
+    r.tok_in = sat_add(s.tok_base, tok);
     const bool fits = r.need_in <= have && r.tok_in <= uint32_t(p.max_tokens);
     r.served = r.ok && fits;
     if (r.ok && !fits)
         flag_error(tell, r.need_in > have ? PKV_DEV_NO_FREE_BLOCKS : PKV_DEV_BAD_QUERY_LAYOUT);
     // the sums of served requests: the largest, over the CTA
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t u = __reduce_max_sync(kFull, r.served ? r.need_in : 0u);
     const uint32_t q = __reduce_max_sync(kFull, r.served ? r.tok_in : 0u);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) warp_sums[warp] = u;
+    if (lane == 0) scratch.a[warp] = u, scratch.b[warp] = q;
     __syncthreads();
-    s.used = max(s.used, __reduce_max_sync(kFull, warp_sums[lane]));
-    __syncthreads();
-    if (lane == 0) warp_sums[warp] = q;
-    __syncthreads();
-    s.placed = max(s.placed, __reduce_max_sync(kFull, warp_sums[lane]));
+    s.used = max(s.used, __reduce_max_sync(kFull, scratch.a[lane % (NT / 32)]));
+    s.placed = max(s.placed, __reduce_max_sync(kFull, scratch.b[lane % (NT / 32)]));
     __syncthreads();
     return r;
 }
@@ -188,16 +204,18 @@ __device__ __forceinline__ int64_t token_limit(const TablesParams& p) {
 
 __global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(TablesParams p) {
     extern __shared__ uint32_t bits[];            // two planes of max_seqs bits
-    __shared__ uint32_t warp_sums[kPlanWarps];
+    __shared__ ScanScratch<kPlanThreads> scratch;
     __shared__ uint32_t need_end[kPlanThreads];   // inclusive needs of the pass's served requests
     __shared__ int32_t dest[kPlanThreads];        // first new table entry of a request ...
     __shared__ int32_t dest_row[kPlanThreads];    // ... in this row
     const uint32_t* twice = bits + (p.max_seqs + 31) / 32;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    if (p.seq_rows)
-        mark_rows(p.seq_rows, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
     const int free0 = *p.free_count;
+    const Given given = load_request(p, threadIdx.x);
+    if (p.seq_rows)
+        mark_rows<kPlanThreads>(p.seq_rows, given.row, p.n, p.max_seqs, bits,
+                                bits + (p.max_seqs + 31) / 32);
     bool free_ok;
     const uint32_t have = free_blocks(p, free0, free_ok);
     if (!free_ok && threadIdx.x == 0) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
@@ -206,7 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(TablesParams 
     StepSums s;
     for (int base = 0; base < p.n; base += kPlanThreads) {
         const int i = base + threadIdx.x;
-        const Request r = plan_pass(p, i, twice, have, limit, warp_sums, s, p.err);
+        const Request r = plan_pass<kPlanThreads>(p, i, base ? load_request(p, i) : given, twice, have, limit, scratch, s, p.err);
         if (i < p.n) {
             p.ctx[i] = r.ok ? r.cached + (r.served ? r.fresh : 0) : 0;
             p.start[i + 1] = int32_t(min(r.tok_in, s.placed));
@@ -296,41 +314,41 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(TablesParams 
     if (p.positions) p.positions[t] = pos;
 }
 
-constexpr int kSmallSeqs = 2048;  // requests of a step in one launch
-constexpr int kSmallCtas = 8;     // CTAs of its cluster
-constexpr int64_t kSmallWork = 1 << 18;   // most table entries and tokens of one launch
+constexpr int kStepSeqs = 2048;   // most requests of a step in one launch
 
-// A step in one launch of one cluster.  Every CTA checks and sums all requests
-// and keeps what the outputs are made of in shared memory; then the CTAs fill the
-// outputs side by side.  Inputs may be outputs too (lengths and count in place):
-// they are written once every CTA of the cluster has read them.
-__global__ void __launch_bounds__(kPlanThreads) tables_small_kernel(TablesParams p, int segments,
-                                                                    int copy_warps) {
-    extern __shared__ uint32_t bits[];            // two planes of max_seqs bits
-    __shared__ uint32_t warp_sums[kPlanWarps];
-    __shared__ int32_t row[kSmallSeqs];           // -1: refused
-    __shared__ int32_t old_blocks[kSmallSeqs];    // blocks held, and with the new ones
-    __shared__ int32_t now_blocks[kSmallSeqs];
-    __shared__ uint32_t before[kSmallSeqs];       // new blocks of the requests in front
-    __shared__ int32_t start[kSmallSeqs + 1], ctx[kSmallSeqs];
+// A step in one launch, for outputs that are not inputs.  Every CTA checks and
+// sums all requests and keeps what the outputs are made of in shared memory; then
+// the CTAs fill the outputs side by side.  What another CTA writes is never read:
+// a new entry is taken from the free list wherever it is needed.
+template <int NT>
+__global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int segments, int copy_warps) {
+    extern __shared__ uint32_t dyn[];             // 6 n + 1 words, then two planes of max_seqs bits
+    __shared__ ScanScratch<NT> scratch;
+    int32_t* row = reinterpret_cast<int32_t*>(dyn);    // -1: refused
+    int32_t* old_blocks = row + p.n;              // blocks held, and with the new ones
+    int32_t* now_blocks = old_blocks + p.n;
+    uint32_t* before = reinterpret_cast<uint32_t*>(now_blocks + p.n);   // new blocks in front
+    int32_t* ctx = reinterpret_cast<int32_t*>(before + p.n);
+    int32_t* start = ctx + p.n;
+    uint32_t* bits = dyn + 6 * p.n + 1;
     const uint32_t* twice = bits + (p.max_seqs + 31) / 32;
-    const int rank = int(cluster_rank());
-    int* const tell = rank == 0 ? p.err : nullptr;
+    int* const tell = blockIdx.x == 0 ? p.err : nullptr;
     const int lane = threadIdx.x & 31;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    if (p.seq_rows)
-        mark_rows(p.seq_rows, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
     const int free0 = *p.free_count;
+    const Given given = load_request(p, threadIdx.x);
+    if (p.seq_rows)
+        mark_rows<NT>(p.seq_rows, given.row, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
     bool free_ok;
     const uint32_t have = free_blocks(p, free0, free_ok);
     if (!free_ok && threadIdx.x == 0) flag_error(tell, PKV_DEV_BAD_BLOCK_ID);
     const int64_t limit = token_limit(p);
     StepSums s;
     if (threadIdx.x == 0) start[0] = 0;
-    for (int base = 0; base < p.n; base += kPlanThreads) {
+    for (int base = 0; base < p.n; base += NT) {
         const int i = base + threadIdx.x;
-        const Request r = plan_pass(p, i, twice, have, limit, warp_sums, s, tell);
+        const Request r = plan_pass<NT>(p, i, base ? load_request(p, i) : given, twice, have, limit, scratch, s, tell);
         if (i < p.n) {
             const int held = r.ok ? int(blocks_of(r.cached, p.block_size)) : 0;
             ctx[i] = r.ok ? r.cached + (r.served ? r.fresh : 0) : 0;
@@ -343,30 +361,14 @@ __global__ void __launch_bounds__(kPlanThreads) tables_small_kernel(TablesParams
         s.need_base = sat_add(s.need_base, r.need_sum);
         s.tok_base = sat_add(s.tok_base, r.tok_sum);
     }
-    cluster_sync();                               // (all inputs are read; shared memory is filled)
-    if (rank == 0) {
-        for (int i = threadIdx.x; i < p.n; i += kPlanThreads) p.ctx[i] = ctx[i];
-        for (int i = threadIdx.x; i <= p.n; i += kPlanThreads) p.start[i] = start[i];
-        if (threadIdx.x == 0) *p.free_count_out = free_ok ? int32_t(have - s.used) : free0;
-    }
+    __syncthreads();
     // block j of request i, as the step leaves it
     auto block = [&](int i, int j, int* flag) {
         if (j >= old_blocks[i]) return take_block(p, have, before[i] + (j - old_blocks[i]), flag);
         return p.table[size_t(row[i]) * p.max_blocks + j];
     };
-    // new entries of the state, one thread each: the request by bisection
-    for (uint32_t b = rank * kPlanThreads + threadIdx.x; b < s.used; b += kSmallCtas * kPlanThreads) {
-        int lo = 0, hi = p.n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (before[mid] + (now_blocks[mid] - old_blocks[mid]) > b) hi = mid;
-            else lo = mid + 1;
-        }
-        p.table[size_t(row[lo]) * p.max_blocks + old_blocks[lo] + (b - before[lo])] =
-            take_block(p, have, b, p.err);
-    }
-    const int warps = kSmallCtas * kPlanWarps;
-    for (int w = rank * kPlanWarps + (threadIdx.x >> 5); w < copy_warps; w += warps) {
+    const int warps = int(gridDim.x) * (NT / 32), first = int(blockIdx.x) * (NT / 32) + (threadIdx.x >> 5);
+    for (int w = first; w < copy_warps; w += warps) {
         const int i = w / segments, j0 = (w % segments) * kSegment;
         int32_t* dst = p.out_tables + size_t(i) * p.width + j0;
         int32_t v[kSegment / 32];
@@ -381,12 +383,30 @@ __global__ void __launch_bounds__(kPlanThreads) tables_small_kernel(TablesParams
             if (j0 + j < p.width) dst[j] = v[k];
         }
     }
-    const int total = p.n ? start[p.n] : 0;
-    for (int t = rank * kPlanThreads + threadIdx.x; t < p.max_tokens; t += kSmallCtas * kPlanThreads) {
+    const int threads = int(gridDim.x) * NT, me = int(blockIdx.x) * NT + threadIdx.x;
+    for (int i = me; i <= p.n; i += threads) {
+        if (i < p.n) p.ctx[i] = ctx[i];
+        p.start[i] = start[i];
+    }
+    if (me == 0) *p.free_count_out = free_ok ? int32_t(have - s.used) : free0;
+    // new entries of the state, one thread each: the request by bisection
+    for (uint32_t b = me; b < s.used; b += threads) {
+        int lo = 0, hi = p.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] + (now_blocks[mid] - old_blocks[mid]) > b) hi = mid;
+            else lo = mid + 1;
+        }
+        p.table[size_t(row[lo]) * p.max_blocks + old_blocks[lo] + (b - before[lo])] =
+            take_block(p, have, b, p.err);
+    }
+    const int total = start[p.n];
+    for (int t = me; t < p.max_tokens; t += threads) {
         int64_t slot = -1;
         int pos = 0;
         if (t < total) {
             int lo = 0, hi = p.n - 1;
+            if (t < p.n && start[t] <= t && t < start[t + 1]) lo = hi = t;   // a decode batch
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
                 if (start[mid + 1] > t) hi = mid;
@@ -416,14 +436,15 @@ struct ReleaseParams {
 // request in table order, and their table entries are set to -1.
 __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleaseParams p) {
     extern __shared__ uint32_t bits[];
-    __shared__ uint32_t warp_sums[kPlanWarps];
+    __shared__ ScanScratch<kPlanThreads> scratch;
     __shared__ uint32_t end[kPlanThreads];
     __shared__ int32_t rows[kPlanThreads];
     const uint32_t* twice = bits + (p.max_seqs + 31) / 32;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     if (p.seq_rows)
-        mark_rows(p.seq_rows, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
+        mark_rows<kPlanThreads>(p.seq_rows, int(threadIdx.x) < p.n ? p.seq_rows[threadIdx.x] : -1,
+                                p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
     const int free0 = *p.free_count;
     const bool free_ok = free0 >= 0 && free0 <= p.num_blocks;
     const uint32_t room = free_ok ? uint32_t(p.num_blocks - free0) : 0u;
@@ -435,7 +456,7 @@ __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleasePar
         uint32_t blocks = 0;
         int row = -1;
         if (i < p.n) {
-            row = row_of(p.seq_rows, i, p.max_seqs, twice);
+            row = checked_row(p.seq_rows ? p.seq_rows[i] : i, p.seq_rows != nullptr, p.max_seqs, twice);
             const int len = p.lens[i];
             if (row < 0) {
                 flag_error(p.err, PKV_DEV_BAD_SEQ_ROW);
@@ -449,15 +470,16 @@ __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleasePar
                 else blocks = uint32_t(blocks_of(len, p.block_size));
             }
         }
-        uint32_t sum;
-        const uint32_t incl = sat_add(base_sum, scan_inclusive(blocks, warp_sums, sum));
+        uint32_t in_pass = blocks, none = 0, sum, none_sum;
+        scan_inclusive<kPlanThreads>(in_pass, none, scratch, sum, none_sum);
+        const uint32_t incl = sat_add(base_sum, in_pass);
         if (blocks && incl > room) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
         // more blocks than the pool has: the stack takes no request past its end
         const uint32_t got = blocks && incl <= room ? incl : 0u;
         top = max(top, __reduce_max_sync(kFull, got));
         if ((threadIdx.x & 31) == 0) end[threadIdx.x >> 5] = top;
         __syncthreads();
-        for (int w = 0; w < kPlanWarps; ++w) top = max(top, end[w]);
+        for (int w = 0; w < kPlanThreads / 32; ++w) top = max(top, end[w]);
         __syncthreads();
         end[threadIdx.x] = min(incl, top);
         rows[threadIdx.x] = row;
@@ -502,6 +524,19 @@ int check_tables_pointers(const pkv_device_tables* t) {
 }
 
 int plane_bytes(int max_seqs) { return 2 * ((max_seqs + 31) / 32) * 4; }
+
+template <int NT>
+int launch_step(const TablesParams& p, int segments, int64_t copy_warps, int planes, cudaStream_t s) {
+    const int fixed = (6 * kStepSeqs + 1) * 4;
+    if (kernel_occupancy<tables_step_kernel<NT>>(NT, fixed + plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
+        return PKV_ERR_CUDA;
+    const int64_t warps = std::max<int64_t>(copy_warps, ceil_div(p.max_tokens, 32));
+    const int64_t ctas = std::max<int64_t>(
+        1, std::min<int64_t>((warps + NT / 32 - 1) / (NT / 32), 1024 / NT * int64_t(num_sms())));
+    return cuda_status(launch_pdl(tables_step_kernel<NT>, dim3(unsigned(ctas)), dim3(NT),
+                                  size_t((6 * p.n + 1) * 4 + planes), s, p, segments,
+                                  int(copy_warps)));
+}
 
 }  // namespace
 }  // namespace pkv
@@ -555,29 +590,15 @@ extern "C" int pkv_tables_step(const pkv_device_tables* tables, const int32_t* s
     p.width = max_blocks_per_seq;
     p.max_tokens = max_tokens;
     const int smem = seq_rows ? plane_bytes(p.max_seqs) : 0;
-    if (num_seqs <= kSmallSeqs && copy_warps * kSegment + max_tokens <= kSmallWork) {
-        if (kernel_occupancy<tables_small_kernel>(kPlanThreads, plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
-            return PKV_ERR_CUDA;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kSmallCtas);
-        cfg.blockDim = dim3(kPlanThreads);
-        cfg.dynamicSmemBytes = size_t(smem);
-        cfg.stream = static_cast<cudaStream_t>(stream);
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = kSmallCtas;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        return cuda_status(
-            cudaLaunchKernelEx(&cfg, tables_small_kernel, p, segments, int(copy_warps)));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // one launch where nothing is written that the other CTAs still read
+    if (num_seqs <= kStepSeqs && context_lens != cached_lens &&
+        p.free_count_out != tables->free_count) {
+        return num_seqs <= 256 ? launch_step<256>(p, segments, copy_warps, smem, cs)
+                               : launch_step<1024>(p, segments, copy_warps, smem, cs);
     }
     if (kernel_occupancy<tables_plan_kernel>(kPlanThreads, plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
         return PKV_ERR_CUDA;
-    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     st = cuda_status(launch_pdl(tables_plan_kernel, dim3(1), dim3(kPlanThreads), size_t(smem), cs, p));
     if (st != PKV_OK || warps == 0) return st;
     const int64_t ctas = (warps + kFillThreads / 32 - 1) / (kFillThreads / 32);

@@ -48,10 +48,25 @@ def _same_state(dt, model):
     assert dt.free_list[:n].cpu().tolist() == model.free
 
 
+# in place the step is two launches, with a count of its own one (up to 2048 requests)
+IN_PLACE = pytest.mark.parametrize("in_place", [True, False])
+
+
+def _count(dt, in_place):
+    return {} if in_place else dict(free_count_out=torch.full_like(dt.free_count, -3))
+
+
+def _settle(dt, kw):
+    """The caller takes over a count that was written apart."""
+    if kw:
+        dt.free_count.copy_(kw["free_count_out"])
+
+
+@IN_PLACE
 @pytest.mark.parametrize("bs,rows,width,chunk,seed", [(16, 40, 9, 40, 0), (4, 12, 70, 3, 1),
                                                       (1, 5, 64, 20, 2), (16, 3000, 5, 18, 3),
-                                                      (7, 33, 257, 600, 4)])
-def test_random_steps_and_releases_match_the_model(pkv, bs, rows, width, chunk, seed):
+                                                      (7, 33, 257, 600, 4), (16, 900, 300, 70, 5)])
+def test_random_steps_and_releases_match_the_model(pkv, bs, rows, width, chunk, seed, in_place):
     rng = np.random.default_rng(seed)
     nb = rows * max(2, min(width, 2 * chunk // bs + 2))
     order = rng.permutation(nb)
@@ -76,7 +91,9 @@ def test_random_steps_and_releases_match_the_model(pkv, bs, rows, width, chunk, 
         tokens = int(new.sum()) + int(rng.integers(0, 40))
         step = Step(len(pick), tokens, width)
         ref = model.step(pick, lens[pick], new, tokens, width)
-        step.call(pkv, dt, i32(pick), i32(lens[pick]), None if it % 3 == 0 else i32(new))
+        kw = _count(dt, in_place)
+        step.call(pkv, dt, i32(pick), i32(lens[pick]), None if it % 3 == 0 else i32(new), **kw)
+        _settle(dt, kw)
         step.check(*ref)
         _same_state(dt, model)
         lens[pick] += new
@@ -116,13 +133,16 @@ def test_a_separate_count_leaves_the_step_repeatable(pkv):
         assert torch.equal(a, b)
 
 
-def test_requests_that_do_not_fit_wait(pkv):
+@IN_PLACE
+def test_requests_that_do_not_fit_wait(pkv, in_place):
     """Blocks, then token rows, run out: the rest of the batch waits and is served
     after a release."""
     model, dt = sparse.TablesModel(6, 4, 5, 4), pkv.DeviceTables.create(6, 4, 5, 4)
     rows, cached, new = [4, 0, 2, 1, 3], [0] * 5, [8, 9, 5, 0, 1]     # 2 + 3 + 2 ... blocks
     ref = model.step(rows, cached, new, 30, 4)
-    s = Step(5, 30, 4).call(pkv, dt, i32(rows), i32(cached), i32(new))
+    kw = _count(dt, in_place)
+    s = Step(5, 30, 4).call(pkv, dt, i32(rows), i32(cached), i32(new), **kw)
+    _settle(dt, kw)
     assert pkv.device_error() == 10                                   # PKV_DEV_NO_FREE_BLOCKS
     s.check(*ref)
     assert ref[0].tolist() == [8, 9, 0, 0, 0]
@@ -130,37 +150,45 @@ def test_requests_that_do_not_fit_wait(pkv):
     pkv.pkv_tables_release(dt, i32([4]), i32([8]))
     model.release([4], [8])
     ref = model.step([2, 3], [0, 0], [5, 1], 5, 4)                    # the last token has no room
-    s = Step(2, 5, 4).call(pkv, dt, i32([2, 3]), i32([0, 0]), i32([5, 1]))
+    kw = _count(dt, in_place)
+    s = Step(2, 5, 4).call(pkv, dt, i32([2, 3]), i32([0, 0]), i32([5, 1]), **kw)
+    _settle(dt, kw)
     assert pkv.device_error() == 5                                    # PKV_DEV_BAD_QUERY_LAYOUT
     s.check(*ref)
     assert ref[0].tolist() == [5, 0]
     _same_state(dt, model)
 
 
+@IN_PLACE
 @pytest.mark.parametrize("rows,cached,new,code", [
     ([0, 9, 2], [0, 0, 0], [3, 3, 3], 9), ([0, -1, 2], [0, 0, 0], [3, 3, 3], 9),
     ([2, 0, 2], [0, 0, 0], [3, 3, 3], 9), ([0, 1, 2], [0, -4, 0], [3, 3, 3], 2),
     ([0, 1, 2], [0, 0, 0], [3, -3, 3], 2), ([0, 1, 2], [0, 0, 0], [3, 17, 3], 7),
     ([0, 1, 2], [0, 2**31 - 1, 0], [3, 2**31 - 1, 3], 7),
 ])
-def test_bad_requests_are_skipped_and_flagged(pkv, rows, cached, new, code):
+def test_bad_requests_are_skipped_and_flagged(pkv, rows, cached, new, code, in_place):
     model, dt = sparse.TablesModel(12, 4, 4, 4), pkv.DeviceTables.create(12, 4, 4, 4)
     ref = model.step(rows, cached, new, 12, 4)
-    s = Step(3, 12, 4).call(pkv, dt, i32(rows), i32(cached), i32(new))
+    kw = _count(dt, in_place)
+    s = Step(3, 12, 4).call(pkv, dt, i32(rows), i32(cached), i32(new), **kw)
+    _settle(dt, kw)
     assert pkv.device_error() == code
     s.check(*ref)
     _same_state(dt, model)
 
 
-def test_bad_free_list_and_count(pkv):
+@IN_PLACE
+def test_bad_free_list_and_count(pkv, in_place):
     dt = pkv.DeviceTables.create(4, 4, 2, 4, free_order=[0, 1, 2, 3])
     dt.free_count.fill_(9)
-    s = Step(1, 4, 4).call(pkv, dt, i32([0]), i32([0]), i32([4]))
+    kw = _count(dt, in_place)
+    s = Step(1, 4, 4).call(pkv, dt, i32([0]), i32([0]), i32([4]), **kw)
+    _settle(dt, kw)
     assert pkv.device_error() == 1                                    # PKV_DEV_BAD_BLOCK_ID
     assert s.ctx.tolist() == [0] and dt.free_count.item() == 9
     dt.free_count.fill_(4)
     dt.free_list[3] = 55
-    s = Step(1, 4, 4).call(pkv, dt, i32([0]), i32([0]), i32([4]))
+    s = Step(1, 4, 4).call(pkv, dt, i32([0]), i32([0]), i32([4]), **_count(dt, in_place))
     assert pkv.device_error() == 1
     assert s.slots.tolist() == [-1] * 4                               # appends skip them
 
