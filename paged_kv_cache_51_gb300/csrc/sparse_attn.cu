@@ -6,10 +6,10 @@
 // pool, and nothing is read twice, so the work is bound by HBM for a batch and
 // by latency for a few rows.  A cluster of CTAs shares one (row, head): the
 // listed blocks go round the cluster's warps, every warp keeps a running
-// (max, sum, output) of its own and a ring of tiles that it fills with
-// asynchronous copies itself, so that no warp waits for another before the end;
-// the states are then merged inside the CTA and, through distributed shared
-// memory, across the cluster, in a fixed order and without a workspace.
+// (max, sum, output) and tiles of its own that it fills with asynchronous copies
+// itself, so that no warp waits for another before the end; the states are then
+// merged inside the CTA and, through distributed shared memory, across the
+// cluster, in a fixed order and without a workspace.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -48,15 +48,13 @@ struct Inbox {
     static constexpr int kFloats = kMaxG * D + kMaxCluster * kStats;
 };
 
-template <typename T, int D, int G>
-struct SparseCfg {
+template <int D, int G>
+struct SparseF32Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kTileBytes = kBlockTokens * D * int(sizeof(T));
+    static constexpr int kTileBytes = kBlockTokens * D * 4;
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kStages = sizeof(T) == 2 && D == 128 ? 3 : D == 64 ? 4 : 2;
-    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-    static constexpr int kQOff = kRingBytes;                          // q as fp32 [G][D]
+    static constexpr int kQOff = kWarps * kStageBytes;                // q as fp32 [G][D]
     static constexpr int kPOff = kQOff + G * D * 4;                   // weights [warp][G][16]
     static constexpr int kRec = record_floats(G, D);
     static constexpr int kCombOff = kPOff + kWarps * G * kBlockTokens * 4;
@@ -67,22 +65,6 @@ struct SparseCfg {
 // 16-byte chunk c of tile row r, so that the reads of eight lanes (four rows,
 // two neighbouring chunks) fall into eight different bank groups
 __device__ __forceinline__ int chunk_at(int r, int c) { return c ^ ((r & 3) << 1); }
-
-template <typename T>
-__device__ __forceinline__ void widen16(const void* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-}
 
 // Merge the CTA's warp states (records in shared memory), then the cluster's,
 // and write the outputs of the (row, head): shared by every variant.  Each CTA
@@ -189,11 +171,14 @@ __device__ __forceinline__ ListCursor fetch_tiles(const SparseParams& p, int b, 
     return c;
 }
 
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kernel(SparseParams p) {
-    using C = SparseCfg<T, D, G>;
-    constexpr int V = 16 / int(sizeof(T));       // elements of a 16-byte chunk
-    constexpr int RC = D / V;                    // chunks of a row
+// On CUDA cores (fp32 caches).  A warp holds one tile at a time: the products are
+// long next to its copy, and three or more CTAs on an SM hide one warp's copy
+// behind the others' products better than a ring of tiles in one CTA does (105 x
+// 40 blocks, groups of 4, 64 dimensions: 75 us, 145 us with four tiles a warp).
+template <int D, int G>
+__global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_kernel(SparseParams p) {
+    using C = SparseF32Cfg<D, G>;
+    constexpr int RC = D / 4;                    // 16-byte chunks of a row
     constexpr int DL = D / 32;                   // output dimensions of a lane
     extern __shared__ __align__(128) unsigned char smem[];
     float* qs = reinterpret_cast<float*>(smem + C::kQOff);
@@ -218,43 +203,14 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
     }
     const int blocks = (keys + kBlockTokens - 1) / kBlockTokens;
     for (int i = threadIdx.x; i < G * D; i += C::kThreads)
-        qs[i] = float(static_cast<const T*>(p.q)[(size_t(t) * p.num_q_heads + size_t(h) * G) * D + i]);
+        qs[i] = static_cast<const float*>(p.q)[(size_t(t) * p.num_q_heads + size_t(h) * G) * D + i];
     __syncthreads();
 
     const int tiles = p.top_k > first ? (p.top_k - first + stride - 1) / stride : 0;
-    unsigned char* ring = smem + warp * (C::kStages * C::kStageBytes);
-    const uint32_t ring_u = smem_u32(ring);
+    unsigned char* kt = smem + warp * C::kStageBytes;
+    unsigned char* vt = kt + C::kTileBytes;
     float* ps = reinterpret_cast<float*>(smem + C::kPOff) + warp * (G * kBlockTokens);
-
-    auto fetch = [&](int j) {
-        const int e = first + (j + lane) * stride;
-        return fetch_tiles(p, j ? (e < p.top_k ? list[e] : -1) : entry0, seq, blocks, e);
-    };
-    ListCursor next{-1, 0}, now{-1, 0};          // tiles being requested, tiles being used
-    auto request = [&](int j) {
-        if (j < tiles) {
-            if (j % 32 == 0) next = fetch(j);
-            const int id = __shfl_sync(kFull, next.phys, j % 32);
-            if (id >= 0) {
-                const size_t off = (size_t(id) * p.num_kv_heads + h) * (kBlockTokens * D);
-                const T* ks = static_cast<const T*>(p.k_cache) + off;
-                const T* vs = static_cast<const T*>(p.v_cache) + off;
-                const uint32_t dst = ring_u + (j % C::kStages) * C::kStageBytes;
-                // rows past the row's keys are zero (they may hold anything; 0 x NaN is NaN)
-                const int live = keys - __shfl_sync(kFull, next.logical, j % 32) * kBlockTokens;
-#pragma unroll
-                for (int i = 0; i < kBlockTokens * RC / 32; ++i) {
-                    const int idx = i * 32 + lane, r = idx / RC, c = idx % RC;
-                    const uint32_t at = dst + (r * RC + chunk_at(r, c)) * 16;
-                    cp_async16(at, ks + idx * V, r < live);
-                    cp_async16(at + C::kTileBytes, vs + idx * V, r < live);
-                }
-            }
-        }
-        cp_commit();
-    };
-    for (int j = 0; j < C::kStages - 1; ++j) request(j);
-    const ListCursor now0 = next;
+    ListCursor now{-1, 0};
 
     float o[G][DL], m[G], l[G];
 #pragma unroll
@@ -267,15 +223,29 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
     int seen = 0;
     const int key = lane >> 1, half = lane & 1;
     for (int j = 0; j < tiles; ++j) {
-        request(j + C::kStages - 1);
-        if (j % 32 == 0) now = j ? fetch(j) : now0;
+        if (j % 32 == 0) {
+            const int e = first + (j + lane) * stride;
+            now = fetch_tiles(p, j ? (e < p.top_k ? list[e] : -1) : entry0, seq, blocks, e);
+        }
         const int id = __shfl_sync(kFull, now.phys, j % 32);
         const int b = __shfl_sync(kFull, now.logical, j % 32);
-        cp_wait<C::kStages - 1>();
-        __syncwarp();
         if (id < 0) continue;
-        const unsigned char* kt = ring + (j % C::kStages) * C::kStageBytes;
-        const unsigned char* vt = kt + C::kTileBytes;
+        const size_t off = (size_t(id) * p.num_kv_heads + h) * (kBlockTokens * D);
+        const float* ks = static_cast<const float*>(p.k_cache) + off;
+        const float* vs = static_cast<const float*>(p.v_cache) + off;
+        // rows past the row's keys are zero (they may hold anything; 0 x NaN is NaN)
+        const int live = keys - b * kBlockTokens;
+        const uint32_t dst = smem_u32(kt);
+#pragma unroll
+        for (int i = 0; i < kBlockTokens * RC / 32; ++i) {
+            const int idx = i * 32 + lane, r = idx / RC, c = idx % RC;
+            const uint32_t at = dst + (r * RC + chunk_at(r, c)) * 16;
+            cp_async16(at, ks + idx * 4, r < live);
+            cp_async16(at + C::kTileBytes, vs + idx * 4, r < live);
+        }
+        cp_commit();
+        cp_wait<0>();
+        __syncwarp();
         const int nvalid = min(kBlockTokens, keys - b * kBlockTokens);
         seen += nvalid;
         // scores: two lanes a key, chunks taken in turn
@@ -285,12 +255,15 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
 #pragma unroll
         for (int i = 0; i < RC / 2; ++i) {
             const int c = 2 * i + half;
-            float x[V];
-            widen16<T>(kt + (key * RC + chunk_at(key, c)) * 16, x);
+            const float4 x = *reinterpret_cast<const float4*>(kt + (key * RC + chunk_at(key, c)) * 16);
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int e = 0; e < V; ++e) s[g] = fmaf(x[e], qs[g * D + c * V + e], s[g]);
+            for (int g = 0; g < G; ++g) {
+                const float4 qv = *reinterpret_cast<const float4*>(qs + g * D + c * 4);
+                s[g] = fmaf(x.x, qv.x, s[g]);
+                s[g] = fmaf(x.y, qv.y, s[g]);
+                s[g] = fmaf(x.z, qv.z, s[g]);
+                s[g] = fmaf(x.w, qv.w, s[g]);
+            }
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -309,20 +282,30 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
             if (!half) ps[g * kBlockTokens + key] = w;
         }
         __syncwarp();
+        // four keys at a time, their weights in one load a head
 #pragma unroll
-        for (int k = 0; k < kBlockTokens; ++k) {
-            float v[DL];
-            const int byte = lane * DL * int(sizeof(T));
-            const unsigned char* src = vt + (k * RC + chunk_at(k, byte / 16)) * 16 + byte % 16;
-            Elem<T>::load(reinterpret_cast<const T*>(src), v);
+        for (int k = 0; k < kBlockTokens; k += 4) {
+            float v[4][DL];
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+            for (int e = 0; e < 4; ++e) {
+                const int byte = lane * DL * 4;
+                const unsigned char* src = vt + ((k + e) * RC + chunk_at(k + e, byte / 16)) * 16 + byte % 16;
+                Elem<float>::load(reinterpret_cast<const float*>(src), v[e]);
+            }
 #pragma unroll
-                for (int d = 0; d < DL; ++d) o[g][d] = fmaf(ps[g * kBlockTokens + k], v[d], o[g][d]);
+            for (int g = 0; g < G; ++g) {
+                const float4 w = *reinterpret_cast<const float4*>(ps + g * kBlockTokens + k);
+#pragma unroll
+                for (int d = 0; d < DL; ++d) {
+                    o[g][d] = fmaf(w.x, v[0][d], o[g][d]);
+                    o[g][d] = fmaf(w.y, v[1][d], o[g][d]);
+                    o[g][d] = fmaf(w.z, v[2][d], o[g][d]);
+                    o[g][d] = fmaf(w.w, v[3][d], o[g][d]);
+                }
+            }
         }
         __syncwarp();
     }
-    cp_wait<0>();
     float* rec = comb + warp * C::kRec;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -336,7 +319,7 @@ __global__ void __launch_bounds__(SparseCfg<T, D, G>::kThreads) sparse_attn_kern
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<T, D, G, C::kWarps>(p, comb, inbox, t, h, G);
+    merge_and_write<float, D, G, C::kWarps>(p, comb, inbox, t, h, G);
 }
 
 // ---- bf16 on tensor cores -------------------------------------------------------
@@ -365,7 +348,7 @@ __device__ __forceinline__ uint32_t pack2(__nv_bfloat16 lo, __nv_bfloat16 hi) {
 }
 
 template <int D>
-struct SparseMmaCfg {
+struct SparseBf16Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kMaxG = 8;
@@ -385,8 +368,8 @@ struct SparseMmaCfg {
 // rounded to bf16 and rows 8-15 what that rounding left, so P enters the
 // product to 2^-16 of itself at no extra instruction.
 template <int D>
-__global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_kernel(SparseParams p) {
-    using C = SparseMmaCfg<D>;
+__global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_kernel(SparseParams p) {
+    using C = SparseBf16Cfg<D>;
     constexpr int RC = D / 8;                    // 16-byte chunks of a row
     extern __shared__ __align__(128) unsigned char smem[];
     float* comb = reinterpret_cast<float*>(smem);
@@ -443,7 +426,6 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
         cp_commit();
     };
     for (int j = 0; j < C::kStages - 1; ++j) request(j);
-    const ListCursor now0 = next;
 
     // q as the A operand: row gid is query head gid of the group
     uint32_t q0[D / 16], q2[D / 16];
@@ -463,7 +445,7 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
     int seen = 0;
     for (int j = 0; j < tiles; ++j) {
         request(j + C::kStages - 1);
-        if (j % 32 == 0) now = j ? fetch(j) : now0;
+        if (j % 32 == 0) now = j ? fetch(j) : next;
         const int id = __shfl_sync(kFull, now.phys, j % 32);
         const int b = __shfl_sync(kFull, now.logical, j % 32);
         cp_wait<C::kStages - 1>();
@@ -552,18 +534,27 @@ __global__ void __launch_bounds__(SparseMmaCfg<D>::kThreads) sparse_attn_mma_ker
     merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps>(p, comb, inbox, t, h, G);
 }
 
-// CTAs that share one (row, head): enough to give every SM two CTAs, but each
-// warp at least two tiles.
-int cluster_for(int64_t items, int top_k, int warps) {
-    int cs = 1;
-    while (cs < 8 && items * cs < 2 * int64_t(num_sms()) && top_k >= 4 * cs * warps) cs *= 2;
-    return cs;
+// CTAs that share one (row, head): those that take the fewest steps, when `slots`
+// CTAs run at a time.  A step is a tile of every warp; the start of a CTA (three
+// dependent loads) and its merge cost about four, the exchange in a cluster one
+// more.  (56 items x 169 blocks: 21 us with 8 CTAs each, which is a second wave,
+// 16 us with 4.)
+int cluster_for(int64_t items, int top_k, int warps, int64_t slots) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int cs = 1; cs <= 8; cs *= 2) {
+        const int64_t waves = (items * cs + slots - 1) / slots;
+        const int64_t steps = waves * (ceil_div(top_k, cs * warps) + (cs > 1 ? 5 : 4));
+        if (steps < least) least = steps, best = cs;
+    }
+    return best;
 }
 
 template <typename C, auto Kern>
 int launch_sparse(const SparseParams& p, int64_t items, cudaStream_t stream) {
-    if (kernel_occupancy<Kern>(C::kThreads, C::kSmem) < 1) return PKV_ERR_CUDA;
-    const int cs = cluster_for(items, p.top_k, C::kWarps);
+    const int per_sm = kernel_occupancy<Kern>(C::kThreads, C::kSmem);
+    if (per_sm < 1) return PKV_ERR_CUDA;
+    const int cs = cluster_for(items, p.top_k, C::kWarps, int64_t(per_sm) * num_sms());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(items * cs));
     cfg.blockDim = dim3(C::kThreads);
@@ -581,13 +572,13 @@ int launch_sparse(const SparseParams& p, int64_t items, cudaStream_t stream) {
     return cuda_status(cudaLaunchKernelEx(&cfg, Kern, p));
 }
 
-template <typename T, int D>
-int launch_sparse_g(const SparseParams& p, int64_t items, cudaStream_t s) {
+template <int D>
+int launch_sparse_f32(const SparseParams& p, int64_t items, cudaStream_t s) {
     switch (p.num_q_heads / p.num_kv_heads) {
-        case 1: return launch_sparse<SparseCfg<T, D, 1>, sparse_attn_kernel<T, D, 1>>(p, items, s);
-        case 2: return launch_sparse<SparseCfg<T, D, 2>, sparse_attn_kernel<T, D, 2>>(p, items, s);
-        case 4: return launch_sparse<SparseCfg<T, D, 4>, sparse_attn_kernel<T, D, 4>>(p, items, s);
-        default: return launch_sparse<SparseCfg<T, D, 8>, sparse_attn_kernel<T, D, 8>>(p, items, s);
+        case 1: return launch_sparse<SparseF32Cfg<D, 1>, sparse_attn_f32_kernel<D, 1>>(p, items, s);
+        case 2: return launch_sparse<SparseF32Cfg<D, 2>, sparse_attn_f32_kernel<D, 2>>(p, items, s);
+        case 4: return launch_sparse<SparseF32Cfg<D, 4>, sparse_attn_f32_kernel<D, 4>>(p, items, s);
+        default: return launch_sparse<SparseF32Cfg<D, 8>, sparse_attn_f32_kernel<D, 8>>(p, items, s);
     }
 }
 
@@ -639,8 +630,8 @@ extern "C" int paged_attention_sparse(void* out, const void* q, const void* k_ca
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (desc->dtype == PKV_BF16)
         return desc->head_dim == 128
-                   ? launch_sparse<SparseMmaCfg<128>, sparse_attn_mma_kernel<128>>(p, items, cs)
-                   : launch_sparse<SparseMmaCfg<64>, sparse_attn_mma_kernel<64>>(p, items, cs);
-    return desc->head_dim == 128 ? launch_sparse_g<float, 128>(p, items, cs)
-                                 : launch_sparse_g<float, 64>(p, items, cs);
+                   ? launch_sparse<SparseBf16Cfg<128>, sparse_attn_bf16_kernel<128>>(p, items, cs)
+                   : launch_sparse<SparseBf16Cfg<64>, sparse_attn_bf16_kernel<64>>(p, items, cs);
+    return desc->head_dim == 128 ? launch_sparse_f32<128>(p, items, cs)
+                                 : launch_sparse_f32<64>(p, items, cs);
 }
