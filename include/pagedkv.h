@@ -567,8 +567,10 @@ PKV_API int pkv_tables_release(const pkv_device_tables* tables, const int32_t* s
  * (num_query_tokens == num_seqs), its last; otherwise query_start_loc is the
  * layout of paged_attention_varlen, and row i of a sequence sees keys
  * 0 .. context_lens - qlen + i.  Rows behind query_start_loc[num_seqs] are left
- * as they are, so a batch may be padded.  Caches PKV_F32 or PKV_BF16.
+ * as they are, so a batch may be padded.  Caches PKV_F32 or PKV_BF16.  Lists of
+ * up to PKV_SPARSE_MAX_TOP_K blocks (PKV_ERR_UNSUPPORTED above).
  * ======================================================================== */
+#define PKV_SPARSE_MAX_TOP_K 134217728
 
 /* Key bounds of the blocks that this step's tokens were appended to (the last
  * qlen positions of each sequence), from all their rows that hold tokens:

@@ -785,6 +785,8 @@ def pkv_select_blocks(selected, q, bounds, exps, desc, block_tables, context_len
     [T, Hkv, top_k], q [T, Hq, D]."""
     if ws is None:
         ws = workspace(select_workspace_bytes(desc, q.shape[0], max_context_len), q.device)
+        if stream is not None:
+            ws.record_stream(stream)       # it is given back while that stream may still use it
     _check(_native().select_blocks(selected, q, bounds, exps, desc, block_tables, context_lens,
                                      max_context_len, num_sink, num_recent, query_start_loc, ws,
                                      _handle(stream)), "pkv_select_blocks")

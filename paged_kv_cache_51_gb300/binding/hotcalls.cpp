@@ -168,7 +168,7 @@ Batch batch(const Call& c, PyObject* tables, PyObject* ctx, PyObject* start, int
     b.n = rows(tensor(ctx, "context_lens"), 0, "context_lens");
     b.width = rows(tensor(tables, "block_tables"), 1, "block_tables");
     if (start == Py_None && tokens != b.n)
-        refuse(PyExc_ValueError, "more or fewer query tokens than sequences need %s%s",
+        refuse(PyExc_ValueError, "query tokens other than one a sequence need %s%s",
                "query_start_loc", "");
     b.tables = static_cast<int32_t*>(c.at(tables, "block_tables", at::kInt, {b.n, b.width}));
     b.ctx = static_cast<int32_t*>(c.at(ctx, "context_lens", at::kInt, {b.n}));
@@ -182,6 +182,8 @@ Batch batch(const Call& c, PyObject* tables, PyObject* ctx, PyObject* start, int
 PyObject* block_bounds(PyObject* const* a) {
     const Call c = call(a[0], "bounds", a[8]);
     const pkv_cache_desc d = structure<pkv_cache_desc>(a[3], "desc");
+    if (a[6] != Py_None && a[7] == Py_None)
+        refuse(PyExc_ValueError, "%s is given, so %s has to be", "query_start_loc", "num_query_tokens");
     const int32_t tokens = a[7] == Py_None ? rows(tensor(a[5], "context_lens"), 0, "context_lens")
                                            : int32(a[7], "num_query_tokens");
     const Batch b = batch(c, a[4], a[5], a[6], tokens);

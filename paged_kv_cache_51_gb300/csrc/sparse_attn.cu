@@ -604,7 +604,7 @@ extern "C" int paged_attention_sparse(void* out, const void* q, const void* k_ca
         return PKV_ERR_INVALID;
     if (!query_start_loc && num_query_tokens != num_seqs) return PKV_ERR_INVALID;
     const int64_t items = int64_t(num_query_tokens) * desc->num_kv_heads;
-    if (items * 8 > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (items * 8 > INT32_MAX || top_k > PKV_SPARSE_MAX_TOP_K) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !selected ||
         !aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(k_cache, 16) ||

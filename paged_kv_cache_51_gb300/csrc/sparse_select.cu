@@ -516,12 +516,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
                 writes0 = tig % LR < 2;
             }
             auto put = [&](int at, int ex, const float (&sc)[NR]) {
-                const float eu = pow2(ex > 50 ? 0 : ex);
+                const float eu = pow2(ex > 50 ? 0 : max(ex, -126));
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     float x = sc[n] * eu;
                     if (ex > 50) x = ex == kBadId ? -INFINITY : ex == kUnbounded ? INFINITY : x;
-                    if (mine[n]) out[n][at] = ordered(x);
+                    if (mine[n]) out[n][at] = ordered(x + 0.f);   // (one zero, not two)
                 }
             };
             if (writes0 && b < end) put(b, e, s[0]);
@@ -861,8 +861,9 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
         num_sink < 0 || num_recent < 1 || int64_t(num_sink) + num_recent > top_k)
         return PKV_ERR_INVALID;
     if (!query_start_loc && num_query_tokens != num_seqs) return PKV_ERR_INVALID;
-    if (int64_t(num_query_tokens) * desc->num_kv_heads * ceil_div(max_context_len, kBlockTokens) >
-        (int64_t(1) << 36))
+    // (launch sizes and indices within 32 bits)
+    if (int64_t(num_query_tokens) * desc->num_kv_heads > INT32_MAX || top_k > PKV_SPARSE_MAX_TOP_K ||
+        ceil_div(max_context_len, kBlockTokens) * int64_t(desc->num_kv_heads) > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     if (!selected || !q || !bounds || !exps || !block_tables || !context_lens ||

@@ -552,7 +552,7 @@ extern "C" int pkv_tables_step(const pkv_device_tables* tables, const int32_t* s
     int st = check_tables(tables);
     if (st != PKV_OK) return st;
     if (num_seqs < 0 || max_tokens < 0) return PKV_ERR_INVALID;
-    if (max_tokens >= int32_t(kSat)) return PKV_ERR_UNSUPPORTED;
+    if (max_tokens >= int32_t(kSat) || max_blocks_per_seq >= int32_t(kSat)) return PKV_ERR_UNSUPPORTED;
     if (block_tables && max_blocks_per_seq < 1) return PKV_ERR_INVALID;
     st = check_tables_pointers(tables);
     if (st != PKV_OK) return st;

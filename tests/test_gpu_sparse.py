@@ -222,6 +222,82 @@ def test_selection_with_values_that_are_not_finite(pkv):
     assert {9, 20} <= set(got[0, 0].tolist())
 
 
+def test_zeros_of_either_sign_are_one_score(pkv):
+    """A head of negative zeros beside one whose score is 0 or negative: every block
+    scores 0, so the lower indices are taken."""
+    n, d = 40, 64
+    bounds = np.zeros((n, 1, 2, d), np.int8)
+    bounds[::2, 0, 0, 0], bounds[::2, 0, 1, 0] = -5, -9
+    exps = np.zeros((n, 1), np.int8)
+    q = np.full((1, 2, d), -0.0, np.float32)
+    q[0, 1, 0] = 1.0
+    t = np.arange(n, dtype=np.int32)[None, :]
+    for dtype in ("f32", "bf16"):
+        qs = q if dtype == "f32" else (q.view(np.uint32) >> 16).astype(np.uint16)
+        got = _run_select(pkv, dtype, qs, bounds, exps, t, [n * 16], [0, 1], 8, 0, 1)
+        assert got[0, 0].tolist() == [0, 1, 2, 3, 4, 5, 6, n - 1]
+    assert pkv.device_error() == 0
+
+
+def test_exponents_out_of_range_still_fill_the_list(pkv):
+    """Exponents that no bounds call writes order somehow; every entry is a block."""
+    rng = np.random.default_rng(21)
+    t, nb, bounds, exps, q, start = _select_case(rng, "f32", 2, 1, 64, [800 * 16], [1])
+    exps[:, 0] = rng.integers(-128, 128, nb)
+    got = _run_select(pkv, "f32", q, bounds, exps, t, [800 * 16], start, 60, 1, 1)
+    assert pkv.device_error() == 0
+    lst = got[0, 0].tolist()
+    assert lst == sorted(set(lst)) and lst[0] == 0 and lst[-1] == 799 and len(lst) == 60
+
+
+def test_binding_refuses_what_does_not_fit_together(pkv):
+    kd = torch.zeros((4, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+    desc = pkv.cache_desc(kd, 2)
+    bb = pkv.BlockBounds(4, 1, 64)
+    t, ctx, start = i32([[0, 1]]), i32([20]), i32([0, 3])
+    q = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    sel = torch.full((1, 1, 2), 5, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="num_query_tokens"):
+        pkv.pkv_block_bounds(bb.bounds, bb.exps, kd, desc, t, ctx, query_start_loc=start)
+    with pytest.raises(ValueError, match="exps: shape"):
+        pkv.pkv_block_bounds(bb.bounds, bb.exps[:3].contiguous(), kd, desc, t, ctx)
+    with pytest.raises(TypeError, match="k_cache must be a contiguous CUDA"):
+        pkv.pkv_block_bounds(bb.bounds, bb.exps, kd.float(), desc, t, ctx)
+    with pytest.raises(ValueError, match="block_tables: shape"):
+        pkv.pkv_select_blocks(sel, q, bb.bounds, bb.exps, desc, t.t(), ctx, 32, 0, 1)
+    with pytest.raises(TypeError, match="block_tables must be a contiguous CUDA"):
+        pkv.pkv_select_blocks(sel, q, bb.bounds, bb.exps, desc, i32([[0, 5, 1]])[:, ::2], ctx, 32,
+                              0, 1)
+    with pytest.raises(ValueError, match="query_start_loc"):
+        pkv.paged_attention_sparse(q.repeat(2, 1, 1), q.repeat(2, 1, 1), kd, kd, desc, t, ctx, sel)
+    with pytest.raises(ValueError, match="context_lens|block_tables"):
+        pkv.paged_attention_sparse(q, q, kd, kd, desc, t, i32([20, 20]), sel,
+                                   query_start_loc=i32([0, 1, 1]))
+    with pytest.raises(ValueError, match="selected: shape"):
+        pkv.paged_attention_sparse(q, q, kd, kd, desc, t, ctx, sel[:, 0])
+    with pytest.raises(pkv.PagedKVError):
+        pkv.pkv_select_blocks(sel, q, bb.bounds, bb.exps, desc, t, ctx, 32, 2, 1)
+    assert (sel == 5).all() and pkv.device_error() == 0
+
+
+def test_selection_on_a_stream_of_its_own_without_a_workspace(pkv):
+    rng = np.random.default_rng(30)
+    ctx = [3000, 2000]
+    t, nb, bounds, exps, q, start = _select_case(rng, "bf16", 4, 2, 128, ctx, [1, 1])
+    desc = pkv.CacheDesc(pkv.PKV_BF16, nb, 16, 2, 4, 128)
+    args = [to_dev(q, "bf16"), to_dev(bounds), to_dev(exps), desc, i32(t), i32(ctx)]
+    sel = torch.empty((2, 2, 20), dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(30):
+        pkv.pkv_select_blocks(sel, *args, max(ctx), 1, 1, stream=st)
+        torch.full((1 << 16,), 0xFF, dtype=torch.uint8, device="cuda")   # may reuse what is free
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    ref = sparse.select(q, bounds, exps, t, start, ctx, 16, 20, 1, 1, "bf16")
+    assert np.array_equal(sel.cpu().numpy(), ref)
+
+
 def test_selection_flags_bad_batches(pkv):
     rng = np.random.default_rng(6)
     ctx = [600, 90, 300]

@@ -45,6 +45,7 @@ def test_tables_step_refuses(lib):
     assert _step(lib, _tables(lib, num_blocks=1 << 30)) == lib.PKV_ERR_UNSUPPORTED
     assert _step(lib, _tables(lib, max_blocks=1 << 28)) == lib.PKV_ERR_UNSUPPORTED
     assert _step(lib, t, tokens=1 << 30) == lib.PKV_ERR_UNSUPPORTED
+    assert _step(lib, t, width=1 << 30) == lib.PKV_ERR_UNSUPPORTED
 
 
 def test_tables_release_refuses(lib):
@@ -121,6 +122,14 @@ def test_select_and_attend_scalars(lib):
     assert _select(lib, d, sink=-1) == bad and _select(lib, d, recent=0) == bad
     assert _select(lib, d, top_k=4, sink=3, recent=2) == bad
     assert _select(lib, d, max_ctx=0) == bad
+    many = 1 << 28
+    assert _select(lib, d, top_k=many) == lib.PKV_ERR_UNSUPPORTED
+    assert _select(lib, d, n=many, tokens=many) == lib.PKV_ERR_UNSUPPORTED
+    wide = _desc(lib, num_kv_heads=1 << 12, num_q_heads=1 << 12)
+    assert _select(lib, wide, max_ctx=1 << 30) == lib.PKV_ERR_UNSUPPORTED
+    assert _attend(lib, d, top_k=many) == lib.PKV_ERR_UNSUPPORTED
+    assert _attend(lib, d, n=many, tokens=many) == lib.PKV_ERR_UNSUPPORTED
+    assert _bounds(lib, d, n=many, tokens=many) == lib.PKV_ERR_UNSUPPORTED
     assert _select(lib, d, ws=None) == lib.PKV_ERR_WORKSPACE
     assert _select(lib, d, ws=ctypes.c_void_p((1 << 20) + 16)) == lib.PKV_ERR_WORKSPACE
     assert _select(lib, d, ws_bytes=16) == lib.PKV_ERR_WORKSPACE
