@@ -275,10 +275,7 @@ __device__ __forceinline__ void raise_codes(uint32_t w, uint32_t& even, uint32_t
     odd = (w >> 8 & 0x00ff00ffu) ^ 0x64806480u;
 }
 
-__device__ __forceinline__ uint32_t half_pair(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
+__device__ __forceinline__ uint32_t bits(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
 // d = c + a . b, the sums of two columns starting from c0 and c1
 __device__ __forceinline__ void mma16816_f16(float (&d)[4], float c0, float c1, float c2, float c3,
@@ -378,20 +375,23 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
     uint4* ring = &ring_all[warp][0][0][lane];
     const uint32_t ring_u = smem_u32(ring);
     int e0[kScoreStages], e1[kScoreStages];
+    const int8_t* bounds_h = p.bounds + h * (2 * D) + tig * 16;
+    const int8_t* exps_h = p.exps + h;
+    const int bounds_step = p.num_kv_heads * (2 * D);
     auto request = [&](int b, int js) {          // the tile at block b, into stage js
         if (b < end) {
-            const bool good0 = id0 >= 0 && id0 < p.num_blocks, good1 = id1 >= 0 && id1 < p.num_blocks;
-            const size_t tile0 = size_t(good0 ? id0 : 0) * p.num_kv_heads + h;
-            const size_t tile1 = size_t(good1 ? id1 : 0) * p.num_kv_heads + h;
-            const int8_t* src0 = p.bounds + tile0 * (2 * D) + tig * 16;
-            const int8_t* src1 = p.bounds + tile1 * (2 * D) + tig * 16;
+            const bool good0 = uint32_t(id0) < uint32_t(p.num_blocks);
+            const bool good1 = uint32_t(id1) < uint32_t(p.num_blocks);
+            const int at0 = good0 ? id0 : 0, at1 = good1 ? id1 : 0;
+            const int8_t* src0 = bounds_h + int64_t(at0) * bounds_step;
+            const int8_t* src1 = bounds_h + int64_t(at1) * bounds_step;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 cp_async16(ring_u + (js * 2 * CH + 2 * c) * 512, src0 + 64 * c, true);
                 cp_async16(ring_u + (js * 2 * CH + 2 * c + 1) * 512, src1 + 64 * c, true);
             }
-            e0[js] = p.exps[tile0];
-            e1[js] = p.exps[tile1];
+            e0[js] = exps_h[int64_t(at0) * p.num_kv_heads];
+            e1[js] = exps_h[int64_t(at1) * p.num_kv_heads];
             if (!good0 || !good1) {
                 if ((!good0 && b + gid < end) || (!good1 && b + gid + 8 < end))
                     if (h == 0) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
@@ -428,27 +428,37 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
         const int eq = code_exponent(amax);
-        // (a query with values that are not finite has codes of 0)
-        const float u = odd ? 0.f : pow2(-eq);
+        const float u = pow2(-eq);
         unit_q = odd ? 0.f : pow2(eq);
+        if (odd || eq == 50) {                   // (rare, and the only values past 127 units)
+#pragma unroll
+            for (int c = 0; c < NP; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)     // a query that is not finite has codes of 0
+                    x[c][i] = odd ? 0.f : fminf(fmaxf(x[c][i], -127.f * pow2(50)), 127.f * pow2(50));
+        }
 #pragma unroll
         for (int c = 0; c < NP; ++c) {
-            float up = 0.f, down = 0.f;
+            // x / 2^eq to the nearest whole number, ties to even: added to 1.5 * 2^23
+            // it is rounded there
+            constexpr float kRound = 12582912.f;
+            float sum = 0.f, size = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float a = odd ? 0.f : fminf(fmaxf(rintf(x[c][i] * u), -127.f), 127.f);
-                up += fmaxf(a, 0.f);
-                down += fminf(a, 0.f);
-                x[c][i] = a;
+                x[c][i] = __fsub_rn(__fmaf_rn(x[c][i], u, kRound), kRound);
+                sum += x[c][i];
+                size += fabsf(x[c][i]);
             }
+            const __half2 zero = __float2half2_rn(0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {    // bytes 0 and 2, then 1 and 3
-                    const float a = x[c][4 * i + k], b = x[c][4 * i + k + 2];
-                    bq[c][i][k] = half_pair(fmaxf(a, 0.f), fmaxf(b, 0.f));
-                    bq[NP + c][i][k] = half_pair(fminf(a, 0.f), fminf(b, 0.f));
+                    const __half2 v = __floats2half2_rn(x[c][4 * i + k], x[c][4 * i + k + 2]);
+                    bq[c][i][k] = bits(__hmax2(v, zero));
+                    bq[NP + c][i][k] = bits(__hmin2(v, zero));
                 }
+            float up = 0.5f * (size + sum), down = 0.5f * (sum - size);   // whole numbers: exact
             up += __shfl_xor_sync(kFull, up, 1);
             up += __shfl_xor_sync(kFull, up, 2);
             down += __shfl_xor_sync(kFull, down, 1);
@@ -516,13 +526,17 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
                 writes0 = tig % LR < 2;
             }
             auto put = [&](int at, int ex, const float (&sc)[NR]) {
-                const float eu = pow2(ex > 50 ? 0 : max(ex, -126));
+                float x[NR];
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float x = sc[n] * eu;
-                    if (ex > 50) x = ex == kBadId ? -INFINITY : ex == kUnbounded ? INFINITY : x;
-                    if (mine[n]) out[n][at] = ordered(x + 0.f);   // (one zero, not two)
+                for (int n = 0; n < NR; ++n) x[n] = sc[n] * pow2(ex);
+                if (ex > 50 || ex < -126) {      // (an exponent that no bounds call writes: any value)
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        x[n] = ex == kBadId ? -INFINITY : ex == kUnbounded ? INFINITY : 0.f;
                 }
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    if (mine[n]) out[n][at] = ordered(x[n] + 0.f);   // (one zero, not two)
             };
             if (writes0 && b < end) put(b, e, s[0]);
             if (writes1 && b + 8 < end) put(b + 8, f, s[1]);
@@ -567,27 +581,30 @@ __device__ __forceinline__ void warps_before(uint32_t& a, uint32_t& b, PickScrat
 // spread over the bins, so one histogram and one ranking is the rule.  A row's
 // keys stay in registers, kHeld to a thread, asked for before the row's context
 // is known; with kHeld 0 (rows longer than that) every pass reads them again.
+// Keys of real blocks lie between those of the two infinities; the ends carry a
+// key above all and places behind the row one below all, so that no pass has to
+// look at indices.
 template <int NT, int kHeld>
 __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
     using S = PickScratch<NT>;
     constexpr bool Held = kHeld > 0;
+    constexpr uint32_t kEnd = 0xffffffffu, kNone = 0u;
     __shared__ __align__(16) S s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 #pragma unroll
     for (int i = 0; i < 4; ++i) s.hist[i * NT + tid] = 0;
     if (tid == 0) s.count = 0;
-    __syncthreads();
     const int h = int(blockIdx.x % uint32_t(p.num_kv_heads));
     const int t = int(blockIdx.x / uint32_t(p.num_kv_heads));
     const uint32_t* far = p.keys + size_t(blockIdx.x) * p.stride;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    const int mine = Held ? warp * 32 * kHeld + lane : 0;
+    const int mine = warp * 32 * kHeld + lane;
     uint32_t held[Held ? kHeld : 1];
     if (Held) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            held[i] = mine + 32 * i < p.stride ? far[mine + 32 * i] : 0u;
+            held[i] = mine + 32 * i < p.stride ? far[mine + 32 * i] : kNone;
     }
     int seq;
     const int row_sees = row_keys(p.rows, t, seq, tid == 0 && h == 0 ? p.err : nullptr);
@@ -599,27 +616,35 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
         return;
     }
     const int b0 = p.sink, b1 = blocks - p.recent;
-    // f(key) for each of this thread's keys of blocks b0 .. b1 - 1
-    auto each = [&](auto f) {
+    auto marked = [&](int b, uint32_t k) {
+        return b >= blocks ? kNone : b < b0 || b >= b1 ? kEnd : k;
+    };
+    if (Held) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = marked(mine + 32 * i, held[i]);
+    }
+    auto each = [&](auto f) {                    // f(key) for each of this thread's keys
         if (Held) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                if (mine + 32 * i >= b0 && mine + 32 * i < b1) f(held[i]);
+            for (int i = 0; i < kHeld; ++i) f(held[i]);
         } else {
             for (int b = b0 + tid; b < b1; b += NT) f(far[b]);
         }
     };
     uint32_t want = uint32_t(p.top_k - p.sink - p.recent);
-    uint32_t cut = 0xffffffffu, take = 0;        // taken: keys above `cut`, `take` equal to it
+    uint32_t cut = kEnd - 1, take = 0;           // taken: keys above `cut`, `take` equal to it
     if (want > 0) {
         uint32_t lo = 0xffffffffu, hi = 0;
-        each([&](uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
+        each([&](uint32_t k) {
+            lo = min(lo, k - 1);                 // (kNone wraps to the top)
+            hi = max(hi, k + 1);                 // (kEnd wraps to 0)
+        });
         lo = __reduce_min_sync(kFull, lo);
         hi = __reduce_max_sync(kFull, hi);
         if (lane == 0) s.warp_a[warp] = lo, s.warp_b[warp] = hi;
         __syncthreads();
-        lo = __reduce_min_sync(kFull, s.warp_a[lane % S::kWarps]);
-        hi = __reduce_max_sync(kFull, s.warp_b[lane % S::kWarps]);
+        lo = __reduce_min_sync(kFull, s.warp_a[lane % S::kWarps]) + 1;
+        hi = __reduce_max_sync(kFull, s.warp_b[lane % S::kWarps]) - 1;
         for (;;) {                               // the range lo .. hi holds the want-th
             if (lo == hi) {                      // equal keys (a query of zeros): the lower indices
                 cut = lo;
@@ -628,7 +653,7 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
             }
             const int shift = max(0, 32 - __clz(hi - lo) - (31 - __clz(S::kBins)));
             each([&](uint32_t k) {
-                if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
+                if (k - lo <= hi - lo) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
             });
             __syncthreads();
             // bins from above, four to a thread
@@ -666,7 +691,7 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
             }
             if (inside <= uint32_t(NT)) {
                 each([&](uint32_t k) {
-                    if (k >= first && k <= last) s.cand[atomicAdd(&s.count, 1u)] = k;
+                    if (k - first <= last - first) s.cand[atomicAdd(&s.count, 1u)] = k;
                 });
                 __syncthreads();
                 if (tid < int(inside)) {
@@ -696,35 +721,41 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
     }
     // in ascending order: a stretch of blocks to a warp, whose counts are summed
     // first; within a warp 32 blocks at a time by ballot
-    const int stretch = Held ? 32 * kHeld : ((blocks + S::kWarps - 1) / S::kWarps + 31) & ~31;
-    const int f = min(blocks, warp * stretch), e = min(blocks, f + stretch);
-    auto walk = [&](auto use) {                  // use(block, above the cut, equal to it)
-        auto one = [&](int b, uint32_t k) {
-            const bool in = b < e, end = b < b0 || b >= b1;
-            use(b, in && (end || k > cut), in && !end && k == cut);
-        };
-        if (Held) {
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                if (f + 32 * i < e) one(mine + 32 * i, held[i]);
-        } else {
-            for (int b = f; b < e; b += 32) one(b + lane, b + lane < e ? far[b + lane] : 0u);
-        }
-    };
-    uint32_t n_above = 0, n_equal = 0;
-    walk([&](int, bool above, bool equal) {
-        n_above += __popc(__ballot_sync(kFull, above));
-        n_equal += __popc(__ballot_sync(kFull, equal));
-    });
-    warps_before<NT>(n_above, n_equal, s);
     const uint32_t below = (1u << lane) - 1u;
-    walk([&](int b, bool above, bool equal) {
-        const uint32_t ma = __ballot_sync(kFull, above), me = __ballot_sync(kFull, equal);
+    uint32_t n_above = 0, n_equal = 0;
+    auto place = [&](int b, uint32_t k, uint32_t ma, uint32_t me) {
         const uint32_t at = n_above + __popc(ma & below), nth = n_equal + __popc(me & below);
-        if (above || (equal && nth < take)) out[at + min(nth, take)] = b;
+        if (k > cut || (k == cut && nth < take)) out[at + min(nth, take)] = b;
         n_above += __popc(ma);
         n_equal += __popc(me);
-    });
+    };
+    if (Held) {
+        uint32_t ma[Held ? kHeld : 1], me[Held ? kHeld : 1];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            ma[i] = __ballot_sync(kFull, held[i] > cut);
+            me[i] = __ballot_sync(kFull, held[i] == cut);
+            n_above += __popc(ma[i]);
+            n_equal += __popc(me[i]);
+        }
+        warps_before<NT>(n_above, n_equal, s);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) place(mine + 32 * i, held[i], ma[i], me[i]);
+    } else {
+        const int stretch = ((blocks + S::kWarps - 1) / S::kWarps + 31) & ~31;
+        const int f = min(blocks, warp * stretch), e = min(blocks, f + stretch);
+        auto key = [&](int b) { return b < e ? marked(b, far[b]) : kNone; };
+        for (int b = f; b < e; b += 32) {
+            const uint32_t k = key(b + lane);
+            n_above += __popc(__ballot_sync(kFull, k > cut));
+            n_equal += __popc(__ballot_sync(kFull, k == cut));
+        }
+        warps_before<NT>(n_above, n_equal, s);
+        for (int b = f; b < e; b += 32) {
+            const uint32_t k = key(b + lane);
+            place(b + lane, k, __ballot_sync(kFull, k > cut), __ballot_sync(kFull, k == cut));
+        }
+    }
 }
 
 size_t select_stride(int32_t max_ctx) {
