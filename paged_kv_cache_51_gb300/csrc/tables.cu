@@ -319,7 +319,9 @@ constexpr int kStepSeqs = 2048;   // most requests of a step in one launch
 // A step in one launch, for outputs that are not inputs.  Every CTA checks and
 // sums all requests and keeps what the outputs are made of in shared memory; then
 // the CTAs fill the outputs side by side.  What another CTA writes is never read:
-// a new entry is taken from the free list wherever it is needed.
+// a new entry is taken from the free list wherever it is needed.  Device time of a
+// call: 64 requests 4.4 us, 515 requests with 2048 tokens 6.7 us, 1024 requests x
+// 2049 entries (12.8 MB) 7.7 us; the two launches take 6.0, 7.2 and 7.9 us.
 template <int NT>
 __global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int segments, int copy_warps) {
     extern __shared__ uint32_t dyn[];             // 6 n + 1 words, then two planes of max_seqs bits
