@@ -537,7 +537,9 @@ typedef struct pkv_device_tables {
  * (PKV_DEV_BAD_CONTEXT_LEN) or more tokens than a row or block_tables has room
  * for (PKV_DEV_TABLE_TOO_NARROW) is skipped: context_lens[i] = 0, no tokens, a
  * row of -1.  num_seqs == 0 writes the padding, query_start_loc[0] and the
- * count.  Outputs do not overlap inputs but where said. */
+ * count.  Outputs do not overlap inputs but where said (block_tables is never
+ * tables->block_table; with seq_rows NULL that table can be passed to the
+ * attention as it is, and block_tables be NULL). */
 PKV_API int pkv_tables_step(const pkv_device_tables* tables, const int32_t* seq_rows,
                             const int32_t* cached_lens, const int32_t* new_lens,
                             int32_t num_seqs, int32_t max_tokens, int32_t* free_count_out,

@@ -320,8 +320,8 @@ constexpr int kStepSeqs = 2048;   // most requests of a step in one launch
 // sums all requests and keeps what the outputs are made of in shared memory; then
 // the CTAs fill the outputs side by side.  What another CTA writes is never read:
 // a new entry is taken from the free list wherever it is needed.  Device time of a
-// call: 64 requests 4.4 us, 515 requests with 2048 tokens 6.7 us, 1024 requests x
-// 2049 entries (12.8 MB) 7.7 us; the two launches take 6.0, 7.2 and 7.9 us.
+// call: 64 requests 3.7 us, 515 requests with 2048 tokens 5.2 us, 1024 requests x
+// 2049 entries (12.8 MB) 6.8 us; the two launches take 6.0, 7.2 and 7.9 us.
 template <int NT>
 __global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int segments, int copy_warps) {
     extern __shared__ uint32_t dyn[];             // 6 n + 1 words, then two planes of max_seqs bits
@@ -369,41 +369,44 @@ __global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int seg
         if (j >= old_blocks[i]) return take_block(p, have, before[i] + (j - old_blocks[i]), flag);
         return p.table[size_t(row[i]) * p.max_blocks + j];
     };
-    const int warps = int(gridDim.x) * (NT / 32), first = int(blockIdx.x) * (NT / 32) + (threadIdx.x >> 5);
-    for (int w = first; w < copy_warps; w += warps) {
-        const int i = w / segments, j0 = (w % segments) * kSegment;
-        int32_t* dst = p.out_tables + size_t(i) * p.width + j0;
-        int32_t v[kSegment / 32];
-#pragma unroll
-        for (int k = 0; k < kSegment / 32; ++k) {
-            const int j = j0 + lane + 32 * k;
-            v[k] = j < now_blocks[i] ? block(i, j, nullptr) : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kSegment / 32; ++k) {
-            const int j = lane + 32 * k;
-            if (j0 + j < p.width) dst[j] = v[k];
-        }
-    }
     const int threads = int(gridDim.x) * NT, me = int(blockIdx.x) * NT + threadIdx.x;
     for (int i = me; i <= p.n; i += threads) {
         if (i < p.n) p.ctx[i] = ctx[i];
         p.start[i] = start[i];
     }
     if (me == 0) *p.free_count_out = free_ok ? int32_t(have - s.used) : free0;
-    // new entries of the state, one thread each: the request by bisection
-    for (uint32_t b = me; b < s.used; b += threads) {
-        int lo = 0, hi = p.n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (before[mid] + (now_blocks[mid] - old_blocks[mid]) > b) hi = mid;
-            else lo = mid + 1;
+    // a warp copies a segment of a row, or makes 32 tokens and as many of the new
+    // entries (each of which holds a new token: there are no more of them)
+    const int total = start[p.n], units = copy_warps + (p.max_tokens + 31) / 32;
+    for (int w = me >> 5; w < units; w += threads >> 5) {
+        if (w < copy_warps) {
+            const int i = w / segments, j0 = (w % segments) * kSegment;
+            int32_t* dst = p.out_tables + size_t(i) * p.width + j0;
+            int32_t v[kSegment / 32];
+#pragma unroll
+            for (int k = 0; k < kSegment / 32; ++k) {
+                const int j = j0 + lane + 32 * k;
+                v[k] = j < now_blocks[i] ? block(i, j, nullptr) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kSegment / 32; ++k) {
+                const int j = lane + 32 * k;
+                if (j0 + j < p.width) dst[j] = v[k];
+            }
+            continue;
         }
-        p.table[size_t(row[lo]) * p.max_blocks + old_blocks[lo] + (b - before[lo])] =
-            take_block(p, have, b, p.err);
-    }
-    const int total = start[p.n];
-    for (int t = me; t < p.max_tokens; t += threads) {
+        const int t = (w - copy_warps) * 32 + lane;
+        if (uint32_t(t) < s.used) {              // the request by bisection
+            int lo = 0, hi = p.n - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (before[mid] + (now_blocks[mid] - old_blocks[mid]) > uint32_t(t)) hi = mid;
+                else lo = mid + 1;
+            }
+            p.table[size_t(row[lo]) * p.max_blocks + old_blocks[lo] + (t - before[lo])] =
+                take_block(p, have, t, p.err);
+        }
+        if (t >= p.max_tokens) continue;
         int64_t slot = -1;
         int pos = 0;
         if (t < total) {
@@ -532,7 +535,7 @@ int launch_step(const TablesParams& p, int segments, int64_t copy_warps, int pla
     const int fixed = (6 * kStepSeqs + 1) * 4;
     if (kernel_occupancy<tables_step_kernel<NT>>(NT, fixed + plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
         return PKV_ERR_CUDA;
-    const int64_t warps = std::max<int64_t>(copy_warps, ceil_div(p.max_tokens, 32));
+    const int64_t warps = copy_warps + ceil_div(p.max_tokens, 32);
     const int64_t ctas = std::max<int64_t>(
         1, std::min<int64_t>((warps + NT / 32 - 1) / (NT / 32), 1024 / NT * int64_t(num_sms())));
     return cuda_status(launch_pdl(tables_step_kernel<NT>, dim3(unsigned(ctas)), dim3(NT),
@@ -558,7 +561,8 @@ extern "C" int pkv_tables_step(const pkv_device_tables* tables, const int32_t* s
     if (block_tables && max_blocks_per_seq < 1) return PKV_ERR_INVALID;
     st = check_tables_pointers(tables);
     if (st != PKV_OK) return st;
-    if (!query_start_loc || (num_seqs > 0 && (!cached_lens || !context_lens)) ||
+    if (block_tables == tables->block_table ||   // the state itself is not an output
+        !query_start_loc || (num_seqs > 0 && (!cached_lens || !context_lens)) ||
         (max_tokens > 0 && !slot_mapping) ||
         !aligned4(seq_rows) || !aligned4(cached_lens) || !aligned4(new_lens) ||
         !aligned4(free_count_out) || !aligned4(block_tables) || !aligned4(context_lens) ||
@@ -568,7 +572,7 @@ extern "C" int pkv_tables_step(const pkv_device_tables* tables, const int32_t* s
     const int segments = block_tables ? ceil_div(max_blocks_per_seq, kSegment) : 0;
     const int64_t copy_warps = int64_t(num_seqs) * segments;
     const int64_t warps = copy_warps + ceil_div(max_tokens, 32);
-    if (copy_warps > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (warps > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
     TablesParams p;
     p.err = device_error_ptr(&st);
     if (st != PKV_OK) return st;

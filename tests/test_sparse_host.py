@@ -11,7 +11,7 @@ ODD = ctypes.c_void_p((1 << 20) + 2)
 
 
 def _tables(lib, **kw):
-    f = dict(block_table=1 << 20, free_list=1 << 20, free_count=1 << 20, max_seqs=8, max_blocks=4,
+    f = dict(block_table=1 << 21, free_list=1 << 20, free_count=1 << 20, max_seqs=8, max_blocks=4,
              num_blocks=32, block_size=16)
     f.update(kw)
     return lib.DeviceTablesDesc(*(f[n] for n, _ in lib.DeviceTablesDesc._fields_))
@@ -41,6 +41,8 @@ def test_tables_step_refuses(lib):
         assert _step(lib, t, **{name: None}) == bad, name
     for name in ("rows", "cached", "new", "count", "tables", "ctx", "start", "slots", "pos"):
         assert _step(lib, t, **{name: ODD}) == bad, name
+    own = _tables(lib, block_table=(1 << 20) + 64)
+    assert _step(lib, own, tables=ctypes.c_void_p((1 << 20) + 64)) == bad
     assert _step(lib, _tables(lib, max_seqs=262145)) == lib.PKV_ERR_UNSUPPORTED
     assert _step(lib, _tables(lib, num_blocks=1 << 30)) == lib.PKV_ERR_UNSUPPORTED
     assert _step(lib, _tables(lib, max_blocks=1 << 28)) == lib.PKV_ERR_UNSUPPORTED
