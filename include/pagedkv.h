@@ -550,9 +550,9 @@ PKV_API int pkv_tables_step(const pkv_device_tables* tables, const int32_t* seq_
 /* Give back the blocks of rows seq_rows[i] (NULL: row i), which hold lens[i]
  * tokens (device [num_seqs]), in request and table order; their entries become
  * -1 and *free_count grows in place.  Skipped and flagged: a row out of range,
- * named twice or already released (PKV_DEV_BAD_SEQ_ROW), a length out of range
- * (as in pkv_tables_step), blocks past the end of the free list
- * (PKV_DEV_BAD_BLOCK_ID). */
+ * named twice, already released or holding fewer blocks (PKV_DEV_BAD_SEQ_ROW), a
+ * length out of range (as in pkv_tables_step), blocks past the end of the free
+ * list (PKV_DEV_BAD_BLOCK_ID). */
 PKV_API int pkv_tables_release(const pkv_device_tables* tables, const int32_t* seq_rows,
                                const int32_t* lens, int32_t num_seqs, void* stream);
 

@@ -80,7 +80,8 @@ __device__ __forceinline__ void scan_inclusive(uint32_t& a, uint32_t& b, ScanScr
     }
     total_a = __shfl_sync(kFull, wa, kWarps - 1);
     total_b = __shfl_sync(kFull, wb, kWarps - 1);
-    const uint32_t pa = __shfl_sync(kFull, wa, max(warp - 1, 0)), pb = __shfl_sync(kFull, wb, max(warp - 1, 0));
+    const uint32_t pa = __shfl_sync(kFull, wa, max(warp - 1, 0));
+    const uint32_t pb = __shfl_sync(kFull, wb, max(warp - 1, 0));
     if (warp > 0) a = sat_add(a, pa), b = sat_add(b, pb);
     __syncthreads();                              // (the scratch may be written again)
 }
@@ -191,7 +192,8 @@ __device__ __forceinline__ uint32_t free_blocks(const TablesParams& p, int count
 }
 
 // Entry `k` from the top of the free stack: the id, or -1 if it is none.
-__device__ __forceinline__ int take_block(const TablesParams& p, uint32_t have, uint32_t k, int* tell) {
+__device__ __forceinline__ int take_block(const TablesParams& p, uint32_t have, uint32_t k,
+                                          int* tell) {
     const int blk = p.free_list[have - 1 - k];
     if (blk >= 0 && blk < p.num_blocks) return blk;
     flag_error(tell, PKV_DEV_BAD_BLOCK_ID);
@@ -224,7 +226,8 @@ __global__ void __launch_bounds__(kPlanThreads) tables_plan_kernel(TablesParams 
     StepSums s;
     for (int base = 0; base < p.n; base += kPlanThreads) {
         const int i = base + threadIdx.x;
-        const Request r = plan_pass<kPlanThreads>(p, i, base ? load_request(p, i) : given, twice, have, limit, scratch, s, p.err);
+        const Request r = plan_pass<kPlanThreads>(p, i, base ? load_request(p, i) : given, twice,
+                                                  have, limit, scratch, s, p.err);
         if (i < p.n) {
             p.ctx[i] = r.ok ? r.cached + (r.served ? r.fresh : 0) : 0;
             p.start[i + 1] = int32_t(min(r.tok_in, s.placed));
@@ -323,7 +326,8 @@ constexpr int kStepSeqs = 2048;   // most requests of a step in one launch
 // call: 64 requests 3.7 us, 515 requests with 2048 tokens 5.2 us, 1024 requests x
 // 2049 entries (12.8 MB) 6.8 us; the two launches take 6.0, 7.2 and 7.9 us.
 template <int NT>
-__global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int segments, int copy_warps) {
+__global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int segments,
+                                                         int copy_warps) {
     extern __shared__ uint32_t dyn[];             // 6 n + 1 words, then two planes of max_seqs bits
     __shared__ ScanScratch<NT> scratch;
     int32_t* row = reinterpret_cast<int32_t*>(dyn);    // -1: refused
@@ -341,7 +345,8 @@ __global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int seg
     const int free0 = *p.free_count;
     const Given given = load_request(p, threadIdx.x);
     if (p.seq_rows)
-        mark_rows<NT>(p.seq_rows, given.row, p.n, p.max_seqs, bits, bits + (p.max_seqs + 31) / 32);
+        mark_rows<NT>(p.seq_rows, given.row, p.n, p.max_seqs, bits,
+                      bits + (p.max_seqs + 31) / 32);
     bool free_ok;
     const uint32_t have = free_blocks(p, free0, free_ok);
     if (!free_ok && threadIdx.x == 0) flag_error(tell, PKV_DEV_BAD_BLOCK_ID);
@@ -350,7 +355,8 @@ __global__ void __launch_bounds__(NT) tables_step_kernel(TablesParams p, int seg
     if (threadIdx.x == 0) start[0] = 0;
     for (int base = 0; base < p.n; base += NT) {
         const int i = base + threadIdx.x;
-        const Request r = plan_pass<NT>(p, i, base ? load_request(p, i) : given, twice, have, limit, scratch, s, tell);
+        const Request r = plan_pass<NT>(p, i, base ? load_request(p, i) : given, twice, have,
+                                        limit, scratch, s, tell);
         if (i < p.n) {
             const int held = r.ok ? int(blocks_of(r.cached, p.block_size)) : 0;
             ctx[i] = r.ok ? r.cached + (r.served ? r.fresh : 0) : 0;
@@ -461,7 +467,8 @@ __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleasePar
         uint32_t blocks = 0;
         int row = -1;
         if (i < p.n) {
-            row = checked_row(p.seq_rows ? p.seq_rows[i] : i, p.seq_rows != nullptr, p.max_seqs, twice);
+            row = checked_row(p.seq_rows ? p.seq_rows[i] : i, p.seq_rows != nullptr, p.max_seqs,
+                              twice);
             const int len = p.lens[i];
             if (row < 0) {
                 flag_error(p.err, PKV_DEV_BAD_SEQ_ROW);
@@ -470,9 +477,12 @@ __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleasePar
             } else if (len > int64_t(p.max_blocks) * p.block_size) {
                 flag_error(p.err, PKV_DEV_TABLE_TOO_NARROW);
             } else if (len > 0) {
-                // a row that was released already holds -1: nothing to give back
-                if (p.table[size_t(row) * p.max_blocks] < 0) flag_error(p.err, PKV_DEV_BAD_SEQ_ROW);
-                else blocks = uint32_t(blocks_of(len, p.block_size));
+                // a row that was released already, or holds fewer blocks, has -1 there:
+                // nothing is given back
+                const int32_t* e = p.table + size_t(row) * p.max_blocks;
+                const int64_t held = blocks_of(len, p.block_size);
+                if (e[0] < 0 || e[held - 1] < 0) flag_error(p.err, PKV_DEV_BAD_SEQ_ROW);
+                else blocks = uint32_t(held);
             }
         }
         uint32_t in_pass = blocks, none = 0, sum, none_sum;
@@ -497,7 +507,8 @@ __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleasePar
                 if (end[mid] > b) hi = mid;
                 else lo = mid + 1;
             }
-            int32_t* e = p.table + size_t(rows[lo]) * p.max_blocks + (b - (lo ? end[lo - 1] : first));
+            int32_t* e = p.table + size_t(rows[lo]) * p.max_blocks +
+                         (b - (lo ? end[lo - 1] : first));
             const int blk = *e;
             if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
             p.free_list[uint32_t(free0) + b] = blk;
@@ -531,7 +542,8 @@ int check_tables_pointers(const pkv_device_tables* t) {
 int plane_bytes(int max_seqs) { return 2 * ((max_seqs + 31) / 32) * 4; }
 
 template <int NT>
-int launch_step(const TablesParams& p, int segments, int64_t copy_warps, int planes, cudaStream_t s) {
+int launch_step(const TablesParams& p, int segments, int64_t copy_warps, int planes,
+                cudaStream_t s) {
     const int fixed = (6 * kStepSeqs + 1) * 4;
     if (kernel_occupancy<tables_step_kernel<NT>>(NT, fixed + plane_bytes(PKV_TABLES_MAX_SEQS)) < 1)
         return PKV_ERR_CUDA;
@@ -557,7 +569,8 @@ extern "C" int pkv_tables_step(const pkv_device_tables* tables, const int32_t* s
     int st = check_tables(tables);
     if (st != PKV_OK) return st;
     if (num_seqs < 0 || max_tokens < 0) return PKV_ERR_INVALID;
-    if (max_tokens >= int32_t(kSat) || max_blocks_per_seq >= int32_t(kSat)) return PKV_ERR_UNSUPPORTED;
+    if (max_tokens >= int32_t(kSat) || max_blocks_per_seq >= int32_t(kSat))
+        return PKV_ERR_UNSUPPORTED;
     if (block_tables && max_blocks_per_seq < 1) return PKV_ERR_INVALID;
     st = check_tables_pointers(tables);
     if (st != PKV_OK) return st;

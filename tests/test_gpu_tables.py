@@ -203,6 +203,8 @@ def test_release_refuses_rows_it_released(pkv):
     assert pkv.device_error() == 2
     pkv.pkv_tables_release(dt, i32([2]), i32([17]))
     assert pkv.device_error() == 7
+    pkv.pkv_tables_release(dt, i32([2]), i32([5]))                    # holds one block, not two
+    assert pkv.device_error() == 9
     assert dt.free_count.item() == 5
     pkv.pkv_tables_release(dt, i32([2, 0]), i32([4, 6]))
     assert pkv.device_error() == 0 and dt.free_count.item() == 8
