@@ -500,6 +500,50 @@ def test_tiles_past_32_bits_of_the_pool(pkv, dtype, hq, hkv):
     assert np.array_equal(exps[nb - n:].cpu().numpy(), e)
 
 
+def test_bounds_past_32_bits_of_their_pool(pkv):
+    """More than 2^31 bytes of bounds: blocks at the end of the pool are scored."""
+    nb, hkv, d, n = 1 << 20, 9, 128, 300
+    bd = torch.empty((nb, hkv, 2, d), dtype=torch.int8, device="cuda")
+    ed = torch.empty((nb, hkv), dtype=torch.int8, device="cuda")
+    assert bd.numel() > 1 << 31
+    rng = np.random.default_rng(19)
+    t, _, bounds, exps, q, start = _select_case(rng, "bf16", 2 * hkv, hkv, d, [n * 16], [1])
+    ids = nb - bounds.shape[0] + np.arange(bounds.shape[0])
+    bd[nb - bounds.shape[0]:], ed[nb - bounds.shape[0]:] = to_dev(bounds), to_dev(exps)
+    desc = pkv.CacheDesc(pkv.PKV_BF16, nb, 16, hkv, 2 * hkv, d)
+    sel = torch.empty((1, hkv, 40), dtype=torch.int32, device="cuda")
+    pkv.pkv_select_blocks(sel, to_dev(q, "bf16"), bd, ed, desc, i32(ids[t]), i32([n * 16]), n * 16,
+                          1, 1)
+    assert pkv.device_error() == 0
+    ref = sparse.select(q, bounds, exps, t, start, [n * 16], 16, 40, 1, 1, "bf16")
+    assert np.array_equal(sel.cpu().numpy(), ref)
+
+
+def test_two_captured_selections_share_a_workspace(pkv):
+    """Two graphs with one workspace, replayed in turn: nothing stays in it."""
+    rng = np.random.default_rng(23)
+    calls = []
+    ws = pkv.workspace(8 << 20)
+    for ctx in ([2500, 900, 40], [700, 4000]):
+        t, nb, bounds, exps, q, start = _select_case(rng, "bf16", 8, 2, 64, ctx, [1] * len(ctx))
+        desc = pkv.CacheDesc(pkv.PKV_BF16, nb, 16, 2, 8, 64)
+        args = (to_dev(q, "bf16"), to_dev(bounds), to_dev(exps), desc, i32(t), i32(ctx), max(ctx))
+        sel = torch.full((len(ctx), 2, 30), -9, dtype=torch.int32, device="cuda")
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            pkv.pkv_select_blocks(sel, *args, 1, 1, ws=ws)
+        ref = sparse.select(q, bounds, exps, t, start, ctx, 16, 30, 1, 1, "bf16")
+        calls.append((g, sel, ref, args))
+    for _ in range(4):
+        for g, sel, ref, _ in calls:
+            sel.fill_(-9)
+            g.replay()
+            assert np.array_equal(sel.cpu().numpy(), ref)
+    assert pkv.device_error() == 0
+
+
 # ---- together ------------------------------------------------------------------
 class Serving:
     """A batch served from the device: tables, append, bounds, selection and sparse
