@@ -53,7 +53,8 @@ struct Call {
             char text[192];
             int n = std::snprintf(text, sizeof text, "(");
             for (const int64_t s : want)
-                if (n < int(sizeof text)) n += std::snprintf(text + n, sizeof text - n, "%lld, ", (long long)s);
+                if (n < int(sizeof text))
+                    n += std::snprintf(text + n, sizeof text - n, "%lld, ", (long long)s);
             refuse(PyExc_ValueError, "%s: shape expected %s...)", name, text);
         }
         return t.data_ptr();
@@ -109,7 +110,8 @@ at::ScalarType values_of(const pkv_cache_desc& d) {
     refuse(PyExc_TypeError, "%s dtype must be float32 or bfloat16%s", "cache", "");
 }
 
-PyObject* guarded(PyObject* (*body)(PyObject* const*), PyObject* const* a, Py_ssize_t n, Py_ssize_t want) {
+PyObject* guarded(PyObject* (*body)(PyObject* const*), PyObject* const* a, Py_ssize_t n,
+                  Py_ssize_t want) {
     if (n != want) {
         PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", want, n);
         return nullptr;

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "launch_cache.h"
 #include "pkv_device.cuh"
@@ -196,7 +197,8 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
     // the first entries, asked for before the row's context is known
     const int entry0 = first + lane * stride < p.top_k ? list[first + lane * stride] : -1;
     int seq;
-    const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    const int keys = row_keys(p.rows, t, seq,
+                              threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
     if (keys < 0) {                              // the whole cluster: left as it is
         if (cs > 1) cluster_wait();
         return;
@@ -289,7 +291,8 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int byte = lane * DL * 4;
-                const unsigned char* src = vt + ((k + e) * RC + chunk_at(k + e, byte / 16)) * 16 + byte % 16;
+                const int chunk = (k + e) * RC + chunk_at(k + e, byte / 16);
+                const unsigned char* src = vt + chunk * 16 + byte % 16;
                 Elem<float>::load(reinterpret_cast<const float*>(src), v[e]);
             }
 #pragma unroll
@@ -391,7 +394,8 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
     // the first entries, asked for before the row's context is known
     const int entry0 = first + lane * stride < p.top_k ? list[first + lane * stride] : -1;
     int seq;
-    const int keys = row_keys(p.rows, t, seq, threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    const int keys = row_keys(p.rows, t, seq,
+                              threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
     if (keys < 0) {                              // the whole cluster: left as it is
         if (cs > 1) cluster_wait();
         return;
@@ -525,8 +529,11 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
     if (gid < G) {
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
-            rec[gid * D + n * 8 + 2 * tig] = o[n][0] + o[n][2];
-            rec[gid * D + n * 8 + 2 * tig + 1] = o[n][1] + o[n][3];
+            // (where an infinite value of V makes the sum infinite, P's remainders,
+            // of either sign or 0, would turn it into NaN)
+            const bool f0 = fabsf(o[n][0]) <= FLT_MAX, f1 = fabsf(o[n][1]) <= FLT_MAX;
+            rec[gid * D + n * 8 + 2 * tig] = o[n][0] + (f0 ? o[n][2] : 0.f);
+            rec[gid * D + n * 8 + 2 * tig + 1] = o[n][1] + (f1 ? o[n][3] : 0.f);
         }
         if (tig == 0) {
             rec[G * D + gid] = m;

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
     const int chunk = int(unit / uint32_t(p.num_kv_heads));
     const int h = int(unit % uint32_t(p.num_kv_heads));
     const int t = int(blockIdx.z * gridDim.y + blockIdx.y);
-    if (t >= p.tokens || chunk >= p.chunks) return;
+    if (uint32_t(t) >= uint32_t(p.tokens) || chunk >= p.chunks) return;
     int first, q;
     const int seq = token_seq(p.rows.start, p.rows.n, t, first, q, nullptr);
     const int rows = seq < 0 || (t - first) % R ? 0 : min(R, first + q - t);
@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
             float d[CH][4];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const uint4 v = ring[(js * 2 * CH + 2 * c) * 32], w = ring[(js * 2 * CH + 2 * c + 1) * 32];
+                const uint4 v = ring[(js * 2 * CH + 2 * c) * 32];
+                const uint4 w = ring[(js * 2 * CH + 2 * c + 1) * 32];
                 const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

@@ -445,6 +445,31 @@ def test_scores_of_minus_infinity(pkv, dtype):
     assert_attention(out[:1], ref0, bound)
 
 
+@pytest.mark.parametrize("top_k", [3, 40])
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64),
+                                            ("f32", 4, 2, 64)])
+def test_infinite_values_stay_infinite(pkv, dtype, hq, hkv, d, top_k):
+    """A visible value of +-inf makes its element infinite and no other (each
+    weight is above 2^-100: scores lie within 30 of one another)."""
+    rng = np.random.default_rng(29)
+    n = top_k * 16 - 5
+    t, nb = tables_for(rng, [n])
+    k, v = (values(rng, (nb, hkv, 16, d), dtype) for _ in range(2))
+    q = values(rng, (1, hq, d), dtype, 0.5)
+    vt = to_dev(v, dtype)
+    for at, dim, x in ((0, 3, float("inf")), (n - 1, 3, float("inf")), (n // 2, 8, -float("inf"))):
+        vt[int(t[0, at // 16]), :, at % 16, dim] = x
+    desc = pkv.CacheDesc({"bf16": pkv.PKV_BF16, "f32": pkv.PKV_F32}[dtype], nb, 16, hkv, hq, d)
+    sel = i32(np.tile(np.arange(top_k), (1, hkv, 1)))
+    qt, kt = to_dev(q, dtype), to_dev(k, dtype)
+    out, clean = torch.empty_like(qt), torch.empty_like(qt)
+    pkv.paged_attention_sparse(out, qt, kt, vt, desc, i32(t), i32([n]), sel)
+    pkv.paged_attention_sparse(clean, qt, kt, to_dev(v, dtype), desc, i32(t), i32([n]), sel)
+    assert pkv.device_error() == 0
+    clean[:, :, 3], clean[:, :, 8] = float("inf"), -float("inf")
+    assert torch.equal(out, clean)
+
+
 def test_attention_flags_bad_entries(pkv):
     rng = np.random.default_rng(4)
     ctx = [300, 20]
