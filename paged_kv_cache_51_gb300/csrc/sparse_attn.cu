@@ -40,14 +40,19 @@ struct SparseParams {
 // Floats of a warp's record: outputs [G][D], max [G], sum [G], keys seen.
 constexpr int record_floats(int g, int d) { return (g * (d + 2) + 1 + 3) & ~3; }
 
+// Floats behind the warps' records: their factors [warp][G], and a CTA's sums [G].
+constexpr int factor_floats(int g, int warps) { return ((warps + 1) * g + 3) & ~3; }
+
 // Where a CTA of a cluster finds what the others send it: from each its part of
-// the outputs (G * D / cluster floats) and its (max, sum) per head and keys seen.
+// the outputs (G * D / cluster floats) and its (max, sum) per head.
 template <int D, int kMaxG>
 struct Inbox {
-    static constexpr int kStats = 2 * kMaxG + 1;
     static constexpr int kMaxCluster = 8;
-    static constexpr int kFloats = kMaxG * D + kMaxCluster * kStats;
+    static constexpr int kFloats = kMaxG * D + kMaxCluster * 2 * kMaxG;
 };
+
+// The sum of a CTA that saw no key.
+constexpr uint32_t kNoKeys = 0x80000000u;
 
 template <int D, int G>
 struct SparseF32Cfg {
@@ -59,7 +64,7 @@ struct SparseF32Cfg {
     static constexpr int kPOff = kQOff + G * D * 4;                   // weights [warp][G][16]
     static constexpr int kRec = record_floats(G, D);
     static constexpr int kCombOff = kPOff + kWarps * G * kBlockTokens * 4;
-    static constexpr int kInboxOff = kCombOff + kWarps * kRec * 4;
+    static constexpr int kInboxOff = kCombOff + (kWarps * kRec + factor_floats(G, kWarps)) * 4;
     static constexpr int kSmem = kInboxOff + Inbox<D, G>::kFloats * 4;
 };
 
@@ -67,46 +72,62 @@ struct SparseF32Cfg {
 // two neighbouring chunks) fall into eight different bank groups
 __device__ __forceinline__ int chunk_at(int r, int c) { return c ^ ((r & 3) << 1); }
 
+// What this CTA will get from the cluster's CTAs, itself among them, announced
+// before any of them can send it.
+__device__ __forceinline__ void expect_parts(uint64_t* arrived, int G, int D, uint32_t cs) {
+    if (threadIdx.x == 0) {
+        mbar_init(arrived, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(arrived, uint32_t(G * D + int(cs) * 2 * G) * 4);
+    }
+    __syncwarp();
+    cluster_arrive();                                // (waited for before the others are written to)
+}
+
 // Merge the CTA's warp states (records in shared memory), then the cluster's,
 // and write the outputs of the (row, head): shared by every variant.  Each CTA
-// owns a part of the outputs; the others send it theirs, so that one cluster
-// barrier stands between the merges and none behind them.  The factors of a head
-// are made once, not by every output.
+// owns a part of the outputs; the others send it theirs by stores that count on
+// the owner's mbarrier, so that between the merges a CTA waits for nothing but
+// what it needs (with a cluster barrier there: 9.2 us for 4 rows of 128 blocks,
+// 8.8 so; 8 rows of fp32 3.9 and 3.5).  The factors of a head are made once, not by every output.
 template <typename T, int D, int kMaxG, int kWarps>
 __device__ __forceinline__ void merge_and_write(const SparseParams& p, float* comb, float* inbox,
-                                                int t, int h, int G) {
+                                                uint64_t* arrived, int t, int h, int G) {
     constexpr int kThreads = kWarps * 32;
     constexpr int kRec = record_floats(kMaxG, D);
-    constexpr int kStats = Inbox<D, kMaxG>::kStats;
     const uint32_t cs = cluster_size(), rank = cluster_rank();
     const int part_log2 = 31 - __clz(G * D) - (31 - __clz(int(cs)));   // all powers of two
     const int part = 1 << part_log2;
     const uint32_t in_u = smem_u32(inbox), stats_u = in_u + kMaxG * D * 4;
+    const uint32_t bar_u = smem_u32(arrived);
+    float* fac = comb + kWarps * kRec;
     T* out = static_cast<T*>(p.out) + (size_t(t) * p.num_q_heads + size_t(h) * G) * D;
     __syncthreads();
     if (cs > 1) cluster_wait();                      // the others have started
-    // one head each: the warps' factors over the maxima, and the CTA's statistics
-    if (int(threadIdx.x) < G) {
-        const int g = threadIdx.x;
-        float M = -INFINITY, L = 0.f, seen = 0.f, s[kWarps];
+    // one head each, and one receiver: the warps' factors over the maxima, and the
+    // CTA's statistics
+    static_assert(kMaxG * Inbox<D, kMaxG>::kMaxCluster <= kThreads, "a thread for each");
+    if (threadIdx.x < uint32_t(G) * cs) {
+        const int g = threadIdx.x & (G - 1);
+        const uint32_t c = threadIdx.x / uint32_t(G);
+        float M = -INFINITY, L = 0.f, seen = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[w * kRec + G * D + g]);
         const float Mx = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            s[w] = exp2f(comb[w * kRec + G * D + g] - Mx);
-            L = fmaf(comb[w * kRec + G * D + G + g], s[w], L);
+            const float s = exp2f(comb[w * kRec + G * D + g] - Mx);
+            L = fmaf(comb[w * kRec + G * D + G + g], s, L);
             seen += comb[w * kRec + 2 * G + G * D];
+            if (c == 0) fac[w * G + g] = s;
         }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) comb[w * kRec + G * D + g] = s[w];
-        // (a row whose list names no key it sees is 0)
-        if (cs == 1) comb[G * D + G + g] = seen > 0.f ? L : INFINITY;
-        for (uint32_t c = 0; cs > 1 && c < cs; ++c) {
-            const uint32_t at = map_rank(stats_u + rank * (kStats * 4), c);
-            st_cluster(at + g * 4, __float_as_uint(M));
-            st_cluster(at + (G + g) * 4, __float_as_uint(L));
-            if (g == 0) st_cluster(at + 2 * G * 4, __float_as_uint(seen));
+        if (cs == 1) {
+            // (a row whose list names no key it sees is 0)
+            fac[kWarps * G + g] = seen > 0.f ? L : INFINITY;
+        } else {
+            if (!(seen > 0.f)) L = __uint_as_float(kNoKeys);
+            st_async(map_rank(stats_u + (rank * G + g) * 8, c), map_rank(bar_u, c),
+                     make_float2(M, L));
         }
     }
     __syncthreads();
@@ -119,36 +140,40 @@ __device__ __forceinline__ void merge_and_write(const SparseParams& p, float* co
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float4 o = *reinterpret_cast<const float4*>(comb + w * kRec + i);
-            const float s = comb[w * kRec + G * D + g];
+            const float s = fac[w * G + g];
             O.x = fmaf(o.x, s, O.x);
             O.y = fmaf(o.y, s, O.y);
             O.z = fmaf(o.z, s, O.z);
             O.w = fmaf(o.w, s, O.w);
         }
         if (cs == 1) {
-            const float L = comb[G * D + G + g];
+            const float L = fac[kWarps * G + g];
             const float v[4] = {O.x / L, O.y / L, O.z / L, O.w / L};
 #pragma unroll
             for (int e = 0; e < 4; ++e) out[i + e] = Elem<T>::store_val(v[e]);
         } else {
-            st_cluster(map_rank(in_u + (rank * part + (i & (part - 1))) * 4, i >> part_log2), O);
+            const uint32_t owner = uint32_t(i >> part_log2);
+            st_async(map_rank(in_u + (rank * part + (i & (part - 1))) * 4, owner),
+                     map_rank(bar_u, owner), O);
         }
     }
     if (cs == 1) return;
-    cluster_sync();
-    const float* stats = inbox + kMaxG * D;
+    if (!mbar_wait(arrived, 0, p.err)) return;
+    const float2* stats = reinterpret_cast<const float2*>(inbox + kMaxG * D);
     for (int i = threadIdx.x; i < part; i += kThreads) {
         const int at = int(rank) * part + i, g = at / D;
-        float M = -INFINITY, L = 0.f, O = 0.f, seen = 0.f;
-        for (uint32_t c = 0; c < cs; ++c) M = fmaxf(M, stats[c * kStats + g]);
+        float M = -INFINITY, L = 0.f, O = 0.f;
+        bool seen = false;
+        for (uint32_t c = 0; c < cs; ++c) M = fmaxf(M, stats[c * G + g].x);
         const float Mx = M == -INFINITY ? 0.f : M;
         for (uint32_t c = 0; c < cs; ++c) {
-            const float s = exp2f(stats[c * kStats + g] - Mx);
-            L = fmaf(stats[c * kStats + G + g], s, L);
+            const float2 ml = stats[c * G + g];
+            const float s = exp2f(ml.x - Mx);
+            L = fmaf(ml.y, s, L);
             O = fmaf(inbox[c * part + i], s, O);
-            seen += stats[c * kStats + 2 * G];
+            seen |= __float_as_uint(ml.y) != kNoKeys;
         }
-        out[at] = Elem<T>::store_val(seen > 0.f ? O / L : 0.f);
+        out[at] = Elem<T>::store_val(seen ? O / L : 0.f);
     }
 }
 
@@ -185,11 +210,12 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
     float* qs = reinterpret_cast<float*>(smem + C::kQOff);
     float* comb = reinterpret_cast<float*>(smem + C::kCombOff);
     float* inbox = reinterpret_cast<float*>(smem + C::kInboxOff);
+    __shared__ uint64_t arrived;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t cs = cluster_size(), rank = cluster_rank();
     const int item = int(blockIdx.x / cs);
     const int t = item / p.num_kv_heads, h = item % p.num_kv_heads;
-    if (cs > 1) cluster_arrive();                // (waited for before the others are written to)
+    if (cs > 1) expect_parts(&arrived, G, D, cs);
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int32_t* list = p.selected + size_t(item) * p.top_k;
@@ -322,7 +348,7 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<float, D, G, C::kWarps>(p, comb, inbox, t, h, G);
+    merge_and_write<float, D, G, C::kWarps>(p, comb, inbox, &arrived, t, h, G);
 }
 
 // ---- bf16 on tensor cores -------------------------------------------------------
@@ -362,7 +388,8 @@ struct SparseBf16Cfg {
     static constexpr int kRec = record_floats(kMaxG, D);
     // (the warps' records go over the ring)
     static constexpr int kSmem = kRingBytes + Inbox<D, kMaxG>::kFloats * 4;
-    static_assert(kWarps * kRec * 4 <= kRingBytes, "records fit into the ring");
+    static_assert((kWarps * kRec + factor_floats(kMaxG, kWarps)) * 4 <= kRingBytes,
+                  "records fit into the ring");
 };
 
 // The same work on warp-level tensor-core products (m16n8k16): S = q K^T with
@@ -372,7 +399,7 @@ struct SparseBf16Cfg {
 // product to 2^-16 of itself at no extra instruction.  A ring of three tiles a warp
 // and two CTAs an SM keep 192 KB in flight: 256 rows x 8 heads x 64 blocks (1.07 GB)
 // 158 us, 6.8 TB/s (two tiles and three CTAs: 165 us); 4 rows x 8 heads x 128 blocks
-// (34 MB), in clusters of 8, 9.5 us.
+// (34 MB), in clusters of 8, 8.8 us.
 template <int D>
 __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_kernel(SparseParams p) {
     using C = SparseBf16Cfg<D>;
@@ -380,13 +407,14 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
     extern __shared__ __align__(128) unsigned char smem[];
     float* comb = reinterpret_cast<float*>(smem);
     float* inbox = reinterpret_cast<float*>(smem + C::kRingBytes);
+    __shared__ uint64_t arrived;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3, mi = lane >> 3;
     const int G = p.num_q_heads / p.num_kv_heads;
     const uint32_t cs = cluster_size(), rank = cluster_rank();
     const int item = int(blockIdx.x / cs);
     const int t = item / p.num_kv_heads, h = item % p.num_kv_heads;
-    if (cs > 1) cluster_arrive();                // (waited for before the others are written to)
+    if (cs > 1) expect_parts(&arrived, G, D, cs);
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int32_t* list = p.selected + size_t(item) * p.top_k;
@@ -541,7 +569,7 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
         }
     }
     if (lane == 0) rec[G * (D + 2)] = float(seen);
-    merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps>(p, comb, inbox, t, h, G);
+    merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps>(p, comb, inbox, &arrived, t, h, G);
 }
 
 // CTAs that share one (row, head): those that take the fewest steps, when `slots`
