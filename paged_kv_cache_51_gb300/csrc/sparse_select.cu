@@ -330,7 +330,7 @@ __device__ __forceinline__ void load16(const SelectParams& p, size_t at, float (
 // that it will use itself (two rows' 16 bytes of each 64) into places of its own
 // in shared memory, a few tiles ahead.  Nothing waits for another lane or warp,
 // and the SM's other warps hide the start of each (context, ids, bounds: three
-// dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 30 us
+// dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 32 us
 // of the call's 37, where a copy of the same rows alone takes 26; bound by HBM's
 // rate for gathered 256-byte rows and by the start and the end of the launch.
 template <int D, int G, int R>
@@ -557,39 +557,33 @@ struct PickScratch {
     static constexpr int kWarps = NT / 32;
     static constexpr int kBins = 4 * NT;
     uint32_t hist[kBins];
-    uint32_t cand[NT];
+    uint4 cand[16];                              // two (key, block) of the last bin in each
     uint32_t warp_a[kWarps], warp_b[kWarps];
-    uint32_t bin, above, inside, count, cut, take;
+    uint32_t bin, above, inside, count;
 };
 
-// Sums of two values over the warps in front of this one (each value is the
-// same for a warp's lanes).
-template <int NT>
-__device__ __forceinline__ void warps_before(uint32_t& a, uint32_t& b, PickScratch<NT>& s) {
-    const int warp = threadIdx.x >> 5;
-    s.warp_a[warp] = a;
-    s.warp_b[warp] = b;
-    __syncthreads();
-    a = b = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32 - 1; ++w) {
-        a += w < warp ? s.warp_a[w] : 0u;
-        b += w < warp ? s.warp_b[w] : 0u;
-    }
+// Sums of a value over the warps in front of this one (the same for a warp's
+// lanes, and written to `of_warps` by all of them before a barrier).
+__device__ __forceinline__ uint32_t warps_before(const uint32_t* of_warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    return __reduce_add_sync(kFull, lane < warp ? of_warps[lane] : 0u);
 }
 
 // One CTA of NT threads for the list of a (query row, KV head).  Wanted are the
 // `want` largest keys of blocks sink .. blocks - recent - 1 (the ends are always
-// taken).  A histogram over the keys' range finds the bin that holds the want-th;
-// its few keys are ranked against one another, or, while they are more than the
-// CTA ranks at once, the bin becomes the next range.  Scores of a real query
-// spread over the bins, so one histogram and one ranking is the rule.  A row's
-// keys stay in registers, kHeld to a thread, asked for before the row's context
-// is known; with kHeld 0 (rows longer than that) every pass reads them again.
-// Keys of real blocks lie between those of the two infinities; the ends carry a
-// key above all and places behind the row one below all, so that no pass has to
-// look at indices.  Bound by its chain of barriers: 7 us behind the scores for 2048
-// rows of up to 512 blocks, 4 us for 32 rows of 2048.
+// taken).  A histogram over the keys' range finds the bin that holds the want-th.
+// Its few keys are ranked by every warp for itself, with the lower index first
+// among equals, and where each warp's part of the list begins follows from the
+// same ranks: one barrier between the histogram and the list.  While the bin holds
+// more keys than a warp ranks at once it becomes the next range.  Scores of a real
+// query spread over the bins, so one histogram and one ranking is the rule.  A
+// row's keys stay in registers, kHeld to a thread, asked for before the row's
+// context is known; with kHeld 0 (rows longer than that) every pass reads them
+// again.  Keys of real blocks lie between those of the two infinities; the ends
+// carry a key above all and places behind the row one below all, so that no pass
+// has to look at indices.  2048 rows of up to 512 blocks: 5.4 us behind the scores,
+// of which 2.4 start the CTAs and 2.0 rank and write; 32 rows of 2048: 2.7 us, a
+// chain of barriers.
 template <int NT, int kHeld>
 __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
     using S = PickScratch<NT>;
@@ -599,6 +593,7 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 #pragma unroll
     for (int i = 0; i < 4; ++i) s.hist[i * NT + tid] = 0;
+    if (tid < 16) s.cand[tid] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) s.count = 0;
     const int h = int(blockIdx.x % uint32_t(p.num_kv_heads));
     const int t = int(blockIdx.x / uint32_t(p.num_kv_heads));
@@ -637,6 +632,19 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
             for (int b = b0 + tid; b < b1; b += NT) f(far[b]);
         }
     };
+    // this warp's stretch of the row (ascending with the warps), 32 blocks at a time
+    const int stretch = Held ? 32 * kHeld : ((blocks + S::kWarps - 1) / S::kWarps + 31) & ~31;
+    auto in_order = [&](auto f) {                // f(block, key)
+        if (Held) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) f(mine + 32 * i, held[i]);
+        } else {
+            const int end = min(blocks, (warp + 1) * stretch);
+            for (int b = warp * stretch + lane; b - lane < end; b += 32)
+                f(b, b < end ? marked(b, far[b]) : kNone);
+        }
+    };
+    const uint32_t below = (1u << lane) - 1u;
     uint32_t want = uint32_t(p.top_k - p.sink - p.recent);
     uint32_t cut = kEnd - 1, take = 0;           // taken: keys above `cut`, `take` equal to it
     if (want > 0) {
@@ -672,9 +680,9 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
                 const uint32_t u = __shfl_up_sync(kFull, sum, o);
                 if (lane >= o) sum += u;
             }
-            uint32_t before = __shfl_sync(kFull, sum, 31), none = 0;
-            warps_before<NT>(before, none, s);
-            sum += before - own;
+            if (lane == 31) s.warp_a[warp] = sum;
+            __syncthreads();
+            sum += warps_before(s.warp_a) - own;
             if (sum < want && want <= sum + own) {   // exactly one thread
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -691,30 +699,41 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
             want -= s.above;
             const uint32_t first = lo + (s.bin << shift);
             const uint32_t last = min(hi, first + ((1u << shift) - 1u));
+            if (inside <= 32) {
+                uint32_t n = 0;
+                in_order([&](int b, uint32_t k) {
+                    n += __popc(__ballot_sync(kFull, k > last));
+                    if (k - first <= last - first)
+                        reinterpret_cast<uint2*>(s.cand)[atomicAdd(&s.count, 1u)] =
+                            make_uint2(k, uint32_t(b));
+                });
+                if (lane == 0) s.warp_a[warp] = n;
+                __syncthreads();
+                const uint2 c = reinterpret_cast<const uint2*>(s.cand)[lane];
+                uint32_t rank = lane < int(inside) ? 0u : want;
+                for (uint32_t j = 0; j < inside; j += 4) {   // (places behind the last hold 0)
+                    const uint4 o = s.cand[j / 2], u = s.cand[j / 2 + 1];
+                    rank += o.x > c.x || (o.x == c.x && o.y < c.y);
+                    rank += o.z > c.x || (o.z == c.x && o.w < c.y);
+                    rank += u.x > c.x || (u.x == c.x && u.y < c.y);
+                    rank += u.z > c.x || (u.z == c.x && u.w < c.y);
+                }
+                // the last one taken
+                const int at = __ffs(__ballot_sync(kFull, rank == want - 1)) - 1;
+                const uint32_t ck = __shfl_sync(kFull, c.x, at);
+                const int cb = int(__shfl_sync(kFull, c.y, at));
+                n = warps_before(s.warp_a) +
+                    __popc(__ballot_sync(kFull, rank < want && int(c.y) < warp * stretch));
+                in_order([&](int b, uint32_t k) {
+                    const bool in = k > ck || (k == ck && b <= cb);
+                    const uint32_t m = __ballot_sync(kFull, in);
+                    if (in) out[n + __popc(m & below)] = b;
+                    n += __popc(m);
+                });
+                return;
+            }
             if (want == inside) {                // the whole bin (no key is 0: -inf's is above)
                 cut = first - 1;
-                break;
-            }
-            if (inside <= uint32_t(NT)) {
-                each([&](uint32_t k) {
-                    if (k - first <= last - first) s.cand[atomicAdd(&s.count, 1u)] = k;
-                });
-                __syncthreads();
-                if (tid < int(inside)) {
-                    const uint32_t k = s.cand[tid];
-                    uint32_t gt = 0, ge = 0;
-                    for (uint32_t j = 0; j < inside; ++j) {
-                        gt += s.cand[j] > k;
-                        ge += s.cand[j] >= k;
-                    }
-                    if (gt < want && want <= ge) {   // the same for all keys equal to the cut
-                        s.cut = k;
-                        s.take = want - gt;
-                    }
-                }
-                __syncthreads();
-                cut = s.cut;
-                take = s.take;
                 break;
             }
             lo = first;
@@ -725,43 +744,24 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
             __syncthreads();
         }
     }
-    // in ascending order: a stretch of blocks to a warp, whose counts are summed
-    // first; within a warp 32 blocks at a time by ballot
-    const uint32_t below = (1u << lane) - 1u;
+    // in ascending order: each warp's counts are summed first
     uint32_t n_above = 0, n_equal = 0;
-    auto place = [&](int b, uint32_t k, uint32_t ma, uint32_t me) {
+    in_order([&](int, uint32_t k) {
+        n_above += __popc(__ballot_sync(kFull, k > cut));
+        n_equal += __popc(__ballot_sync(kFull, k == cut));
+    });
+    __syncthreads();                             // (what the warps left there was read by all)
+    if (lane == 0) s.warp_a[warp] = n_above, s.warp_b[warp] = n_equal;
+    __syncthreads();
+    n_above = warps_before(s.warp_a);
+    n_equal = warps_before(s.warp_b);
+    in_order([&](int b, uint32_t k) {
+        const uint32_t ma = __ballot_sync(kFull, k > cut), me = __ballot_sync(kFull, k == cut);
         const uint32_t at = n_above + __popc(ma & below), nth = n_equal + __popc(me & below);
         if (k > cut || (k == cut && nth < take)) out[at + min(nth, take)] = b;
         n_above += __popc(ma);
         n_equal += __popc(me);
-    };
-    if (Held) {
-        uint32_t ma[Held ? kHeld : 1], me[Held ? kHeld : 1];
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            ma[i] = __ballot_sync(kFull, held[i] > cut);
-            me[i] = __ballot_sync(kFull, held[i] == cut);
-            n_above += __popc(ma[i]);
-            n_equal += __popc(me[i]);
-        }
-        warps_before<NT>(n_above, n_equal, s);
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) place(mine + 32 * i, held[i], ma[i], me[i]);
-    } else {
-        const int stretch = ((blocks + S::kWarps - 1) / S::kWarps + 31) & ~31;
-        const int f = min(blocks, warp * stretch), e = min(blocks, f + stretch);
-        auto key = [&](int b) { return b < e ? marked(b, far[b]) : kNone; };
-        for (int b = f; b < e; b += 32) {
-            const uint32_t k = key(b + lane);
-            n_above += __popc(__ballot_sync(kFull, k > cut));
-            n_equal += __popc(__ballot_sync(kFull, k == cut));
-        }
-        warps_before<NT>(n_above, n_equal, s);
-        for (int b = f; b < e; b += 32) {
-            const uint32_t k = key(b + lane);
-            place(b + lane, k, __ballot_sync(kFull, k > cut), __ballot_sync(kFull, k == cut));
-        }
-    }
+    });
 }
 
 size_t select_stride(int32_t max_ctx) {
@@ -770,11 +770,14 @@ size_t select_stride(int32_t max_ctx) {
 
 template <int D, int G, int R>
 int launch_scores_r(SelectParams p, cudaStream_t stream) {
-    // chunks that give every SM some tens of warps, of 2 to 16 tiles each
+    // chunks of 4 to 16 tiles that give every SM some tens of warps, of 2 for a few
+    // rows (8 items of 2048 blocks: 6.1 us, 7.1 with chunks of 4; 32 items: 9.0
+    // and 8.7)
     const int64_t items = ceil_div(int64_t(p.tokens), R) * int64_t(p.num_kv_heads);
     const int tiles = ceil_div(p.stride, kTileBlocks);
     p.chunk_tiles = 16;
-    while (p.chunk_tiles > 2 && items * ceil_div(tiles, p.chunk_tiles) < 32 * int64_t(num_sms()))
+    while (p.chunk_tiles > 2 && items * ceil_div(tiles, p.chunk_tiles) <
+                                    (p.chunk_tiles > 4 ? 32 : 2) * int64_t(num_sms()))
         p.chunk_tiles /= 2;
     p.chunks = ceil_div(tiles, p.chunk_tiles);
     const int64_t units = int64_t(p.chunks) * p.num_kv_heads;
@@ -808,13 +811,16 @@ int launch_pick_t(const SelectParams& p, cudaStream_t s) {
                                   s, p));
 }
 
-// The least threads that hold a row's keys, four to eight each.  (2048 rows of up
-// to 512 blocks, the whole call: 39.3 us with four warps to a row, 40.9 with two;
-// one alone takes 21 us where two take 7.)
+// Threads that hold a row's keys, four to sixteen each.  The whole call: 32 rows of
+// 2048 blocks 8.5 us with 256 threads, 8.9 with 512, 9.6 with 128; 768 such rows 38,
+// 39 and 39.5; 8 rows of 8192 blocks 10.7 us with 512 threads, 12.9 with 256, 14.1
+// by passes over memory.  Longer rows take as many threads as there are: 8 rows of
+// 16384 blocks 19 to 21 us, 28 with 512.
 int launch_pick(const SelectParams& p, cudaStream_t s) {
     if (p.stride <= 128 * 4) return launch_pick_t<128, 4>(p, s);
     if (p.stride <= 256 * 8) return launch_pick_t<256, 8>(p, s);
-    return launch_pick_t<512, 0>(p, s);
+    if (p.stride <= 512 * 16) return launch_pick_t<512, 16>(p, s);
+    return launch_pick_t<1024, 0>(p, s);
 }
 
 bool aligned_to(const void* p, uintptr_t a) {

@@ -208,6 +208,28 @@ def test_selection_from_keys_in_few_bins(pkv, kind):
         assert np.array_equal(got, ref)
 
 
+@pytest.mark.parametrize("n", [129, 512, 513, 2048, 2049, 8192, 8193])
+@pytest.mark.parametrize("levels", [1, 2, 31, 64, 5000])
+def test_selection_at_the_ends_of_the_row_lengths(pkv, n, levels):
+    """Rows at the limits of the kernels' lengths, their scores of few or many
+    different values, one of them far from the others."""
+    rng = np.random.default_rng(n + levels)
+    d = 64
+    bounds = np.zeros((n, 2, 2, d), np.int8)
+    exps = np.zeros((n, 2), np.int8)
+    value = rng.integers(0, levels, (n, 2))
+    bounds[:, :, 0, 0], bounds[:, :, 0, 1] = value // 100, value % 100
+    exps[rng.integers(0, n), 1] = 20
+    q = np.zeros((1, 2, d), np.float32)
+    q[0, :, 0], q[0, :, 1] = 100.0, 1.0
+    t = rng.permutation(n).astype(np.int32)[None, :]
+    for top_k, sink, recent in ((2, 0, 1), (5, 1, 2), (100, 4, 30), (n - 1, 1, 1)):
+        got = _run_select(pkv, "f32", q, bounds, exps, t, [n * 16], [0, 1], top_k, sink, recent)
+        assert pkv.device_error() == 0
+        ref = sparse.select(q, bounds, exps, t, [0, 1], [n * 16], 16, top_k, sink, recent, "f32")
+        assert np.array_equal(got, ref)
+
+
 def test_selection_with_values_that_are_not_finite(pkv):
     rng = np.random.default_rng(5)
     ctx = [600, 600, 600]
