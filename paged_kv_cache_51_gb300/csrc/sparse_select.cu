@@ -260,7 +260,7 @@ struct SelectParams {
 
 constexpr int kScoreWarps = 4;
 constexpr int kTileBlocks = 16;      // blocks of a product tile
-constexpr int kScoreStages = 3;      // tiles in flight per warp
+constexpr int kScoreStages = 2;      // tiles in flight per warp
 
 // Floats in an order that unsigned compare keeps (no NaN among the scores).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -328,10 +328,10 @@ __device__ __forceinline__ void load16(const SelectParams& p, size_t at, float (
 // Every warp works alone on a chunk of a row's tiles: it makes the codes in the
 // registers that the product takes them from, and every lane copies the bounds
 // that it will use itself (two rows' 16 bytes of each 64) into places of its own
-// in shared memory, a few tiles ahead.  Nothing waits for another lane or warp,
+// in shared memory, a tile ahead.  Nothing waits for another lane or warp,
 // and the SM's other warps hide the start of each (context, ids, bounds: three
-// dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 32 us
-// of the call's 37, where a copy of the same rows alone takes 26; bound by HBM's
+// dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 31 us
+// of the call's 37 (with two tiles ahead 32), where a copy of the same rows alone takes 26; bound by HBM's
 // rate for gathered 256-byte rows and by the start and the end of the launch.
 template <int D, int G, int R>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(SelectParams p) {
