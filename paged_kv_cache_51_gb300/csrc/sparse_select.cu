@@ -254,7 +254,9 @@ struct SelectParams {
     int32_t tokens, num_blocks, num_q_heads, num_kv_heads;
     int32_t top_k, sink, recent;
     int32_t q_f32;              // q is fp32, else bf16
-    int32_t chunk_tiles, chunks;   // tiles that one warp scores, and such chunks of a row
+    // tiles that one warp scores, and CTAs of a query row: of the first rows, and of
+    // the others, which begin at `fine_row` and at CTA `fine_cta`
+    int32_t chunk_tiles, row_ctas, fine_tiles, fine_ctas, fine_row, fine_cta;
     int* err;
 };
 
@@ -330,8 +332,8 @@ __device__ __forceinline__ void load16(const SelectParams& p, size_t at, float (
 // that it will use itself (two rows' 16 bytes of each 64) into places of its own
 // in shared memory, a tile ahead.  Nothing waits for another lane or warp,
 // and the SM's other warps hide the start of each (context, ids, bounds: three
-// dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 31 us
-// of the call's 37 (with two tiles ahead 32), where a copy of the same rows alone
+// dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 29 us
+// of the call's 35, where a copy of the same rows alone
 // takes 26; bound by HBM's rate for gathered 256-byte rows and by the start and the
 // end of the launch.
 template <int D, int G, int R>
@@ -346,11 +348,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     // neighbouring warps take neighbouring heads: their bounds lie side by side
-    const uint32_t unit = blockIdx.x * kScoreWarps + warp;
+    const bool fine = int(blockIdx.x) >= p.fine_cta;
+    const int chunk_tiles = fine ? p.fine_tiles : p.chunk_tiles;
+    const uint32_t cta = blockIdx.x - (fine ? p.fine_cta : 0);
+    const uint32_t ctas = fine ? p.fine_ctas : p.row_ctas;
+    const int t = int(cta / ctas) + (fine ? p.fine_row : 0);
+    const uint32_t unit = cta % ctas * kScoreWarps + warp;
     const int chunk = int(unit / uint32_t(p.num_kv_heads));
     const int h = int(unit % uint32_t(p.num_kv_heads));
-    const int t = int(blockIdx.z * gridDim.y + blockIdx.y);
-    if (uint32_t(t) >= uint32_t(p.tokens) || chunk >= p.chunks) return;
     int first, q;
     const int seq = token_seq(p.rows.start, p.rows.n, t, first, q, nullptr);
     const int rows = seq < 0 || (t - first) % R ? 0 : min(R, first + q - t);
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
     // asked for at once, before the context is known: the first tile's ids and
     // the values of this lane's query head (column gid)
     const int32_t* table = p.rows.block_tables + size_t(seq) * p.rows.table_stride;
-    const int base = chunk * p.chunk_tiles * kTileBlocks;
+    const int base = chunk * chunk_tiles * kTileBlocks;
     const int last = p.rows.table_stride - 1;
     int id0 = table[min(base + gid, last)], id1 = table[min(base + gid + 8, last)];
     float x[NP][16];
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
     const int blocks = (keys_end + kBlockTokens - 1) / kBlockTokens;
     // (a row whose blocks are all taken needs no scores)
     if (blocks <= p.top_k || base >= blocks) return;
-    const int end = min(blocks, base + p.chunk_tiles * kTileBlocks);
+    const int end = min(blocks, base + chunk_tiles * kTileBlocks);
 
     // this lane's two rows of a tile are blocks gid and gid + 8
     constexpr int kBadId = 1000;                 // exponent of an id outside the pool
@@ -771,21 +776,30 @@ size_t select_stride(int32_t max_ctx) {
 
 template <int D, int G, int R>
 int launch_scores_r(SelectParams p, cudaStream_t stream) {
-    // chunks of 4 to 16 tiles that give every SM some tens of warps, of 2 for a few
-    // rows (8 items of 2048 blocks: 6.1 us, 7.1 with chunks of 4; 32 items: 9.0
-    // and 8.7)
+    // Chunks of 4 to 16 tiles that give every SM some warps, of 2 for a few rows (8
+    // items of 2048 blocks: 6.1 us, 7.1 with chunks of 4; 32 items: 9.0 and 8.7).
+    // Where they are longer than 4, the last fifth of the rows goes in chunks of 4,
+    // so that the SMs run dry at about the same time.  The whole call, 256 rows of 64
+    // to 512 blocks / 48 x 2 of 2048: 34.7 / 35.2 us; with no fine rows 37.2 / 36.8,
+    // with half of them fine 35.8 / 37.5, with chunks of 8 throughout 36.8 / 37.5.
     const int64_t items = ceil_div(int64_t(p.tokens), R) * int64_t(p.num_kv_heads);
     const int tiles = ceil_div(p.stride, kTileBlocks);
+    auto ctas = [&](int chunk_tiles) {           // of a row
+        return ceil_div(ceil_div(tiles, chunk_tiles) * int64_t(p.num_kv_heads), kScoreWarps);
+    };
     p.chunk_tiles = 16;
     while (p.chunk_tiles > 2 && items * ceil_div(tiles, p.chunk_tiles) <
-                                    (p.chunk_tiles > 4 ? 32 : 2) * int64_t(num_sms()))
+                                    (p.chunk_tiles > 4 ? 8 : 2) * int64_t(num_sms()))
         p.chunk_tiles /= 2;
-    p.chunks = ceil_div(tiles, p.chunk_tiles);
-    const int64_t units = int64_t(p.chunks) * p.num_kv_heads;
-    const unsigned gy = unsigned(std::min(p.tokens, 65535));
-    return cuda_status(launch_pdl(block_scores_kernel<D, G, R>,
-                                  dim3(unsigned((units + kScoreWarps - 1) / kScoreWarps), gy,
-                                       unsigned(ceil_div(p.tokens, gy))),
+    p.fine_tiles = std::min(p.chunk_tiles, 4);
+    p.fine_row = p.fine_tiles < p.chunk_tiles ? p.tokens - p.tokens / 5 : p.tokens;
+    p.row_ctas = ctas(p.chunk_tiles);
+    p.fine_ctas = ctas(p.fine_tiles);
+    const int64_t coarse = int64_t(p.fine_row) * p.row_ctas;
+    const int64_t all = coarse + int64_t(p.tokens - p.fine_row) * p.fine_ctas;
+    if (all > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    p.fine_cta = int32_t(coarse);
+    return cuda_status(launch_pdl(block_scores_kernel<D, G, R>, dim3(unsigned(all)),
                                   dim3(kScoreWarps * 32), 0, stream, p));
 }
 

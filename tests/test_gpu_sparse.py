@@ -230,6 +230,22 @@ def test_selection_at_the_ends_of_the_row_lengths(pkv, n, levels):
         assert np.array_equal(got, ref)
 
 
+@pytest.mark.parametrize("rows,hq,hkv,qlen", [(41, 16, 8, 1), (23, 32, 8, 2), (14, 8, 8, 3),
+                                              (19, 8, 8, 1)])
+def test_selection_of_batches_in_long_and_short_stretches(pkv, rows, hq, hkv, qlen):
+    """Batches large enough for stretches of 128 or 256 blocks, the last rows in
+    shorter ones; contexts of every length among them."""
+    rng = np.random.default_rng(rows)
+    ctx = [int(x) for x in rng.integers(qlen, 1300 * 16, rows)]
+    ctx[0], ctx[-1], ctx[rows // 2] = 1300 * 16, 1299 * 16 + 1, qlen
+    lens = [qlen - (i % 3 == 1 and qlen > 1) for i in range(rows)]
+    t, nb, bounds, exps, q, start = _select_case(rng, "bf16", hq, hkv, 64, ctx, lens)
+    got = _run_select(pkv, "bf16", q, bounds, exps, t, ctx, start, 48, 1, 2, layout=qlen > 1)
+    assert pkv.device_error() == 0
+    ref = sparse.select(q, bounds, exps, t, start, ctx, 16, 48, 1, 2, "bf16")
+    assert np.array_equal(got, ref)
+
+
 def test_selection_with_values_that_are_not_finite(pkv):
     rng = np.random.default_rng(5)
     ctx = [600, 600, 600]
