@@ -333,9 +333,8 @@ __device__ __forceinline__ void load16(const SelectParams& p, size_t at, float (
 // in shared memory, a tile ahead.  Nothing waits for another lane or warp,
 // and the SM's other warps hide the start of each (context, ids, bounds: three
 // dependent loads).  256 rows of 64 to 512 blocks, 8 heads (152 MB of bounds): 29 us
-// of the call's 35, where a copy of the same rows alone
-// takes 26; bound by HBM's rate for gathered 256-byte rows and by the start and the
-// end of the launch.
+// of the call's 35, where a copy of the same rows alone takes 26; bound by HBM's rate
+// for gathered 256-byte rows and by the start and the end of the launch.
 template <int D, int G, int R>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(SelectParams p) {
     __shared__ __align__(128) uint4 ring_all[kScoreWarps][kScoreStages][2 * D / 32][32];
