@@ -659,7 +659,7 @@ extern "C" int paged_attention_sparse(void* out, const void* q, const void* k_ca
     p.v_cache = v_cache;
     p.selected = selected;
     p.rows = QueryRows{block_tables, query_start_loc, context_lens, max_blocks_per_seq, num_seqs,
-                       INT32_MAX};
+                       INT32_MAX, num_query_tokens};
     p.num_blocks = desc->num_blocks;
     p.num_q_heads = desc->num_q_heads;
     p.num_kv_heads = desc->num_kv_heads;

@@ -11,14 +11,17 @@ struct QueryRows {
     const int32_t* start;          // query_start_loc [n + 1], or null: one row per sequence
     const int32_t* ctx;            // context_lens [n]
     int32_t table_stride, n, max_ctx;
+    int32_t tokens;                // query rows that the call was given
 };
 
 // Sequence of query token t, found by a whole warp: t itself without
 // query_start_loc, else the last one that starts at or before t; -1 for a token
 // behind the last sequence.  `first` is the sequence's first token, `count` its
-// number of tokens.  A batch of single tokens or of up to 32 sequences is answered
-// by one round of loads, others by one more for every factor of 32 in their number.
-__device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int& first,
+// number of tokens, all of them among the `tokens` rows of the call: where the
+// offsets end above that, or a sequence above their end, the answer is -1 too.
+// A batch of single tokens or of up to 32 sequences is answered by one round of
+// loads, others by one more for every factor of 32 in their number.
+__device__ __forceinline__ int token_seq(const int32_t* start, int n, int tokens, int t, int& first,
                                          int& count, int* err) {
     if (!start) {
         first = t;
@@ -32,6 +35,10 @@ __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int
     int lo = min(t, n - 1);
     first = start[lo];
     int next = start[lo + 1];
+    if (total > tokens) {
+        flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
+        return -1;
+    }
     if (t >= total) return -1;
     if (t < first || t >= next) {
         // (of several sequences that start there, those before the last are empty)
@@ -57,6 +64,10 @@ __device__ __forceinline__ int token_seq(const int32_t* start, int n, int t, int
             return -1;
         }
     }
+    if (next > total) {
+        flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
+        return -1;
+    }
     count = next - first;
     return lo;
 }
@@ -81,7 +92,7 @@ __device__ __forceinline__ bool sequence_keys(const QueryRows& r, int seq, int q
 // behind the last sequence.
 __device__ __forceinline__ int row_keys(const QueryRows& r, int t, int& seq, int* err) {
     int first, q;
-    seq = token_seq(r.start, r.n, t, first, q, err);
+    seq = token_seq(r.start, r.n, r.tokens, t, first, q, err);
     if (seq < 0) return -1;
     return sequence_keys(r, seq, q, err) ? r.ctx[seq] - q + (t - first) + 1 : 0;
 }

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(BoundsP
     if (t0 >= p.tokens) return;
     int* const tell = h == 0 ? p.err : nullptr;
     int first, q, id = -1, nrow = 0;
-    int s = token_seq(p.start, p.n, int(t0), first, q, lane == 0 ? tell : nullptr);
+    int s = token_seq(p.start, p.n, p.tokens, int(t0), first, q, lane == 0 ? tell : nullptr);
     const int64_t t = t0 + lane;
     if (lane < p.span && t < p.tokens && s >= 0) {
         // the lane's own token: a later sequence than the first token's, perhaps
@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(Selec
     const int chunk = int(unit / uint32_t(p.num_kv_heads));
     const int h = int(unit % uint32_t(p.num_kv_heads));
     int first, q;
-    const int seq = token_seq(p.rows.start, p.rows.n, t, first, q, nullptr);
+    const int seq = token_seq(p.rows.start, p.rows.n, p.tokens, t, first, q, nullptr);
+    // (the sequence's rows are rows of the call, so the group's are)
     const int rows = seq < 0 || (t - first) % R ? 0 : min(R, first + q - t);
     if (rows == 0) return;                       // another warp's row, or behind the last one
     // asked for at once, before the context is known: the first tile's ids and
@@ -939,7 +940,7 @@ extern "C" int pkv_select_blocks(int32_t* selected, const void* q, const int8_t*
     p.bounds = bounds;
     p.exps = exps;
     p.rows = QueryRows{block_tables, query_start_loc, context_lens, max_blocks_per_seq, num_seqs,
-                       max_context_len};
+                       max_context_len, num_query_tokens};
     p.keys = static_cast<uint32_t*>(workspace);
     p.stride = int32_t(select_stride(max_context_len));
     p.tokens = num_query_tokens;
