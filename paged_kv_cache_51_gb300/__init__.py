@@ -503,6 +503,16 @@ def workspace(nbytes, device=None):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def _own_workspace(nbytes, device, stream):
+    """A workspace that a call takes for itself.  It comes from the pool of the stream
+    that the call runs on: memory of the current stream's may still be in use by
+    what was enqueued there, which another stream does not wait for."""
+    if stream is None:
+        return workspace(nbytes, device)
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, device)
+
+
 def paged_attention_decode(out, q, k_cache, v_cache, desc, block_tables, context_lens,
                            max_context_len, scale=None, ws=None, stream=None):
     """out, q: CUDA [S, Hq, D]; block_tables int32 [S, W]; context_lens int32 [S]."""
@@ -783,13 +793,13 @@ def pkv_select_blocks(selected, q, bounds, exps, desc, block_tables, context_len
                       stream=None):
     """List the blocks that each (query token, KV head) attends: selected CUDA int32
     [T, Hkv, top_k], q [T, Hq, D]."""
+    handle = _handle(stream)
     if ws is None:
-        ws = workspace(select_workspace_bytes(desc, q.shape[0], max_context_len), q.device)
-        if stream is not None:
-            ws.record_stream(stream)       # it is given back while that stream may still use it
+        ws = _own_workspace(select_workspace_bytes(desc, q.shape[0], max_context_len), q.device,
+                            stream)
     _check(_native().select_blocks(selected, q, bounds, exps, desc, block_tables, context_lens,
                                      max_context_len, num_sink, num_recent, query_start_loc, ws,
-                                     _handle(stream)), "pkv_select_blocks")
+                                     handle), "pkv_select_blocks")
     return selected
 
 
