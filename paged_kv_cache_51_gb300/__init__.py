@@ -528,7 +528,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, desc, block_tables, context
                            ("v_cache", v_cache), ("block_tables", block_tables),
                            ("context_lens", context_lens), ("ws", ws))
     if ws is None:
-        ws = workspace(decode_workspace_bytes(desc, S, max_context_len), q.device)
+        ws = _own_workspace(decode_workspace_bytes(desc, S, max_context_len), q.device, stream)
     _check(lib().paged_attention_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                         ctypes.byref(desc), _ptr(block_tables),
                                         block_tables.shape[1], _ptr(context_lens), S,
@@ -587,8 +587,8 @@ def paged_attention_varlen(out, q, k_cache, v_cache, desc, block_tables, query_s
                            ("query_start_loc", query_start_loc), ("context_lens", context_lens),
                            ("ws", ws))
     if ws is None:
-        ws = workspace(varlen_workspace_bytes(desc, S, Tq, max_query_len, max_context_len),
-                       q.device)
+        ws = _own_workspace(varlen_workspace_bytes(desc, S, Tq, max_query_len, max_context_len),
+                            q.device, stream)
     if window:
         _check(lib().paged_attention_varlen_window(
             _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
@@ -691,7 +691,7 @@ def paged_attention_decode_int8(out, q, cache, block_tables, context_lens, max_c
                            ("block_tables", block_tables), ("context_lens", context_lens),
                            ("ws", ws))
     if ws is None:
-        ws = workspace(decode_workspace_bytes(desc, S, max_context_len), q.device)
+        ws = _own_workspace(decode_workspace_bytes(desc, S, max_context_len), q.device, stream)
     _check(lib().paged_attention_decode_int8(_ptr(out), _ptr(q), _ptr(cache.kv_pool),
                                              ctypes.byref(desc),
                                              _ptr(block_tables), block_tables.shape[1],

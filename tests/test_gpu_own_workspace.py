@@ -62,3 +62,43 @@ def test_selection_beside_a_busy_stream(pkv):
     ref = sparse.select(q, bounds, exps, t, [0, 1, 2], ctx, 16, 20, 1, 1, "bf16")
     for s in sel:
         assert np.array_equal(s.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("kind", ["decode", "varlen", "int8"])
+def test_dense_attention_beside_a_busy_stream(pkv, kind):
+    """The same lists of splits and partial results as with a workspace of the
+    caller's, bit for bit."""
+    rng = np.random.default_rng(31)
+    ctx = [9000, 7000, 600]
+    t, nb = tables_for(rng, ctx)
+    td, cd, start = i32(t), i32(ctx), i32([0, 1, 2, 3])
+    q = to_dev(values(rng, (3, 8, 128), "bf16"), "bf16")
+    k, v = (to_dev(values(rng, (sum(ctx), 2, 128), "bf16"), "bf16") for _ in range(2))
+    slots = torch.cat([td[s, torch.arange(n, device="cuda") // 16].long() * 16 +
+                       torch.arange(n, device="cuda") % 16 for s, n in enumerate(ctx)])
+    if kind == "int8":
+        cache = pkv.Int8Cache(nb, 2, 16, 128, 8)
+        pkv.paged_kv_append_int8(k, v, slots, cache)
+        need = pkv.decode_workspace_bytes(cache.desc, 3, max(ctx))
+    else:
+        kc, vc = (torch.zeros((nb, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+                  for _ in range(2))
+        desc = pkv.cache_desc(kc, 8)
+        pkv.paged_kv_append(k, v, slots, kc, vc, desc)
+        need = (pkv.decode_workspace_bytes(desc, 3, max(ctx)) if kind == "decode" else
+                pkv.varlen_workspace_bytes(desc, 3, 3, 1, max(ctx)))
+
+    def call(out, **kw):
+        if kind == "int8":
+            pkv.paged_attention_decode_int8(out, q, cache, td, cd, max(ctx), **kw)
+        elif kind == "decode":
+            pkv.paged_attention_decode(out, q, kc, vc, desc, td, cd, max(ctx), **kw)
+        else:
+            pkv.paged_attention_varlen(out, q, kc, vc, desc, td, start, cd, 1, max(ctx), **kw)
+
+    ref, outs = torch.empty_like(q), [torch.empty_like(q) for _ in range(CALLS)]
+    call(ref, ws=pkv.workspace(need))
+    _beside_a_busy_stream(need, lambda i, side: call(outs[i], stream=side))
+    assert pkv.device_error() == 0
+    for out in outs:
+        assert torch.equal(out, ref)

@@ -51,7 +51,35 @@ def _select(lib, **kw):
                           _FakeTensor(0, i32, (4, 8)), _FakeTensor(0, i32, (4,)), 100, 1, 1, **kw)
 
 
-CALLS = [_select]
+def _dense(lib):
+    i32, bf = torch.int32, torch.bfloat16
+    cache = _FakeTensor(0, bf, (64, 8, 16, 128))
+    row = _FakeTensor(0, bf, (4, 32, 128))
+    return dict(out=row, q=row, k_cache=cache, v_cache=cache,
+                desc=lib.CacheDesc(lib.PKV_BF16, 64, 16, 8, 32, 128),
+                block_tables=_FakeTensor(0, i32, (4, 8)), context_lens=_FakeTensor(0, i32, (4,)),
+                max_context_len=100)
+
+
+def _decode(lib, **kw):
+    lib.paged_attention_decode(**_dense(lib), **kw)
+
+
+def _varlen(lib, **kw):
+    lib.paged_attention_varlen(**_dense(lib), query_start_loc=_FakeTensor(0, torch.int32, (5,)),
+                               max_query_len=1, **kw)
+
+
+def _decode_int8(lib, **kw):
+    a = _dense(lib)
+    cache = type("Cache", (), {})()
+    cache.desc = lib.CacheDesc(lib.PKV_INT8, 64, 16, 8, 32, 128)
+    cache.kv_pool = _FakeTensor(0, torch.uint8, (64, 8, 2, lib.int8_tile_bytes(128)))
+    lib.paged_attention_decode_int8(a["out"], a["q"], cache, a["block_tables"], a["context_lens"],
+                                    100, **kw)
+
+
+CALLS = [_select, _decode, _varlen, _decode_int8]
 
 
 @pytest.mark.parametrize("call", CALLS)
