@@ -572,7 +572,8 @@ PKV_API int pkv_tables_release(const pkv_device_tables* tables, const int32_t* s
  * as they are, so a batch may be padded (paged_attention_varlen takes no padded
  * batch: there query_start_loc[num_seqs] is num_query_tokens).  Where
  * query_start_loc[num_seqs] is above num_query_tokens, PKV_DEV_BAD_QUERY_LAYOUT is
- * set and nothing is written.  Caches PKV_F32 or PKV_BF16.  Lists of
+ * set and nothing is written; offsets that do not rise from 0 are flagged as well,
+ * and what the rows between them get is undefined.  Caches PKV_F32 or PKV_BF16.  Lists of
  * up to PKV_SPARSE_MAX_TOP_K blocks (PKV_ERR_UNSUPPORTED above).
  * ======================================================================== */
 #define PKV_SPARSE_MAX_TOP_K 134217728

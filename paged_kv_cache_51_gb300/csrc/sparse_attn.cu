@@ -222,9 +222,11 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
     const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
     // the first entries, asked for before the row's context is known
     const int entry0 = first + lane * stride < p.top_k ? list[first + lane * stride] : -1;
+    const OffsetStep step(p.rows.start, p.rows.n);
     int seq;
     const int keys = row_keys(p.rows, t, seq,
                               threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    step.check(p.err);
     if (keys < 0) {                              // the whole cluster: left as it is
         if (cs > 1) cluster_wait();
         return;
@@ -421,9 +423,11 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
     const int first = int(rank) * C::kWarps + warp, stride = int(cs) * C::kWarps;
     // the first entries, asked for before the row's context is known
     const int entry0 = first + lane * stride < p.top_k ? list[first + lane * stride] : -1;
+    const OffsetStep step(p.rows.start, p.rows.n);
     int seq;
     const int keys = row_keys(p.rows, t, seq,
                               threadIdx.x == 0 && h == 0 && rank == 0 ? p.err : nullptr);
+    step.check(p.err);
     if (keys < 0) {                              // the whole cluster: left as it is
         if (cs > 1) cluster_wait();
         return;

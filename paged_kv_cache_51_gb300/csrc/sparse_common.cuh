@@ -59,18 +59,49 @@ __device__ __forceinline__ int token_seq(const int32_t* start, int n, int tokens
             first = start[lo];
             next = start[lo + 1];
         }
-        if (first < 0 || t < first || t >= next) {   // offsets that are not in order
+        if (t < first || t >= next) {            // offsets that are not in order
             flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
             return -1;
         }
     }
-    if (next > total) {
+    if (first < 0 || next > total) {
         flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
         return -1;
     }
     count = next - first;
     return lo;
 }
+
+// Flags offsets that do not rise from 0 (one out of order between two others shows in
+// no row of theirs): the steps i, i + threads, ... of one of `threads` threads.
+__device__ __forceinline__ void check_offsets(const int32_t* start, int n, int64_t i,
+                                              int64_t threads, int* err) {
+    for (; i < n; i += threads)
+        if (start[i + 1] < start[i] || (i == 0 && start[0] != 0))
+            flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
+}
+
+// The same by all threads of a grid beside their own work: each one's first step is
+// asked for when this is made and looked at by `check`, behind the lookup of the
+// thread's own row.
+struct OffsetStep {
+    const int32_t* start;
+    int32_t n, from, to;
+    __device__ __forceinline__ OffsetStep(const int32_t* start_, int32_t n_)
+        : start(start_), n(n_), from(0), to(0) {
+        const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+        if (start && i < n) from = start[i], to = start[i + 1];
+    }
+    __device__ __forceinline__ void check(int* err) const {
+        if (!start) return;
+        if (to < from || ((blockIdx.x | threadIdx.x) == 0 && from != 0))
+            flag_error(err, PKV_DEV_BAD_QUERY_LAYOUT);
+        const int64_t threads = int64_t(gridDim.x) * blockDim.x;
+        if (threads < n)
+            check_offsets(start, n, threads + int64_t(blockIdx.x) * blockDim.x + threadIdx.x,
+                          threads, err);
+    }
+};
 
 // Whether a sequence of q query rows has a context that can be read (flagged
 // where `err` is given).

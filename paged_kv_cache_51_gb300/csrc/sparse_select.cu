@@ -48,6 +48,7 @@ struct BoundsParams {
     const int32_t* ctx;
     int32_t table_stride, n, tokens, num_blocks, num_kv_heads;
     int span;                   // tokens that one warp looks at
+    int work_ctas;              // the CTAs behind these look over the offsets
     int* err;
 };
 
@@ -151,6 +152,12 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(BoundsP
     const uint32_t unit = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
     const int h = int(unit % uint32_t(p.num_kv_heads));
     const int64_t t0 = int64_t(unit / uint32_t(p.num_kv_heads)) * p.span;
+    if (int(blockIdx.x) >= p.work_ctas) {        // (beside the work these would delay its lookups)
+        const int64_t width = kBoundsWarps * 32;
+        check_offsets(p.start, p.n, (blockIdx.x - p.work_ctas) * width + threadIdx.x,
+                      (gridDim.x - p.work_ctas) * width, p.err);
+        return;
+    }
     if (t0 >= p.tokens) return;
     int* const tell = h == 0 ? p.err : nullptr;
     int first, q, id = -1, nrow = 0;
@@ -264,7 +271,9 @@ constexpr int kScoreWarps = 4;
 constexpr int kTileBlocks = 16;      // blocks of a product tile
 constexpr int kScoreStages = 2;      // tiles in flight per warp
 
-// Floats in an order that unsigned compare keeps (no NaN among the scores).
+// Floats in an order that unsigned compare keeps (no NaN among the scores), and the
+// ends of that order, -inf and inf.
+constexpr uint32_t kLeastKey = 0x007fffffu, kMostKey = 0xff800000u;
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t b = __float_as_uint(x);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -587,7 +596,9 @@ __device__ __forceinline__ uint32_t warps_before(const uint32_t* of_warps) {
 // context is known; with kHeld 0 (rows longer than that) every pass reads them
 // again.  Keys of real blocks lie between those of the two infinities; the ends
 // carry a key above all and places behind the row one below all, so that no pass
-// has to look at indices.  2048 rows of up to 512 blocks: 5.4 us behind the scores,
+// has to look at indices.  (They are held to that: where the offsets of the batch are
+// out of order a row may find keys that no warp wrote, and the counts below are
+// those of the list only while every block's key is between the ends.)  2048 rows of up to 512 blocks: 5.4 us behind the scores,
 // of which 2.4 start the CTAs and 2.0 rank and write; 32 rows of 2048: 2.7 us, a
 // chain of barriers.
 template <int NT, int kHeld>
@@ -613,8 +624,10 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
         for (int i = 0; i < kHeld; ++i)
             held[i] = mine + 32 * i < p.stride ? far[mine + 32 * i] : kNone;
     }
+    const OffsetStep step(p.rows.start, p.rows.n);
     int seq;
     const int row_sees = row_keys(p.rows, t, seq, tid == 0 && h == 0 ? p.err : nullptr);
+    step.check(p.err);
     if (row_sees < 0) return;                    // behind the last sequence: left as it is
     const int blocks = (row_sees + kBlockTokens - 1) / kBlockTokens;
     int32_t* out = p.selected + size_t(blockIdx.x) * p.top_k;
@@ -623,10 +636,15 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
         return;
     }
     const int b0 = p.sink, b1 = blocks - p.recent;
+    auto between = [](uint32_t k) { return min(max(k, kLeastKey), kMostKey); };
     auto marked = [&](int b, uint32_t k) {
         return b >= blocks ? kNone : b < b0 || b >= b1 ? kEnd : k;
     };
     if (Held) {
+        if (p.rows.start) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) held[i] = between(held[i]);
+        }
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) held[i] = marked(mine + 32 * i, held[i]);
     }
@@ -635,7 +653,7 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) f(held[i]);
         } else {
-            for (int b = b0 + tid; b < b1; b += NT) f(far[b]);
+            for (int b = b0 + tid; b < b1; b += NT) f(between(far[b]));
         }
     };
     // this warp's stretch of the row (ascending with the warps), 32 blocks at a time
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
         } else {
             const int end = min(blocks, (warp + 1) * stretch);
             for (int b = warp * stretch + lane; b - lane < end; b += 32)
-                f(b, b < end ? marked(b, far[b]) : kNone);
+                f(b, b < end ? marked(b, between(far[b])) : kNone);
         }
     };
     const uint32_t below = (1u << lane) - 1u;
@@ -843,10 +861,12 @@ bool aligned_to(const void* p, uintptr_t a) {
 }
 
 template <typename T, int D>
-int launch_bounds(const BoundsParams& p, cudaStream_t s) {
+int launch_bounds(BoundsParams p, cudaStream_t s) {
     const int64_t units = ceil_div(p.tokens, p.span) * int64_t(p.num_kv_heads);
-    return cuda_status(launch_pdl(block_bounds_kernel<T, D>,
-                                  dim3(unsigned((units + kBoundsWarps - 1) / kBoundsWarps)),
+    p.work_ctas = int((units + kBoundsWarps - 1) / kBoundsWarps);
+    // (two offsets a thread)
+    const int checks = p.start ? std::min(ceil_div(p.n, 2 * kBoundsWarps * 32), num_sms()) : 0;
+    return cuda_status(launch_pdl(block_bounds_kernel<T, D>, dim3(unsigned(p.work_ctas + checks)),
                                   dim3(kBoundsWarps * 32), 0, s, p));
 }
 

@@ -131,3 +131,64 @@ def test_padded_layouts_stay_served(pkv, rows, start, ctx):
     args = (batch.q[:m], batch.k, batch.v, batch.t, start, ctx, batch.lists[:m], "bf16")
     ref = sparse.attention(*args)
     assert_attention(out[:m], ref, attention_bound(*args, ref))
+
+
+@pytest.mark.parametrize("ws_byte", [0x00, 0xFF])
+@pytest.mark.parametrize("dtype,hq,hkv", [("bf16", 2, 2), ("bf16", 4, 2), ("f32", 8, 1)])
+@pytest.mark.parametrize("rows,start,ctx", [
+    (8, [0, 5, 2, 8], [700, 900, 400]),            # every row belongs to a sequence all the same
+    (8, [-3, 8], [700]),                           # rows that begin before the batch
+    (8, [3, 8], [700]),                            # rows of no sequence in front
+    (9, [0, 4, 4, 3, 9], [500, 20, 700, 640]),
+    (12, [0, 9, 1, 12, 2, 12], [300, 1500, 2500, 700, 900]),
+])
+def test_layouts_out_of_order_are_flagged(pkv, dtype, hq, hkv, rows, start, ctx, ws_byte):
+    """Whatever the workspace held before: rows whose group leads in another sequence
+    find scores there that no warp wrote."""
+    batch = Batch(pkv, dtype, hq, hkv, ctx, rows)
+    assert batch.bounds(start, rows)[0] == BAD_LAYOUT
+    code, sel = batch.select(start, ws_byte)
+    assert code == BAD_LAYOUT
+    assert ((sel == -9) | ((sel >= -1) & (sel < -(-max(ctx) // 16)))).all()
+    assert batch.attend(start)[0] == BAD_LAYOUT
+
+
+@pytest.mark.parametrize("blocks", [600, 2100, 9000])
+def test_layouts_out_of_order_over_long_rows(pkv, blocks):
+    """Every length of row that the lists are made for, over a workspace of ones."""
+    batch = Batch(pkv, "bf16", 2, 2, [blocks * 16, 300, blocks * 16 - 5], 8, top_k=40)
+    code, sel = batch.select([0, 5, 2, 8], 0xFF)
+    assert code == BAD_LAYOUT and (sel < blocks).all()
+
+
+def test_many_empty_sequences_are_looked_over(pkv):
+    """More offsets than the kernels have threads, one of them out of order."""
+    n, rows = 70000, 4
+    rng = np.random.default_rng(3)
+    ctx = np.ones(n, dtype=np.int64)
+    ctx[n - 1] = 700
+    t = np.full((n, 44), -1, dtype=np.int32)
+    t[:, 0] = 0
+    t[n - 1] = rng.permutation(44)
+    kd = to_dev(values(rng, (44, 1, 16, 64), "f32"))
+    desc = pkv.cache_desc(kd, 1)
+    qd = to_dev(values(rng, (rows, 1, 64), "f32"))
+    td, cd = i32(t), i32(ctx)
+    bb = pkv.BlockBounds(44, 1, 64)
+    sel = torch.full((rows, 1, 4), -9, dtype=torch.int32, device="cuda")
+    for bad in (None, 1, n // 2, n - 2):
+        start = np.zeros(n + 1, dtype=np.int64)
+        start[n] = rows
+        if bad is not None:
+            start[bad] = 1
+        sd = i32(start)
+        want = 0 if bad is None else BAD_LAYOUT
+        pkv.pkv_block_bounds(bb.bounds, bb.exps, kd, desc, td, cd, query_start_loc=sd,
+                             num_query_tokens=rows)
+        assert pkv.device_error() == want
+        pkv.pkv_select_blocks(sel, qd, bb.bounds, bb.exps, desc, td, cd, 704, 1, 1,
+                              query_start_loc=sd)
+        assert pkv.device_error() == want
+        pkv.paged_attention_sparse(torch.empty_like(qd), qd, kd, kd, desc, td, cd, sel.clamp(min=0),
+                                   query_start_loc=sd)
+        assert pkv.device_error() == want
