@@ -551,8 +551,9 @@ PKV_API int pkv_tables_step(const pkv_device_tables* tables, const int32_t* seq_
  * tokens (device [num_seqs]), in request and table order; their entries become
  * -1 and *free_count grows in place.  Skipped and flagged: a row out of range,
  * named twice, already released or holding fewer blocks (PKV_DEV_BAD_SEQ_ROW), a
- * length out of range (as in pkv_tables_step), blocks past the end of the free
- * list (PKV_DEV_BAD_BLOCK_ID). */
+ * length out of range (as in pkv_tables_step), a row with an entry outside the pool
+ * among its blocks, blocks past the end of the free list (PKV_DEV_BAD_BLOCK_ID).
+ * A skipped row keeps its entries. */
 PKV_API int pkv_tables_release(const pkv_device_tables* tables, const int32_t* seq_rows,
                                const int32_t* lens, int32_t num_seqs, void* stream);
 

@@ -478,43 +478,64 @@ __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleasePar
                 flag_error(p.err, PKV_DEV_TABLE_TOO_NARROW);
             } else if (len > 0) {
                 // a row that was released already, or holds fewer blocks, has -1 there:
-                // nothing is given back
+                // nothing is given back (entries between them are looked at below)
                 const int32_t* e = p.table + size_t(row) * p.max_blocks;
                 const int64_t held = blocks_of(len, p.block_size);
                 if (e[0] < 0 || e[held - 1] < 0) flag_error(p.err, PKV_DEV_BAD_SEQ_ROW);
                 else blocks = uint32_t(held);
             }
         }
-        uint32_t in_pass = blocks, none = 0, sum, none_sum;
-        scan_inclusive<kPlanThreads>(in_pass, none, scratch, sum, none_sum);
-        const uint32_t incl = sat_add(base_sum, in_pass);
-        if (blocks && incl > room) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
-        // more blocks than the pool has: the stack takes no request past its end
-        const uint32_t got = blocks && incl <= room ? incl : 0u;
-        top = max(top, __reduce_max_sync(kFull, got));
-        if ((threadIdx.x & 31) == 0) end[threadIdx.x >> 5] = top;
-        __syncthreads();
-        for (int w = 0; w < kPlanThreads / 32; ++w) top = max(top, end[w]);
-        __syncthreads();
-        end[threadIdx.x] = min(incl, top);
-        rows[threadIdx.x] = row;
-        __syncthreads();
-        const uint32_t first = min(base_sum, top);
-        for (uint32_t b = first + threadIdx.x; b < top; b += kPlanThreads) {
-            int lo = 0, hi = kPlanThreads - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (end[mid] > b) hi = mid;
-                else lo = mid + 1;
+        uint32_t sum, incl, first;
+        const uint32_t top_before = top;
+        for (bool again = false;; again = true) {
+            uint32_t in_pass = blocks, none = 0, none_sum;
+            scan_inclusive<kPlanThreads>(in_pass, none, scratch, sum, none_sum);
+            incl = sat_add(base_sum, in_pass);
+            // more blocks than the pool has: the stack takes no request past its end
+            const uint32_t got = blocks && incl <= room ? incl : 0u;
+            top = max(top_before, __reduce_max_sync(kFull, got));
+            if ((threadIdx.x & 31) == 0) end[threadIdx.x >> 5] = top;
+            __syncthreads();
+            for (int w = 0; w < kPlanThreads / 32; ++w) top = max(top, end[w]);
+            __syncthreads();
+            end[threadIdx.x] = min(incl, top);
+            rows[threadIdx.x] = row;
+            __syncthreads();
+            first = min(base_sum, top);
+            auto entry = [&](uint32_t b) {           // of the b-th block given back
+                int lo = 0, hi = kPlanThreads - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (end[mid] > b) hi = mid;
+                    else lo = mid + 1;
+                }
+                return p.table + size_t(rows[lo]) * p.max_blocks +
+                       (b - (lo ? end[lo - 1] : first));
+            };
+            bool odd = false;
+            for (uint32_t b = first + threadIdx.x; b < top; b += kPlanThreads) {
+                int32_t* e = entry(b);
+                const int blk = *e;
+                odd |= blk < 0 || blk >= p.num_blocks;
+                p.free_list[uint32_t(free0) + b] = blk;
+                *e = -1;
             }
-            int32_t* e = p.table + size_t(rows[lo]) * p.max_blocks +
-                         (b - (lo ? end[lo - 1] : first));
-            const int blk = *e;
-            if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
-            p.free_list[uint32_t(free0) + b] = blk;
-            *e = -1;
+            if (!__syncthreads_or(odd) || again) break;
+            // A row has an entry that is no block: the pass's rows get their entries back
+            // (what lies above the stack's count counts for nothing), and are given back
+            // without the rows that have one.
+            for (uint32_t b = first + threadIdx.x; b < top; b += kPlanThreads)
+                *entry(b) = p.free_list[uint32_t(free0) + b];
+            __syncthreads();
+            const int32_t* e = p.table + size_t(max(row, 0)) * p.max_blocks;
+            for (uint32_t j = 0; j < blocks; ++j) {
+                if (e[j] < 0 || e[j] >= p.num_blocks) {
+                    flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
+                    blocks = 0;
+                }
+            }
         }
-        __syncthreads();
+        if (blocks && incl > room) flag_error(p.err, PKV_DEV_BAD_BLOCK_ID);
         base_sum = sat_add(base_sum, sum);
     }
     if (threadIdx.x == 0 && free_ok) *p.free_count = int32_t(free0 + top);
