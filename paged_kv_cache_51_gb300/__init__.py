@@ -717,6 +717,11 @@ class DeviceTables:
         if block_table.dim() != 2 or free_list.dim() != 1 or free_count.numel() != 1:
             raise ValueError("block_table [max_seqs, max_blocks], free_list [num_blocks] and "
                              "free_count [1] expected")
+        # (the calls check the device of block_table against the current one)
+        for t, nm in ((free_list, "free_list"), (free_count, "free_count")):
+            if t.device != block_table.device:
+                raise ValueError(f"{nm} is on {t.device}, but block_table is on "
+                                 f"{block_table.device}")
         self.block_table, self.free_list, self.free_count = block_table, free_list, free_count
         self.block_size = block_size
         self.desc = DeviceTablesDesc(block_table.data_ptr(), free_list.data_ptr(),
