@@ -3,11 +3,14 @@
 Every translation unit under csrc/ is compiled in parallel, then linked into
 one shared library next to this file.  _hotcalls.so (binding/hotcalls.cpp) is the
 Python extension that marshals the calls of the shortest kernels; it is compiled
-beside the library, against the installed torch, and linked to it.  A stamp of the
-sources and flags skips the build when nothing changed.
+beside the library, against the installed torch, and linked to it.  A user of the C
+ABI needs neither torch nor Python's headers: without torch, or with
+``python _build.py --library``, the library alone is built.  A stamp of the sources
+and flags skips the build when nothing changed.
 """
 
 import hashlib
+import importlib.util
 import os
 import subprocess
 import sys
@@ -77,22 +80,28 @@ def build_variant(tag, defines, verbose=False):
             fcntl.flock(lock, fcntl.LOCK_UN)
 
 
-def build(force=False, verbose=False):
-    """Compile and link the library; return its path.  Raises on compiler errors.
+def build(force=False, verbose=False, binding=None):
+    """Compile and link the library, and the Python extension unless ``binding`` is
+    False (by default it is made where torch is installed, which the Python package
+    needs anyway); return the library's path.  Raises on compiler errors.
 
     Processes that build at the same time (one per rank under torchrun) take
     turns through a lock file next to the library; the later ones find the
     fresh stamp and return at once."""
     import fcntl
 
+    if binding is None:
+        binding = importlib.util.find_spec("torch") is not None
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     with open(LIB + ".lock", "w") as lock:
         fcntl.flock(lock, fcntl.LOCK_EX)
         try:
+            if not binding:
+                return _build_locked(force, verbose)
             with ThreadPoolExecutor(max_workers=1) as ex:
-                binding = ex.submit(_compile_binding, force)
+                extension = ex.submit(_compile_binding, force)
                 lib = _build_locked(force, verbose)
-                _link_binding(*binding.result())
+                _link_binding(*extension.result())
             return lib
         finally:
             fcntl.flock(lock, fcntl.LOCK_UN)
@@ -188,4 +197,5 @@ def _build_locked(force, verbose, lib=LIB, build_dir=BUILD, extra=()):
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True))
+    print(build(force="--force" in sys.argv, verbose=True,
+                binding=False if "--library" in sys.argv else None))
