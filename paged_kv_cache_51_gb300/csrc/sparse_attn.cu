@@ -37,8 +37,13 @@ struct SparseParams {
     int* err;
 };
 
-// Floats of a warp's record: outputs [G][D], max [G], sum [G], keys seen.
-constexpr int record_floats(int g, int d) { return (g * (d + 2) + 1 + 3) & ~3; }
+// Floats of a head's outputs in a warp's record: eight more than D, so that the lanes
+// that write two dimensions each of eight heads meet different banks (4 rows of 128
+// blocks: 9.4 us, 9.5 without).
+constexpr int head_floats(int d) { return d + 8; }
+
+// Floats of a warp's record: outputs [G][head_floats], max [G], sum [G], keys seen.
+constexpr int record_floats(int g, int d) { return (g * (head_floats(d) + 2) + 1 + 3) & ~3; }
 
 // Floats behind the warps' records: their factors [warp][G], and a CTA's sums [G].
 constexpr int factor_floats(int g, int warps) { return ((warps + 1) * g + 3) & ~3; }
@@ -94,7 +99,7 @@ template <typename T, int D, int kMaxG, int kWarps>
 __device__ __forceinline__ void merge_and_write(const SparseParams& p, float* comb, float* inbox,
                                                 uint64_t* arrived, int t, int h, int G) {
     constexpr int kThreads = kWarps * 32;
-    constexpr int kRec = record_floats(kMaxG, D);
+    constexpr int kRec = record_floats(kMaxG, D), kHead = head_floats(D);
     const uint32_t cs = cluster_size(), rank = cluster_rank();
     const int part_log2 = 31 - __clz(G * D) - (31 - __clz(int(cs)));   // all powers of two
     const int part = 1 << part_log2;
@@ -112,13 +117,13 @@ __device__ __forceinline__ void merge_and_write(const SparseParams& p, float* co
         const uint32_t c = threadIdx.x / uint32_t(G);
         float M = -INFINITY, L = 0.f, seen = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[w * kRec + G * D + g]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb[w * kRec + G * kHead + g]);
         const float Mx = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float s = exp2f(comb[w * kRec + G * D + g] - Mx);
-            L = fmaf(comb[w * kRec + G * D + G + g], s, L);
-            seen += comb[w * kRec + 2 * G + G * D];
+            const float s = exp2f(comb[w * kRec + G * kHead + g] - Mx);
+            L = fmaf(comb[w * kRec + G * kHead + G + g], s, L);
+            seen += comb[w * kRec + G * kHead + 2 * G];
             if (c == 0) fac[w * G + g] = s;
         }
         if (cs == 1) {
@@ -139,7 +144,7 @@ __device__ __forceinline__ void merge_and_write(const SparseParams& p, float* co
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4 o = *reinterpret_cast<const float4*>(comb + w * kRec + i);
+            const float4 o = *reinterpret_cast<const float4*>(comb + w * kRec + g * kHead + i % D);
             const float s = fac[w * G + g];
             O.x = fmaf(o.x, s, O.x);
             O.y = fmaf(o.y, s, O.y);
@@ -206,6 +211,7 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
     using C = SparseF32Cfg<D, G>;
     constexpr int RC = D / 4;                    // 16-byte chunks of a row
     constexpr int DL = D / 32;                   // output dimensions of a lane
+    constexpr int kHead = head_floats(D);
     extern __shared__ __align__(128) unsigned char smem[];
     float* qs = reinterpret_cast<float*>(smem + C::kQOff);
     float* comb = reinterpret_cast<float*>(smem + C::kCombOff);
@@ -343,13 +349,13 @@ __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_
 #pragma unroll
         for (int of = 1; of < 32; of <<= 1) l[g] += __shfl_xor_sync(kFull, l[g], of);
 #pragma unroll
-        for (int d = 0; d < DL; ++d) rec[g * D + lane * DL + d] = o[g][d];
+        for (int d = 0; d < DL; ++d) rec[g * kHead + lane * DL + d] = o[g][d];
         if (lane == 0) {
-            rec[G * D + g] = m[g];
-            rec[G * D + G + g] = l[g];
+            rec[G * kHead + g] = m[g];
+            rec[G * kHead + G + g] = l[g];
         }
     }
-    if (lane == 0) rec[G * (D + 2)] = float(seen);
+    if (lane == 0) rec[G * (kHead + 2)] = float(seen);
     merge_and_write<float, D, G, C::kWarps>(p, comb, inbox, &arrived, t, h, G);
 }
 
@@ -373,9 +379,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 lo, __nv_bfloat16 hi) {
-    const __nv_bfloat162 v(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+// The same for rows lane / 4 + 8 alone: d2, d3 += a . b, rows of zeros above them.  (Those
+// rows' sums go nowhere: zeros times an infinite b are not zero.)
+__device__ __forceinline__ void mma16816_lower(float (&d)[4], uint32_t a1, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    float above[2];
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%4,%6}, "
+        "{%7,%8}, {%9,%9,%2,%3};"
+        : "=f"(above[0]), "=f"(above[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(0u), "r"(a1), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The upper halves of two words: bf16 values that are the words' leading bits.
+__device__ __forceinline__ uint32_t upper2(uint32_t lo, uint32_t hi) {
+    return __byte_perm(lo, hi, 0x7632);
 }
 
 template <int D>
@@ -395,17 +412,22 @@ struct SparseBf16Cfg {
 };
 
 // The same work on warp-level tensor-core products (m16n8k16): S = q K^T with
-// the group's query heads as rows 0 .. G-1, then O += P V.  The 16-row tile has
-// eight rows to spare; the second product puts them to use: rows 0-7 carry P
-// rounded to bf16 and rows 8-15 what that rounding left, so P enters the
-// product to 2^-16 of itself at no extra instruction.  A ring of three tiles a warp
-// and two CTAs an SM keep 192 KB in flight: 256 rows x 8 heads x 64 blocks (1.07 GB)
-// 158 us, 6.8 TB/s (two tiles and three CTAs: 165 us); 4 rows x 8 heads x 128 blocks
-// (34 MB), in clusters of 8, 8.8 us.
+// the group's query heads as rows 0 .. G-1, then O += P V.  A weight of P enters the
+// product whole, as three bf16 values of eight of its 24 bits each: rows 0-7 carry
+// the leading bits and rows 8-15, which the heads leave free, the next ones; the last
+// ones go through a second product into rows 8-15.  (Without the second product, P to
+// 2^-17, 0.23 % of the outputs were a bf16 step away from the nearest value; 0.02 %
+// are, 0.04 % of those of a sum in single precision.  It costs 0.4 us of 9.4 for 4
+// rows of 128 blocks and 1 % of a batch.  With O^T = V^T P^T, the heads as columns, it
+// is one product instead of two, but the call takes 10.2 us.)  A ring of three tiles a
+// warp and two CTAs an SM keep 192 KB in flight: 256 rows x 8 heads x 64 blocks
+// (1.07 GB) 160 us, 6.7 TB/s (two tiles and three CTAs: 4 % more); 4 rows x 8 heads x
+// 128 blocks (34 MB), in clusters of 8, 9.8 us.
 template <int D>
 __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_kernel(SparseParams p) {
     using C = SparseBf16Cfg<D>;
     constexpr int RC = D / 8;                    // 16-byte chunks of a row
+    constexpr int kHead = head_floats(D);
     extern __shared__ __align__(128) unsigned char smem[];
     float* comb = reinterpret_cast<float*>(smem);
     float* inbox = reinterpret_cast<float*>(smem + C::kRingBytes);
@@ -519,14 +541,16 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
         const float mn = fmaxf(m, mx);
         const float mz = mn == -INFINITY ? 0.f : mn;     // nothing above -inf so far
         const float alpha = exp2f(m - mz);
-        __nv_bfloat16 hi[4], lo[4];
+        uint32_t part[3][4];                     // eight leading bits, the next eight, the last
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float w = exp2f(v[i] - mz);
             sum += w;
-            hi[i] = __float2bfloat16_rn(w);
-            lo[i] = __float2bfloat16_rn(w - __bfloat162float(hi[i]));
+            part[0][i] = __float_as_uint(w) & 0xffff0000u;
+            const float behind = w - __uint_as_float(part[0][i]);
+            part[1][i] = __float_as_uint(behind) & 0xffff0000u;
+            part[2][i] = __float_as_uint(behind - __uint_as_float(part[1][i]));
         }
         l = l * alpha + sum;
         m = mn;
@@ -539,16 +563,22 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
                 o[n][3] *= alpha;
             }
         }
-        const uint32_t a0 = pack2(hi[0], hi[1]), a2 = pack2(hi[2], hi[3]);
-        const uint32_t a1 = pack2(lo[0], lo[1]), a3 = pack2(lo[2], lo[3]);
+        const uint32_t a0 = upper2(part[0][0], part[0][1]), a2 = upper2(part[0][2], part[0][3]);
+        const uint32_t a1 = upper2(part[1][0], part[1][1]), a3 = upper2(part[1][2], part[1][3]);
+        const uint32_t b1 = upper2(part[2][0], part[2][1]), b3 = upper2(part[2][2], part[2][3]);
         {
             const int r = ((mi & 1) << 3) + (lane & 7);
+            uint32_t f[D / 16][4];
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
-                uint32_t f[4];
-                ldsm_x4_t(vt + (r * RC + ((n * 2 + (mi >> 1)) ^ (r & 7))) * 16, f);
-                mma16816(o[2 * n], a0, a1, a2, a3, f[0], f[1]);
-                mma16816(o[2 * n + 1], a0, a1, a2, a3, f[2], f[3]);
+                ldsm_x4_t(vt + (r * RC + ((n * 2 + (mi >> 1)) ^ (r & 7))) * 16, f[n]);
+                mma16816(o[2 * n], a0, a1, a2, a3, f[n][0], f[n][1]);
+                mma16816(o[2 * n + 1], a0, a1, a2, a3, f[n][2], f[n][3]);
+            }
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                mma16816_lower(o[2 * n], b1, b3, f[n][0], f[n][1]);
+                mma16816_lower(o[2 * n + 1], b1, b3, f[n][2], f[n][3]);
             }
         }
         __syncwarp();
@@ -564,15 +594,15 @@ __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_k
             // (where an infinite value of V makes the sum infinite, P's remainders,
             // of either sign or 0, would turn it into NaN)
             const bool f0 = fabsf(o[n][0]) <= FLT_MAX, f1 = fabsf(o[n][1]) <= FLT_MAX;
-            rec[gid * D + n * 8 + 2 * tig] = o[n][0] + (f0 ? o[n][2] : 0.f);
-            rec[gid * D + n * 8 + 2 * tig + 1] = o[n][1] + (f1 ? o[n][3] : 0.f);
+            rec[gid * kHead + n * 8 + 2 * tig] = o[n][0] + (f0 ? o[n][2] : 0.f);
+            rec[gid * kHead + n * 8 + 2 * tig + 1] = o[n][1] + (f1 ? o[n][3] : 0.f);
         }
         if (tig == 0) {
-            rec[G * D + gid] = m;
-            rec[G * D + G + gid] = l;
+            rec[G * kHead + gid] = m;
+            rec[G * kHead + G + gid] = l;
         }
     }
-    if (lane == 0) rec[G * (D + 2)] = float(seen);
+    if (lane == 0) rec[G * (kHead + 2)] = float(seen);
     merge_and_write<__nv_bfloat16, D, C::kMaxG, C::kWarps>(p, comb, inbox, &arrived, t, h, G);
 }
 
