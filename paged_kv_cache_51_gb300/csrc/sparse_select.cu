@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(BoundsP
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float y = lower ? -ex.low(j + i) : ex.top(j + i);
-                    // (a positive value that vanishes in the product is rounded up to 1)
-                    const float least = y > 0.f ? 1.f : -127.f;
-                    const int c = int(fminf(fmaxf(ceilf(y * unit_inv), least), 127.f));
+                    // (a product too small for its type is rounded up too: to 1, if positive)
+                    const float x = ceilf(__fmul_ru(y, unit_inv));
+                    const int c = int(fminf(fmaxf(x, -127.f), 127.f));
                     w[j / 4] |= uint32_t((lower ? -c : c) & 0xff) << (8 * i);
                 }
                 if (odd) w[j / 4] = 0u;          // (such a block has codes of 0)
