@@ -536,7 +536,13 @@ typedef struct pkv_device_tables {
  * of range or named twice in the batch (PKV_DEV_BAD_SEQ_ROW), a negative length
  * (PKV_DEV_BAD_CONTEXT_LEN) or more tokens than a row or block_tables has room
  * for (PKV_DEV_TABLE_TOO_NARROW) is skipped: context_lens[i] = 0, no tokens, a
- * row of -1.  num_seqs == 0 writes the padding, query_start_loc[0] and the
+ * row of -1.  (Where context_lens is the cached_lens buffer the length of such a
+ * request is lost, and the next step takes it for a new one: a loop that updates the
+ * lengths in place ends or drops its sequences before their rows are full.)  With
+ * more rows than tokens (max_tokens above query_start_loc[num_seqs]) the batch is
+ * padded: the appends skip the slots of -1 and the sparse entry points the rows
+ * behind the last sequence, but paged_attention_varlen takes no such batch.
+ * num_seqs == 0 writes the padding, query_start_loc[0] and the
  * count.  Outputs do not overlap inputs but where said (block_tables is never
  * tables->block_table; with seq_rows NULL that table can be passed to the
  * attention as it is, and block_tables be NULL). */

@@ -93,8 +93,9 @@ __device__ __forceinline__ void expect_parts(uint64_t* arrived, int G, int D, ui
 // and write the outputs of the (row, head): shared by every variant.  Each CTA
 // owns a part of the outputs; the others send it theirs by stores that count on
 // the owner's mbarrier, so that between the merges a CTA waits for nothing but
-// what it needs (with a cluster barrier there: 9.2 us for 4 rows of 128 blocks,
-// 8.8 so; 8 rows of fp32 3.9 and 3.5).  The factors of a head are made once, not by every output.
+// what it needs (with a cluster barrier there the call of 4 rows of 128 blocks and
+// that of 8 rows of fp32 took 0.4 us more).  The factors of a head are made once, not
+// by every output.
 template <typename T, int D, int kMaxG, int kWarps>
 __device__ __forceinline__ void merge_and_write(const SparseParams& p, float* comb, float* inbox,
                                                 uint64_t* arrived, int t, int h, int G) {
@@ -204,8 +205,11 @@ __device__ __forceinline__ ListCursor fetch_tiles(const SparseParams& p, int b, 
 
 // On CUDA cores (fp32 caches).  A warp holds one tile at a time: the products are
 // long next to its copy, and three or more CTAs on an SM hide one warp's copy
-// behind the others' products better than a ring of tiles in one CTA does (105 x
-// 40 blocks, groups of 4, 64 dimensions: 75 us, 145 us with four tiles a warp).
+// behind the others' products better than a ring of tiles in one CTA does (at the
+// step that chose, groups of 4, 64 dimensions, four tiles a warp took 1.8 times as
+// long).  64 rows x 8 heads x 64 blocks, groups of 1 / 4 / 8: 64 dimensions (269 MB,
+// 40 us at HBM's rate) 50 / 46 / 75 us, 128 dimensions (538 MB, 80 us) 83 / 89 / 112
+// us; in groups of 8 bound by the products.
 template <int D, int G>
 __global__ void __launch_bounds__(SparseF32Cfg<D, G>::kThreads) sparse_attn_f32_kernel(SparseParams p) {
     using C = SparseF32Cfg<D, G>;
@@ -418,11 +422,11 @@ struct SparseBf16Cfg {
 // ones go through a second product into rows 8-15.  (Without the second product, P to
 // 2^-17, 0.23 % of the outputs were a bf16 step away from the nearest value; 0.02 %
 // are, 0.04 % of those of a sum in single precision.  It costs 0.4 us of 9.4 for 4
-// rows of 128 blocks and 1 % of a batch.  With O^T = V^T P^T, the heads as columns, it
-// is one product instead of two, but the call takes 10.2 us.)  A ring of three tiles a
-// warp and two CTAs an SM keep 192 KB in flight: 256 rows x 8 heads x 64 blocks
-// (1.07 GB) 160 us, 6.7 TB/s (two tiles and three CTAs: 4 % more); 4 rows x 8 heads x
-// 128 blocks (34 MB), in clusters of 8, 9.8 us.
+// rows of 128 blocks and 1 % of a batch.  As O^T = V^T P^T, the heads as columns, the
+// three parts take three products of 16 dimensions in place of four, but the call
+// 10.3 us.)  A ring of three tiles a warp and two CTAs an SM keep 192 KB in flight:
+// 256 rows x 8 heads x 64 blocks (1.07 GB) 161 us, 6.7 TB/s (two tiles and three CTAs
+// 4 % more); 4 rows x 8 heads x 128 blocks (34 MB), in clusters of 8, 9.8 us.
 template <int D>
 __global__ void __launch_bounds__(SparseBf16Cfg<D>::kThreads) sparse_attn_bf16_kernel(SparseParams p) {
     using C = SparseBf16Cfg<D>;

