@@ -648,6 +648,149 @@ PKV_API int paged_attention_sparse(void* out, const void* q, const void* k_cache
                                    const int32_t* selected, int32_t top_k, int32_t num_seqs,
                                    int32_t num_query_tokens, float scale, void* stream);
 
+/* ======================================================================== *
+ * Latent attention over a paged cache.
+ *
+ * All heads of a token share one latent vector c (latent_dim values) and one
+ * rotated key part k (rope_dim values), which is all that the cache holds.  A
+ * head's keys and values are products of c with its own matrices,
+ *   key = (W_k c, k),   value = W_v c,
+ * and there are two ways to attend over them, the same in exact arithmetic:
+ *   absorbed: the query's first part is multiplied by W_k once, a = W_k^T q, and
+ *     attention runs over the cached rows themselves (paged_attention_latent); the
+ *     outputs, sums of c, are multiplied by W_v.  It reads latent_dim + rope_dim
+ *     values a token for all heads together: the form for single tokens.
+ *   expanded: the cached rows are read back in order (paged_latent_gather),
+ *     multiplied by W_k and W_v of all heads, and attention runs over the result
+ *     (pkv_attention_expanded).  It takes fewer products where many query tokens
+ *     attend over the same keys: the form for prompts and their chunks.
+ * The products with W_k and W_v are the caller's.
+ *
+ * Cache: [num_blocks][block_size][latent_dim + rope_dim], row-major, in the cache
+ * dtype, 16-byte aligned; blocks, tables and slots are those of the other caches
+ * (pkv_pool, pkv_device_tables).
+ * ======================================================================== */
+typedef struct pkv_latent_desc {
+    int32_t dtype;        /* PKV_F32 or PKV_BF16: all tensors of the calls below share it */
+    int32_t num_blocks;
+    int32_t block_size;   /* 16 */
+    int32_t latent_dim;   /* 128, 256, 384 or 512 */
+    int32_t rope_dim;     /* 64 */
+    int32_t num_q_heads;  /* any (65536 at most) */
+} pkv_latent_desc;
+
+#define PKV_ROPE_HALF        0  /* value i is rotated with value i + rope_dim / 2 */
+#define PKV_ROPE_INTERLEAVED 1  /* value 2 i is rotated with value 2 i + 1 */
+
+/* Append a step's latent vectors and rotated keys, and rotate its queries:
+ *   cache[slot] = (norm(latent[t]), rot(k_rope[t])),   q_out[t][h] = rot(q[t][h])
+ * norm(x)[d] = x[d] * norm_weight[d] / sqrt(mean(x^2) + eps), computed in fp32 and
+ * rounded once; norm_weight NULL: x itself, bit for bit.  rot turns the pair i of
+ * the 64 values (rope_layout says which two) by the angle whose cosine and sine are
+ * cos_sin[p][i] and cos_sin[p][32 + i], p = positions[t], rounded as in
+ * paged_kv_append_rope; a table scaled for long contexts is the caller's.
+ *   latent:  device, num_tokens rows of latent_dim values, latent_stride apart
+ *   k_rope:  device, num_tokens rows of 64 values, k_rope_stride apart
+ *   norm_weight: device [latent_dim] in the cache dtype, or NULL
+ *   q, q_out: device, 64 values at [t * token_stride + h * head_stride], both NULL
+ *            to skip; q_out may be q itself (same strides), and overlaps nothing else
+ * Strides are in values; rows start on 16 bytes.  A query's rotary part is usually
+ * the end of a head, and q_out the end of the absorbed query's.  Slots and positions
+ * as for paged_kv_append_rope: a token with a slot out of range (PKV_DEV_BAD_SLOT)
+ * is not written, one with a position outside [0, max_position) neither written nor
+ * rotated (PKV_DEV_BAD_POSITION). */
+PKV_API int paged_latent_append(const void* latent, int64_t latent_stride, const void* k_rope,
+                                int64_t k_rope_stride, const void* norm_weight, float eps,
+                                const int64_t* slot_mapping, const int32_t* positions,
+                                const float* cos_sin, int32_t max_position, int32_t rope_layout,
+                                int32_t num_tokens, void* latent_cache, const void* q,
+                                int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                                int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                const pkv_latent_desc* desc, void* stream);
+
+/* Copy-on-write of whole blocks, as pkv_copy_blocks. */
+PKV_API int pkv_copy_blocks_latent(const int32_t* block_pairs, int32_t num_pairs,
+                                   void* latent_cache, const pkv_latent_desc* desc, void* stream);
+
+/* Read sequences back in order: token i of sequence s (its first
+ * key_start_loc[s + 1] - key_start_loc[s] tokens) to row key_start_loc[s] + i of
+ * latent_out [num_keys][latent_dim] and rope_out [num_keys][64], bit for bit.  Rows
+ * behind key_start_loc[num_seqs] are left as they are.  A row whose block id is out of
+ * range (PKV_DEV_BAD_BLOCK_ID) or past the table's width (PKV_DEV_TABLE_TOO_NARROW),
+ * or that no sequence holds because the offsets do not rise from 0
+ * (PKV_DEV_BAD_QUERY_LAYOUT), is left as it is; so is everything if the offsets end
+ * above num_keys. */
+PKV_API int paged_latent_gather(void* latent_out, void* rope_out, const void* latent_cache,
+                                const pkv_latent_desc* desc, const int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* key_start_loc,
+                                int32_t num_seqs, int32_t num_keys, void* stream);
+
+/* Bytes of workspace paged_attention_latent needs (0 on bad arguments). */
+PKV_API size_t pkv_latent_workspace_bytes(const pkv_latent_desc* desc, int32_t num_seqs,
+                                          int32_t num_query_tokens, int32_t max_context_len);
+
+/* Attention over the cached rows (absorbed form): for query token t and head h
+ *   out[t][h] = sum_j p_j c_j,  p = softmax_j(scale * (a . c_j + b . k_j)),  q[t][h] = (a, b)
+ * over the keys that the row sees.  Rows: query_start_loc NULL is one query token per
+ * sequence, its last; otherwise the layout of paged_attention_varlen, and row i of a
+ * sequence sees keys 0 .. context_lens - qlen + i.  Rows behind the last sequence are
+ * left as they are.
+ *   out:  device [num_query_tokens][num_q_heads][latent_dim]
+ *   q:    device [num_query_tokens][num_q_heads][latent_dim + 64]
+ *   scale: above 0; 1 / sqrt(the expanded key's size), which the cache does not tell
+ *   workspace: 256-byte aligned, not shared by concurrent calls
+ * Sums and softmax in fp32; for PKV_BF16 the weights enter the second product in bf16.
+ * The work is cut where the batch's keys divide evenly over the SMs, so a sequence's
+ * result depends on the batch by roundings.  A context outside [qlen, max_context_len]
+ * (PKV_DEV_BAD_CONTEXT_LEN) or of more blocks than max_blocks_per_seq
+ * (PKV_DEV_TABLE_TOO_NARROW) gives zeros; a block id out of range sets
+ * PKV_DEV_BAD_BLOCK_ID and leaves the sequence's outputs undefined; a sequence whose
+ * offsets fall or pass num_query_tokens, and the first where they do not begin with 0,
+ * is not computed (PKV_DEV_BAD_QUERY_LAYOUT). */
+PKV_API int paged_attention_latent(void* out, const void* q, const void* latent_cache,
+                                   const pkv_latent_desc* desc, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                   const int32_t* context_lens, int32_t num_seqs,
+                                   int32_t num_query_tokens, int32_t max_context_len, float scale,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keys and values of every head, as the expansion leaves them (no cache). */
+typedef struct pkv_expanded_desc {
+    int32_t dtype;        /* PKV_F32 or PKV_BF16 */
+    int32_t num_heads;
+    int32_t head_dim;     /* 64 or 128: of a key's first part and of a value */
+    int32_t rope_dim;     /* 64 */
+    int64_t k_token_stride, k_head_stride;   /* in values; rows start on 16 bytes */
+    int64_t v_token_stride, v_head_stride;
+} pkv_expanded_desc;
+
+PKV_API size_t pkv_expanded_workspace_bytes(const pkv_expanded_desc* desc, int32_t num_seqs,
+                                            int32_t num_query_tokens);
+
+/* Ragged causal attention over expanded keys: sequence s owns query rows
+ * query_start_loc[s] .. and key rows key_start_loc[s] .. ; with n keys and m queries,
+ * query i sees keys 0 .. n - m + i (a query that sees none, m > n, gives zeros):
+ *   out[t][h] = sum_j p_j v[j][h],
+ *   p = softmax_j(scale * (q[t][h][0 .. D-1] . k[j][h] + q[t][h][D .. D+63] . k_rope[j]))
+ *   out: device [num_query_tokens][num_heads][D]
+ *   q:   device [num_query_tokens][num_heads][D + 64]
+ *   k, v: device, D values at [j * token_stride + h * head_stride]
+ *   k_rope: device [num_keys][64], shared by all heads
+ *   max_query_len: host upper bound of a sequence's queries; longer ones are
+ *         PKV_DEV_BAD_QUERY_LAYOUT
+ *   scale: above 0; usually 1 / sqrt(head_dim + 64)
+ * Rows behind the last sequence are left as they are; a sequence whose offsets fall or
+ * pass num_query_tokens or num_keys is not computed (PKV_DEV_BAD_QUERY_LAYOUT).  Keys and
+ * values that no query of the call sees may hold anything.  Sums and softmax in fp32;
+ * for PKV_BF16 the weights enter the second product in bf16.  workspace: 256-byte
+ * aligned, not shared by concurrent calls. */
+PKV_API int pkv_attention_expanded(void* out, const void* q, const void* k, const void* v,
+                                   const void* k_rope, const pkv_expanded_desc* desc,
+                                   const int32_t* query_start_loc, const int32_t* key_start_loc,
+                                   int32_t num_seqs, int32_t num_query_tokens, int32_t num_keys,
+                                   int32_t max_query_len, float scale, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Read the current device's error word into *code_out (PKV_DEV_* code of the
  * first fault recorded since the last clear) and, if `clear` is non-zero,
  * reset it.  Synchronizes the device.  The word's device address is looked up

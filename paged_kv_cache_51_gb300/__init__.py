@@ -3,7 +3,7 @@
 Every function here only marshals arguments (tensor data pointers, sizes and
 the current CUDA stream) into the C ABI declared in include/pagedkv.h; all work
 runs in the library's CUDA kernels or its C++ block pool.  The calls of the
-shortest kernels (device tables, sparse attention) are marshalled by the extension
+shortest kernels (device tables, sparse and latent attention) are marshalled by the extension
 module _hotcalls, the others through ctypes.  There is no fallback: if the library
 is missing or was built for another machine, calls raise.
 
@@ -55,6 +55,9 @@ EXPORTS = (
     "paged_attention_varlen_window",
     "pkv_tables_step", "pkv_tables_release", "pkv_block_bounds", "pkv_select_workspace_bytes",
     "pkv_select_blocks", "paged_attention_sparse",
+    "paged_latent_append", "pkv_copy_blocks_latent", "paged_latent_gather",
+    "pkv_latent_workspace_bytes", "paged_attention_latent", "pkv_expanded_workspace_bytes",
+    "pkv_attention_expanded",
 )
 
 PKV_POOL_PREFIX_CACHING = 1
@@ -77,6 +80,19 @@ class DeviceTablesDesc(ctypes.Structure):
                 ("free_count", ctypes.c_void_p), ("max_seqs", ctypes.c_int32),
                 ("max_blocks", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32)]
+
+
+class LatentDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("num_q_heads", ctypes.c_int32)]
+
+
+class ExpandedDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -143,6 +159,17 @@ def lib():
                                              i32, i32, i32, i32, p, sz, p]),
         "paged_attention_sparse": (ctypes.c_int, [p, p, p, p, P(CacheDesc), p, i32, p, p, p, i32,
                                                   i32, i32, ctypes.c_float, p]),
+        "paged_latent_append": (ctypes.c_int, [p, i64, p, i64, p, ctypes.c_float, p, p, p, i32,
+                                               i32, i32, p, p, i64, i64, p, i64, i64,
+                                               P(LatentDesc), p]),
+        "pkv_copy_blocks_latent": (ctypes.c_int, [p, i32, p, P(LatentDesc), p]),
+        "paged_latent_gather": (ctypes.c_int, [p, p, p, P(LatentDesc), p, i32, p, i32, i32, p]),
+        "pkv_latent_workspace_bytes": (sz, [P(LatentDesc), i32, i32, i32]),
+        "paged_attention_latent": (ctypes.c_int, [p, p, p, P(LatentDesc), p, i32, p, p, i32, i32,
+                                                  i32, ctypes.c_float, p, sz, p]),
+        "pkv_expanded_workspace_bytes": (sz, [P(ExpandedDesc), i32, i32]),
+        "pkv_attention_expanded": (ctypes.c_int, [p, p, p, p, p, P(ExpandedDesc), p, p, i32, i32,
+                                                  i32, i32, ctypes.c_float, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -816,6 +843,92 @@ def paged_attention_sparse(out, q, k_cache, v_cache, desc, block_tables, context
     _check(_native().attention_sparse(out, q, k_cache, v_cache, desc, block_tables,
                                         context_lens, selected, query_start_loc, scale,
                                         _handle(stream)), "paged_attention_sparse")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# latent attention
+# ----------------------------------------------------------------------------
+def latent_desc(latent_cache, latent_dim, num_q_heads):
+    """Descriptor of a latent cache tensor [num_blocks, block_size, latent_dim + rope_dim]."""
+    nb, bs, width = latent_cache.shape
+    dt = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16}.get(latent_cache.dtype)
+    if dt is None:
+        raise TypeError("cache dtype must be float32 or bfloat16")
+    return LatentDesc(dt, nb, bs, latent_dim, width - latent_dim, num_q_heads)
+
+
+def paged_latent_append(latent, k_rope, slot_mapping, positions, cos_sin, latent_cache, desc,
+                        norm_weight=None, eps=1e-6, q=None, q_out=None, interleaved=False,
+                        stream=None):
+    """Write a step's latent vectors (CUDA [T, R], normalised by ``norm_weight`` [R] if
+    given) and rotated keys ([T, 64]) into the latent cache, and rotate the queries'
+    rotary part ``q`` [T, H, 64] into ``q_out`` (default: in place).  latent, k_rope, q and
+    q_out may be views whose last dimension is contiguous, such as the end of each head.
+    ``interleaved``: pairs of neighbours are rotated, instead of value i with i + 32."""
+    if q is not None and q_out is None:
+        q_out = q
+    _check(_native().latent_append(latent, k_rope, slot_mapping, positions, cos_sin, latent_cache,
+                                   desc, norm_weight, eps, q, q_out, interleaved,
+                                   _handle(stream)), "paged_latent_append")
+    return q_out
+
+
+def pkv_copy_blocks_latent(block_pairs, latent_cache, desc, stream=None):
+    """Copy-on-write for a latent cache; block_pairs: CUDA int32 [n, 2] (src, dst)."""
+    n = block_pairs.shape[0] if block_pairs is not None else 0
+    if n == 0:
+        return
+    _need(block_pairs, torch.int32, "block_pairs")
+    _need(latent_cache, _TORCH_DTYPE[desc.dtype], "latent_cache")
+    st = _stream_on_device(stream, ("block_pairs", block_pairs), ("latent_cache", latent_cache))
+    _check(lib().pkv_copy_blocks_latent(_ptr(block_pairs), n, _ptr(latent_cache),
+                                        ctypes.byref(desc), st), "pkv_copy_blocks_latent")
+
+
+def paged_latent_gather(latent_out, rope_out, latent_cache, desc, block_tables, key_start_loc,
+                        stream=None):
+    """Read sequences back in order: latent_out [N, R], rope_out [N, 64]; sequence s, whose
+    blocks are row s of block_tables (CUDA int32 [S, W]), goes to rows key_start_loc[s] ..
+    key_start_loc[s + 1] - 1 (CUDA int32 [S + 1])."""
+    _check(_native().latent_gather(latent_out, rope_out, latent_cache, desc, block_tables,
+                                   key_start_loc, _handle(stream)), "paged_latent_gather")
+    return latent_out, rope_out
+
+
+def latent_workspace_bytes(desc, num_seqs, num_query_tokens, max_context_len):
+    return int(lib().pkv_latent_workspace_bytes(ctypes.byref(desc), num_seqs, num_query_tokens,
+                                                max_context_len))
+
+
+def paged_attention_latent(out, q, latent_cache, desc, block_tables, context_lens,
+                           max_context_len, scale, query_start_loc=None, ws=None, stream=None):
+    """Attention over the cached rows (absorbed form): out CUDA [T, H, R], q [T, H, R + 64].
+    One token a sequence, its last, or query_start_loc (CUDA int32 [S + 1])."""
+    handle = _handle(stream)
+    if ws is None:
+        ws = _own_workspace(latent_workspace_bytes(desc, context_lens.shape[0], q.shape[0],
+                                                   max_context_len), q.device, stream)
+    _check(_native().attention_latent(out, q, latent_cache, desc, block_tables, context_lens,
+                                      max_context_len, scale, query_start_loc, ws, handle),
+           "paged_attention_latent")
+    return out
+
+
+def pkv_attention_expanded(out, q, k, v, k_rope, query_start_loc, key_start_loc, max_query_len,
+                           scale=None, ws=None, stream=None):
+    """Ragged causal attention over expanded keys: out CUDA [Tq, H, D], q [Tq, H, D + 64],
+    k and v [Tk, H, D] (views with contiguous last dimension), k_rope [Tk, 64] for all
+    heads; sequence s has query rows query_start_loc[s] .. and key rows key_start_loc[s] ..
+    (CUDA int32 [S + 1]).  scale: 1 / sqrt(D + 64) by default."""
+    handle = _handle(stream)
+    if ws is None:
+        need = _native().attention_expanded(out, q, k, v, k_rope, query_start_loc, key_start_loc,
+                                            max_query_len, scale, None, handle)
+        ws = _own_workspace(need, q.device, stream)
+    _check(_native().attention_expanded(out, q, k, v, k_rope, query_start_loc, key_start_loc,
+                                        max_query_len, scale, ws, handle),
+           "pkv_attention_expanded")
     return out
 
 

@@ -465,6 +465,31 @@ extern "C" int pkv_copy_blocks_int8(const int32_t* block_pairs, int32_t num_pair
     return cuda_status(cudaGetLastError());
 }
 
+extern "C" int pkv_copy_blocks_latent(const int32_t* block_pairs, int32_t num_pairs,
+                                      void* latent_cache, const pkv_latent_desc* desc, void* stream) {
+    int st = check_latent_desc(desc);
+    if (st != PKV_OK) return st;
+    if (num_pairs < 0) return PKV_ERR_INVALID;
+    if (num_pairs == 0) return PKV_OK;
+    if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (!block_pairs || !latent_cache || !aligned16(latent_cache) ||
+        (reinterpret_cast<uintptr_t>(block_pairs) & 3u))
+        return PKV_ERR_INVALID;
+    int* err = device_error_ptr(&st);
+    if (st != PKV_OK) return st;
+    CopyParams p;
+    p.pairs = block_pairs;
+    p.k_cache = static_cast<uint4*>(latent_cache);
+    p.v_cache = nullptr;
+    p.vec_per_block = int64_t(desc->block_size) * (desc->latent_dim + desc->rope_dim) *
+                      int64_t(elem_bytes(desc->dtype)) / 16;
+    p.num_blocks = desc->num_blocks;
+    p.err = err;
+    const unsigned gx = unsigned(std::min<int64_t>((p.vec_per_block + 255) / 256, 64));
+    return cuda_status(launch_pdl(copy_blocks_kernel, dim3(gx, unsigned(num_pairs)), dim3(256), 0,
+                                  static_cast<cudaStream_t>(stream), p));
+}
+
 extern "C" int paged_kv_append_rope(const void* q, void* q_out, const void* k, const void* v,
                                     const int64_t* slot_mapping, const int32_t* positions,
                                     const float* cos_sin, int32_t max_position,

@@ -22,6 +22,8 @@ inline size_t elem_bytes(int dtype) { return dtype == PKV_F32 ? 4 : 2; }
 // grouping and head_dim the attention kernels implement.
 int check_desc(const pkv_cache_desc* d, bool attention);
 
+int check_latent_desc(const pkv_latent_desc* d);
+
 // Address of this device's error word (looked up once per device).
 int* device_error_ptr(int* status);
 

@@ -107,4 +107,46 @@ bool make_query_tensor_map(CUtensorMap* m, const void* q, int32_t num_tokens, in
     return true;
 }
 
+// Rows of `columns` x 64 bf16 values side by side as (64 values, rows, columns): a box of
+// `box_rows` rows and all columns lands as [column][row][128 bytes], 128-byte swizzled.
+// Rows past the end read as zero.
+bool make_latent_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int32_t columns,
+                            int32_t box_rows) {
+    const MapKey key{2, base, rows, columns, box_rows, 0};
+    if (map_lookup(key, m)) return true;
+    auto fn = encode_fn();
+    if (!fn || rows < 1 || rows >= (int64_t(1) << 31)) return false;
+    const cuuint64_t gdim[3] = {64, cuuint64_t(rows), cuuint64_t(columns)};
+    const cuuint64_t gstride[2] = {cuuint64_t(columns) * 128, 128};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(columns)};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box,
+           estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    map_store(key, *m);
+    return true;
+}
+
+// bf16 [tokens][heads][dim] with strides in elements as (dims, heads, tokens); a box is 64
+// dims of one head and `box_tokens` tokens: 128-byte rows, 128-byte swizzled.
+bool make_strided_tensor_map(CUtensorMap* m, const void* base, int32_t dim, int32_t heads,
+                             int32_t tokens, int64_t head_stride, int64_t token_stride,
+                             int32_t box_tokens) {
+    const MapKey key{3 + int(dim) * 16 + box_tokens * 65536, base, heads, tokens, head_stride, token_stride};
+    if (map_lookup(key, m)) return true;
+    auto fn = encode_fn();
+    if (!fn || tokens < 1) return false;
+    const cuuint64_t gdim[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(tokens)};
+    const cuuint64_t gstride[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2};
+    const cuuint32_t box[3] = {64, 1, cuuint32_t(box_tokens)};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box,
+           estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    map_store(key, *m);
+    return true;
+}
+
 }  // namespace pkv
