@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (global_ns() - t0 < 1000000ull) {
                 }
             }
-        } else if (warp == kMmaWarp && lane == 0) {
+        } else if (warp == kMmaWarp && elect_one()) {
             constexpr uint32_t idesc_s = tc_idesc(kT, kT, false), idesc_o = tc_idesc(kT, D, true);
             const uint64_t qd = tc_smem_desc(base, 16, 1024);
             const uint64_t kd = tc_smem_desc(base + S::kRing, 16, 1024);

@@ -7,25 +7,28 @@
 // staged once in shared memory and is both operands: K-major for the first product,
 // and, through another descriptor over the same bytes, MN-major for the second.
 //
-// Shapes.  A CTA takes 64 (token, head) rows of one sequence and tiles of 64 keys.  A
-// product of 64 rows in its plain form runs at half the rate of 128 (measured: 128
-// cycles for 64 x 256 x 16, the same as 128 x 256 x 16); the .ws form spreads the
-// columns' halves over all 128 TMEM lanes and takes 80, bound by the 10 KB of shared
-// memory it reads at 128 bytes a cycle.  O of 512 values then needs 256 TMEM columns
-// (in the plain form with 128 rows it would take all 512 and leave none for S).
-// A thread of the softmax holds one row's 32 keys (lanes 0-63: the tile's first 32,
-// lanes 64-127 the others) and, when O is read, half of the row's values.
+// Shapes.  A CTA takes 64 (token, head) rows of one sequence and tiles of 32 keys.
+// Products of this size are bound by the shared memory they read (128 bytes a cycle;
+// measured, in cycles: 64 x 32 x 16 takes 24, 64 x 64 x 16 32, 64 x 256 x 16 80 in the .ws
+// form, which spreads the halves of the columns over all 128 TMEM lanes, and 128 in the
+// plain form): a tile's S takes 864 and its P C 320, of the 1575 that an SM's share of HBM
+// needs for its 36 KB.  64-key tiles take 896 in all, but only two of them fit beside the
+// queries (72 KB of 227): with two buffers that are empty at about the same time the SM
+// computes on both while nothing is being loaded, and 4 x 32k keys took 40 us instead of 31.
 //
-// Shared memory: 64 query rows (latent 512: 72 KB), two key tiles (144 KB), P (8 KB).
-// Rows lie as [8-row group][64-value column][8 rows][128 bytes, swizzled], which one
-// TMA box a group fills (9 KB) and whose groups and columns are both evenly spaced,
-// as the two descriptors need.
+// S (plain form: row 16 w + i in lane 32 w + i) is read with the 16x256b shape, so a
+// thread holds 8 keys of two rows and four threads share a row.  O (.ws form: row r in
+// lanes r and 64 + r, a half of the columns each) is read a lane a thread.  The two meet
+// only where O has to be rescaled, which the warps tell one another through shared memory.
 //
-// Warps: 0 loads (queries, tiles), 1 issues the products, 2 and 3 zero the rows of
-// sequences that the call does not allow, 4-7 are the softmax.  S of the next tile goes
-// out while the softmax works on this one; the issuer takes whichever of the two
-// products is ready, so a tile that has not landed does not hold back the P C that
-// frees the other.
+// Shared memory: the query rows (latent 512: 72 KB for 64 rows, less for fewer), as many
+// tile buffers as fit (4 to 8), two P buffers (4 KB each).  Rows lie as [8-row group]
+// [64-value column][8 rows][128 bytes, swizzled], which one TMA box a group fills (9 KB)
+// and whose groups and columns are both evenly spaced, as the two descriptors need.
+//
+// Warps: 0 loads (queries, tiles), 1 issues S, 2 P C, 3 zeroes the rows of sequences that
+// the call does not allow, 4-7 are the softmax.  (One thread that issued both took 1727
+// cycles a tile, 450 of them its own waits and bookkeeping between the two.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -39,41 +42,56 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 64;
-constexpr int kKeys = 64;
+constexpr int kKeys = 32;
 constexpr int kThreads = 256;
 constexpr int kSoftWarp0 = 4;
 constexpr int kSoftWarps = 4;
 constexpr int kLoadWarp = 0;
-constexpr int kMmaWarp = 1;
+constexpr int kMmaWarp = 1;                // S; owns TMEM
+constexpr int kPcWarp = 2;                 // P C
 constexpr int kGroups = kKeys / 8;         // 8-row groups of a tile
-constexpr int kPBytes = kRows * kKeys * 2;
+constexpr int kPBytes = 2 * kRows * kKeys * 2;
+constexpr int kSBufs = 4;
+constexpr int kMostSlots = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;            // S buffers: 32 columns each behind O
 constexpr float kRescale = 8.f;            // log2 units: O is rescaled when a row's max grows by more
-constexpr int kLeastSteps = 2;             // a CTA takes at least 128 keys
+constexpr int kLeastSteps = 4;             // a CTA takes at least 128 keys
 
 enum {
     B_K_FULL = 0,                          // [tile buffer]
-    B_S_FULL = B_K_FULL + 2,               // [S buffer]
-    B_S_EMPTY = B_S_FULL + 2,              // [S buffer]: the softmax has loaded it
-    B_O_DONE = B_S_EMPTY + 2,              // [tile buffer]: its P C is complete, the buffer is free
-    B_P_FULL = B_O_DONE + 2,
-    B_Q_FULL,
+    B_O_DONE = B_K_FULL + kMostSlots,      // [tile buffer]: its P C is complete, the buffer is free
+    B_S_FULL = B_O_DONE + kMostSlots,      // [S buffer]
+    B_S_EMPTY = B_S_FULL + kSBufs,         // [S buffer]: the softmax has loaded it
+    B_P_FULL = B_S_EMPTY + kSBufs,         // [P buffer]
+    B_Q_FULL = B_P_FULL + 2,
     B_Q_EMPTY,                             // the fragment's last S is complete
     B_O_EMPTY,                             // the softmax has read the fragment's O
-    B_XM,                                  // [row half]: both key halves' maxima are there
-    B_SUM = B_XM + 2,                      // [row half]: both key halves' sums are there
-    B_DRAIN = B_SUM + 2,
-    B_COUNT
+    B_NEED,                                // every warp has said whether its rows' O is rescaled
+    B_SUM,                                 // the rows' sums are there
+    B_DRAIN,                               // [issuer]
+    B_COUNT = B_DRAIN + 2
 };
 
 struct Smem {                              // behind the operands
     uint64_t bars[B_COUNT];
     int64_t sums[kThreads / 32 + 2];
-    float xm[2][128];
-    float sum[128];
+    float alpha[2][kRows];                 // [tile parity]
+    int need[2][kSoftWarps];
+    float m[kRows], l[kRows];              // at the end of a fragment
     uint32_t tmem;
     int abort;
+};
+
+// A place in the ring of tile buffers: tile g is in buffer g % slots.
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ void next(uint32_t slots) {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -85,10 +103,32 @@ __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
+__device__ __forceinline__ void mma_plain(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// 16 lanes x 32 columns: register 4 i + e of lane t is row t / 4 + 8 (e / 2), column
+// 8 i + 2 (t % 4) + e % 2
+__device__ __forceinline__ void tc_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15},"
+        " [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15])
+        : "r"(taddr));
+}
+
 struct Params {
     LatentBatch b;
     LatentWorkspace ws;
     __nv_bfloat16* out;
+    int32_t q_groups;                      // 8-row groups of the query buffer
+    int32_t slots;
 };
 
 using Walk = LatentWalk<kRows, kKeys>;
@@ -131,10 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cols = p.b.latent / 64 + 1;                 // 64-value columns of a row
     const uint32_t group = uint32_t(cols) * 1024;         // bytes of an 8-row group
     const uint32_t tile = group * kGroups;
-    const uint32_t k_at = base + tile, p_at = base + 3 * tile;
-    unsigned char* k_ptr = smem + tile;
-    unsigned char* p_ptr = smem + 3 * tile;
-    Smem& sh = *reinterpret_cast<Smem*>(smem + 3 * tile + kPBytes);
+    const uint32_t slots = uint32_t(p.slots);
+    // P first: the products read 64 query rows whatever the buffer holds, and then what
+    // lies behind it, which is still shared memory (the tile buffers)
+    const uint32_t p_at = base, q_at = base + kPBytes;
+    const uint32_t k_off = kPBytes + uint32_t(p.q_groups) * group, k_at = base + k_off;
+    unsigned char* p_ptr = smem;
+    unsigned char* k_ptr = smem + k_off;
+    Smem& sh = *reinterpret_cast<Smem*>(k_ptr + slots * tile);
     uint64_t* bars = sh.bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_flag = &sh.abort;
@@ -143,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
             int n = 1;
-            if (i == B_S_EMPTY || i == B_S_EMPTY + 1 || i == B_P_FULL || i == B_O_EMPTY) n = kSoftWarps;
-            if (i >= B_XM && i < B_DRAIN) n = 2;
+            if (i >= B_S_EMPTY && i < B_Q_FULL) n = kSoftWarps;
+            if (i == B_O_EMPTY || i == B_NEED || i == B_SUM) n = kSoftWarps;
             mbar_init(&bars[i], n);
         }
         sh.abort = 0;
@@ -165,116 +209,114 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
     if (warp == kLoadWarp) {
-        // ---- queries and key tiles: lane i < 8 loads the 8 rows of group i ----
+        // ---- queries and key tiles: lane i < 4 loads the 8 rows of group i ----
         Tiles t;
+        Ring at;
         bool ok = true;
         uint32_t q_loads = 0, k_loads = 0;
         for (t.start(p.b, plan); t.live; t.next(p.b)) {
             const int32_t* table = p.b.block_tables + int64_t(t.f.seq) * p.b.table_stride;
+            const int key0 = (t.f.kt0 + t.j) * kKeys;
+            const int groups = (min(kKeys, t.f.ctx - key0) + 7) / 8;
+            const int blk = lane < groups ? __ldg(table + key0 / kBlockTokens + (lane >> 1)) : 0;
             if (t.j == 0) {
                 ok = __all_sync(0xffffffffu, t.k == 0 || mbar_wait(&bars[B_Q_EMPTY], (t.k - 1) & 1, err));
                 if (!ok || *abort_flag) break;
-                const int groups = (t.f.nrows + 7) / 8;
-                if (lane == 0) mbar_arrive_expect_tx(&bars[B_Q_FULL], uint32_t(groups) * group);
+                const int rows = (t.f.nrows + 7) / 8;
+                if (lane == 0) mbar_arrive_expect_tx(&bars[B_Q_FULL], uint32_t(rows) * group);
                 ++q_loads;
                 __syncwarp();
-                if (lane < groups)
-                    tc_load_3d(base + uint32_t(lane) * group, &map_q, 0, t.f.row0 + lane * 8, 0,
+                if (lane < rows)
+                    tc_load_3d(q_at + uint32_t(lane) * group, &map_q, 0, t.f.row0 + lane * 8, 0,
                                &bars[B_Q_FULL]);
             }
-            const int key0 = (t.f.kt0 + t.j) * kKeys;
-            const int keys = min(kKeys, t.f.ctx - key0);
-            const int groups = (keys + 7) / 8;
-            int blk = lane < groups ? __ldg(table + key0 / kBlockTokens + (lane >> 1)) : 0;
-            const uint32_t st = t.g & 1;
             ok = __all_sync(0xffffffffu,
-                            t.g < 2 || mbar_wait(&bars[B_O_DONE + st], ((t.g - 2) >> 1) & 1, err));
+                            t.g < slots || mbar_wait(&bars[B_O_DONE + at.slot], at.phase ^ 1, err));
             if (!ok || *abort_flag) break;
             const bool good = lane < groups && blk >= 0 && blk < p.b.num_blocks;
             if (lane < groups && !good) flag_error(err, PKV_DEV_BAD_BLOCK_ID);
             const unsigned mask = __ballot_sync(0xffffffffu, good);
-            if (lane == 0) mbar_arrive_expect_tx(&bars[B_K_FULL + st], uint32_t(__popc(mask)) * group);
+            uint64_t* full = &bars[B_K_FULL + at.slot];
+            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(__popc(mask)) * group);
             ++k_loads;
             __syncwarp();
             if (good)
-                tc_load_3d(k_at + st * tile + uint32_t(lane) * group, &map_kv, 0,
-                           blk * kBlockTokens + (lane & 1) * 8, 0, &bars[B_K_FULL + st]);
+                tc_load_3d(k_at + at.slot * tile + uint32_t(lane) * group, &map_kv, 0,
+                           blk * kBlockTokens + (lane & 1) * 8, 0, full);
             __syncwarp();
+            at.next(slots);
         }
         if (t.live) *abort_flag = 1;
         // never leave with copies in flight
         if (lane == 0) {
             if (q_loads > 0) mbar_wait(&bars[B_Q_FULL], (q_loads - 1) & 1, err);
-            for (uint32_t i = 0; i < 2 && i < k_loads; ++i) {
+            for (uint32_t i = 0; i < slots && i < k_loads; ++i) {
                 const uint32_t last = k_loads - 1 - i;
-                mbar_wait(&bars[B_K_FULL + (last & 1)], (last >> 1) & 1, err);
+                mbar_wait(&bars[B_K_FULL + last % slots], (last / slots) & 1, err);
             }
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            // S of tile g goes to S buffer g & 1 and P C of tile g follows it; whichever is
-            // ready first goes out, S in front where both are
-            const uint32_t idesc_s = tc_idesc(kRows, kKeys, false);
-            const int n0 = min(256, p.b.latent), n1 = p.b.latent - n0;
-            const uint32_t idesc_o0 = tc_idesc(kRows, n0, true), idesc_o1 = tc_idesc(kRows, n1, true);
-            const uint64_t qd = tc_smem_desc(base, 16, group);
+        if (elect_one()) {
+            constexpr uint32_t idesc = tc_idesc(kRows, kKeys, false);
+            const uint64_t qd = tc_smem_desc(q_at, 16, group);
             const uint64_t kd = tc_smem_desc(k_at, 16, group);
-            const uint64_t vd = tc_smem_desc(k_at, 1024, group);
-            const uint64_t pd = tc_smem_desc(p_at, 16, 1024);
-            Tiles s, o;
-            s.start(p.b, plan);
-            o.start(p.b, plan);
+            Tiles t;
+            Ring at;
             bool ok = true;
-            uint64_t t0 = 0;
-            uint32_t spins = 0;
-            while (o.live && ok) {
-                bool moved = false;
-                if (s.live && s.g <= o.g + 1 && (s.g < 2 || mbar_test(&bars[B_S_EMPTY + (s.g & 1)], ((s.g - 2) >> 1) & 1)) &&
-                    mbar_test(&bars[B_K_FULL + (s.g & 1)], (s.g >> 1) & 1) &&
-                    (s.j != 0 || mbar_test(&bars[B_Q_FULL], s.k & 1))) {
-                    tc_fence_after();
-                    const uint32_t d = tmem + kSCol + (s.g & 1) * 32;
-                    const uint64_t k0 = kd + uint64_t((s.g & 1) * (tile >> 4));
-                    for (int c = 0; c < cols; ++c) {
+            for (t.start(p.b, plan); t.live; t.next(p.b)) {
+                const uint32_t sb = t.g & (kSBufs - 1);
+                const uint32_t d = tmem + kSCol + sb * 32;
+                const uint64_t k0 = kd + uint64_t(at.slot * (tile >> 4));
+                ok = (t.j != 0 || mbar_wait(&bars[B_Q_FULL], t.k & 1, err)) &&
+                     (t.g < kSBufs || mbar_wait(&bars[B_S_EMPTY + sb], ((t.g / kSBufs) & 1) ^ 1, err)) &&
+                     mbar_wait(&bars[B_K_FULL + at.slot], at.phase, err);
+                if (!ok || *abort_flag) break;
+                tc_fence_after();
+                for (int c = 0; c < cols; ++c) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_ws(d, qd + uint64_t(c * 64 + i * 2), k0 + uint64_t(c * 64 + i * 2),
-                                   idesc_s, (c | i) != 0);
-                    }
-                    tc_commit(&bars[B_S_FULL + (s.g & 1)]);
-                    if (s.j == s.f.n - 1) tc_commit(&bars[B_Q_EMPTY]);
-                    s.next(p.b);
-                    moved = true;
+                    for (int i = 0; i < 4; ++i)
+                        mma_plain(d, qd + uint64_t(c * 64 + i * 2), k0 + uint64_t(c * 64 + i * 2), idesc,
+                                  (c | i) != 0);
                 }
-                if (o.g < s.g && mbar_test(&bars[B_P_FULL], o.g & 1) &&
-                    (o.j != 0 || o.k == 0 || mbar_test(&bars[B_O_EMPTY], (o.k - 1) & 1))) {
-                    tc_fence_after();
-                    const uint64_t v0 = vd + uint64_t((o.g & 1) * (tile >> 4));
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i) {
-                        const uint32_t acc = (o.j | i) != 0;
-                        const uint64_t v = v0 + uint64_t(i * 2 * (group >> 4));
-                        mma_ws(tmem, pd + uint64_t(i * 2), v, idesc_o0, acc);
-                        if (n1 > 0) mma_ws(tmem + 128, pd + uint64_t(i * 2), v + 4 * 64, idesc_o1, acc);
-                    }
-                    tc_commit(&bars[B_O_DONE + (o.g & 1)]);
-                    o.next(p.b);
-                    moved = true;
-                }
-                if (moved) {
-                    spins = 0;
-                } else if (++spins == 64) {
-                    t0 = global_ns();
-                } else if (spins > 64 && (spins & 63) == 0 &&
-                           (*abort_flag || global_ns() - t0 > kWaitLimitNs)) {
-                    if (!*abort_flag) flag_error(err, PKV_DEV_WAIT_TIMEOUT);
-                    ok = false;
-                }
+                tc_commit(&bars[B_S_FULL + sb]);
+                if (t.j == t.f.n - 1) tc_commit(&bars[B_Q_EMPTY]);
+                at.next(slots);
             }
-            if (!ok) *abort_flag = 1;
+            if (t.live) *abort_flag = 1;
             tc_commit(&bars[B_DRAIN]);
             mbar_wait(&bars[B_DRAIN], 0, err);
+        }
+        __syncwarp();
+    } else if (warp == kPcWarp) {
+        if (elect_one()) {
+            const int n0 = min(256, p.b.latent), n1 = p.b.latent - n0;
+            const uint32_t idesc0 = tc_idesc(kRows, n0, true), idesc1 = tc_idesc(kRows, n1, true);
+            const uint64_t vd = tc_smem_desc(k_at, 1024, group);
+            const uint64_t pd = tc_smem_desc(p_at, 16, 1024);
+            Tiles t;
+            Ring at;
+            bool ok = true;
+            for (t.start(p.b, plan); t.live; t.next(p.b)) {
+                const uint64_t v0 = vd + uint64_t(at.slot * (tile >> 4));
+                const uint64_t p0 = pd + uint64_t((t.g & 1) * 4);
+                ok = (t.j != 0 || t.k == 0 || mbar_wait(&bars[B_O_EMPTY], (t.k - 1) & 1, err)) &&
+                     mbar_wait(&bars[B_P_FULL + (t.g & 1)], (t.g >> 1) & 1, err);
+                if (!ok || *abort_flag) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i) {
+                    const uint32_t acc = (t.j | i) != 0;
+                    const uint64_t v = v0 + uint64_t(i * 2 * (group >> 4));
+                    mma_ws(tmem, p0 + uint64_t(i * 2), v, idesc0, acc);
+                    if (n1 > 0) mma_ws(tmem + 128, p0 + uint64_t(i * 2), v + 4 * 64, idesc1, acc);
+                }
+                tc_commit(&bars[B_O_DONE + at.slot]);
+                at.next(slots);
+            }
+            if (t.live) *abort_flag = 1;
+            tc_commit(&bars[B_DRAIN + 1]);
+            mbar_wait(&bars[B_DRAIN + 1], 0, err);
         }
         __syncwarp();
     } else if (warp < kSoftWarp0) {
@@ -284,109 +326,110 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!x.zero) continue;
             const int64_t row_vecs = int64_t(p.b.heads) * p.b.latent / 8;
             uint4* dst = reinterpret_cast<uint4*>(p.out) + int64_t(x.q0) * row_vecs;
-            for (int64_t i = (warp - 2) * 32 + lane; i < row_vecs * x.qlen; i += 64)
+            for (int64_t i = lane; i < row_vecs * x.qlen; i += 32)
                 dst[i] = make_uint4(0, 0, 0, 0);
         }
     } else {
-        // ---- softmax: thread = (row r, key half h) ----
+        // ---- softmax: thread = 8 keys of rows ra and ra + 8 ----
         const int w4 = warp - kSoftWarp0;
-        const int r = (w4 & 1) * 32 + lane, h = w4 >> 1;
+        const int ra = w4 * 16 + (lane >> 2), quad = lane & 3;
         const uint32_t lanes = uint32_t(w4 * 32) << 16;
+        // O: row r, half h of the columns of each product
+        const int r = (w4 & 1) * 32 + lane, h = w4 >> 1;
         const int n0 = min(256, p.b.latent);
         const int half0 = n0 / 2, half1 = (p.b.latent - n0) / 2;
         const int ocols = half0 + half1;                  // TMEM columns of O
         Walk w = plan;
         LatentFrag f;
         uint32_t g = 0, k = 0;
+        Ring at, prev, prev2;                             // tiles g, g - 1 and g - 2
         bool ok = true;
         if (int(threadIdx.x) == kSoftWarp0 * 32) p.ws.merge[blockIdx.x].nrows = 0;
         while (w.next(p.b, f)) {
-            const int tok = f.t0 + (f.rest + r) / p.b.heads;
-            const int limit = r < f.nrows ? f.first_pos + tok : -1;   // last key that the row sees
-            float m = -INFINITY, l = 0.f;
+            int limit[2];                                 // last key that the row sees
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = ra + 8 * e;
+                limit[e] = row < f.nrows ? f.first_pos + f.t0 + (f.rest + row) / p.b.heads : -1;
+            }
             for (int j = 0; j < f.n; ++j, ++g) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_S_FULL + (g & 1)], (g >> 1) & 1, err));
+                const uint32_t sb = g & (kSBufs - 1);
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_S_FULL + sb], (g / kSBufs) & 1, err));
                 if (!ok) break;
                 tc_fence_after();
-                float s[32];
+                float s[16];
                 {
-                    uint32_t v[32];
-                    tc_ld32(tmem + lanes + kSCol + (g & 1) * 32, v);
+                    uint32_t v[16];
+                    tc_ld_16x32(tmem + lanes + kSCol + sb * 32, v);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(v[i]) * p.b.scale_log2;
+                    for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(v[i]) * p.b.scale_log2;
                 }
-                const int key0 = (f.kt0 + j) * kKeys;
-                const int khalf = key0 + h * 32;
-                if (khalf + 31 > limit) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = khalf + i <= limit ? s[i] : -INFINITY;
-                }
-                float mx4[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(s[i], s[i + 4]);
-#pragma unroll
-                for (int i = 8; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                // the row's other key half is the same lane of the warp two on
-                sh.xm[g & 1][h * 64 + r] = mx;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[B_XM + (w4 & 1)]);
-                    mbar_arrive(&bars[B_S_EMPTY + (g & 1)]);
+                if (lane == 0) mbar_arrive(&bars[B_S_EMPTY + sb]);
+                const int key0 = (f.kt0 + j) * kKeys;
+                if (key0 + kKeys - 1 > min(limit[0], limit[1])) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[i] = key0 + 8 * (i >> 2) + 2 * quad + (i & 1) <= limit[(i >> 1) & 1] ? s[i] : -INFINITY;
                 }
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_XM + (w4 & 1)], g & 1, err));
-                if (!ok) break;
-                const float m_new = fmaxf(m, fmaxf(mx, sh.xm[g & 1][(h ^ 1) * 64 + r]));
-                const bool need = m_new > m + kRescale;   // first visible keys included
-                float alpha = 1.f;
-                if (need) {
-                    alpha = exp2_fast(m - m_new);
-                    m = m_new;
-                    l *= alpha;
+                float alpha[2], neg_m[2];
+                bool need = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[2 * e], s[2 * e + 1]);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) mx = fmaxf(mx, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float m_new = fmaxf(m[e], mx);
+                    alpha[e] = 1.f;
+                    if (m_new > m[e] + kRescale) {         // first visible keys included
+                        alpha[e] = exp2_fast(m[e] - m_new);
+                        m[e] = m_new;
+                        l[e] *= alpha[e];
+                        need = true;
+                    }
+                    neg_m[e] = m[e] == -INFINITY ? 0.f : -m[e];
                 }
+                // O has nothing to rescale in a fragment's first tile
+                const bool tell = j > 0 && __any_sync(0xffffffffu, need);
+                if (tell && quad == 0) {
+                    sh.alpha[g & 1][ra] = alpha[0];
+                    sh.alpha[g & 1][ra + 8] = alpha[1];
+                }
+                if (lane == 0) sh.need[g & 1][w4] = tell;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_NEED]);
                 // P in bf16: 2^-8 of a weight at most; the sum is taken of the same rounded
                 // weights, so that what is lost does not shift the weighted mean
-                const float neg_m = m == -INFINITY ? 0.f : -m;
-                uint32_t pk[16];
-                float sum[2] = {0.f, 0.f};
+                uint32_t pk[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    pk[i] = pack_bf16x2(exp2_fast(s[2 * i] + neg_m), exp2_fast(s[2 * i + 1] + neg_m));
-                    sum[0] += __uint_as_float(pk[i] << 16);
-                    sum[1] += __uint_as_float(pk[i] & 0xffff0000u);
+                for (int i = 0; i < 8; ++i) {
+                    const int e = i & 1;
+                    pk[i] = pack_bf16x2(exp2_fast(s[2 * i] + neg_m[e]), exp2_fast(s[2 * i + 1] + neg_m[e]));
+                    l[e] += __uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xffff0000u);
                 }
-                l += sum[0] + sum[1];
-                // the previous tile's P C reads P and O
-                if (g > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + ((g - 1) & 1)],
-                                                           ((g - 1) >> 1) & 1, err));
+                // the P buffer was read by the tile before the last
+                if (g >= 2) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev2.slot], prev2.phase, err));
                     if (!ok) break;
                 }
-                tc_fence_after();
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
-                    for (int c = 0; c < ocols; c += 32) {
-                        uint32_t v[32];
-                        const uint32_t at = tmem + lanes + (c < half0 ? c : 128 + c - half0);
-                        tc_ld32(at, v);
-                        tc_wait_ld();
+                // (row & 7) is lane / 4 for both rows
+                unsigned char* row = p_ptr + ra * 128 + quad * 4;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                        tc_st32(at, v);
-                    }
-                    tc_wait_st();
+                for (int i = 0; i < 4; ++i) {
+                    const int c = ((((g & 1) * 4 + i) ^ (lane >> 2)) * 16);
+                    *reinterpret_cast<uint32_t*>(row + c) = pk[2 * i];
+                    *reinterpret_cast<uint32_t*>(row + 8 * 128 + c) = pk[2 * i + 1];
                 }
-                unsigned char* row = p_ptr + r * 128;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4*>(row + (((h * 4 + c) ^ (r & 7)) * 16)) =
-                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                 // rows behind the context hold another tile's or nothing: their values are
                 // zeroed, since 0 times anything must stay 0
                 const int keys = f.ctx - key0;
                 if (keys < kKeys) {
-                    unsigned char* ks = k_ptr + (g & 1) * tile;
+                    unsigned char* ks = k_ptr + at.slot * tile;
                     const int vecs = cols * 8;             // 16-byte vectors of a row
                     for (int i = w4 * 32 + lane; i < (kKeys - keys) * vecs; i += 128) {
                         const int row_i = keys + i / vecs, c = i % vecs;
@@ -396,47 +439,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fence_proxy_async_shared();
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_NEED], g & 1, err));
+                if (!ok) break;
+                const volatile int* any = sh.need[g & 1];
+                if (any[0] | any[1] | any[2] | any[3]) {
+                    // the previous tile's P C adds to O
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev.slot], prev.phase, err));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float a = any[r >> 4] ? sh.alpha[g & 1][r] : 1.f;
+                    for (int c = 0; c < ocols; c += 32) {
+                        uint32_t v[32];
+                        const uint32_t to = tmem + lanes + (c < half0 ? c : 128 + c - half0);
+                        tc_ld32(to, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+                        tc_st32(to, v);
+                    }
+                    tc_wait_st();
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_P_FULL]);
+                if (lane == 0) mbar_arrive(&bars[B_P_FULL + (g & 1)]);
+                prev2 = prev;
+                prev = at;
+                at.next(slots);
             }
             if (!ok) break;
             // ---- the fragment's output or state ----
+            float mr = -INFINITY, lr = 0.f;                // of row r
             if (f.n > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + ((g - 1) & 1)],
-                                                       ((g - 1) >> 1) & 1, err));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                    if (quad == 0) {
+                        sh.m[ra + 8 * e] = m[e];
+                        sh.l[ra + 8 * e] = l[e];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_SUM]);
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev.slot], prev.phase, err) &&
+                                                 mbar_wait(&bars[B_SUM], k & 1, err));
                 if (!ok) break;
                 tc_fence_after();
-                sh.sum[h * 64 + r] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_SUM + (w4 & 1)]);
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_SUM + (w4 & 1)], k & 1, err));
-                if (!ok) break;
-                l += sh.sum[(h ^ 1) * 64 + r];
+                mr = sh.m[r];
+                lr = sh.l[r];
             }
-            if (!f.whole && h == 0) p.ws.ml[f.slot * kLatentRowTile + r] = make_float2(m, l);
+            if (!f.whole && h == 0) p.ws.ml[f.slot * kLatentRowTile + r] = make_float2(mr, lr);
             if (f.starts && int(threadIdx.x) == kSoftWarp0 * 32)
                 p.ws.merge[blockIdx.x] = LatentMerge{f.row0, f.nrows, int(blockIdx.x), f.last_cta, f.slot};
             if (f.n > 0) {
-                const float inv = 1.f / l;
+                const float inv = 1.f / lr;
                 __nv_bfloat16* dst = p.out + int64_t(f.row0 + r) * p.b.latent;
                 float* part = p.ws.o + int64_t(f.slot) * kLatentRowTile * p.b.latent;
                 for (int c = 0; c < ocols; c += 32) {
                     uint32_t v[32];
                     tc_ld32(tmem + lanes + (c < half0 ? c : 128 + c - half0), v);
                     tc_wait_ld();
-                    if (f.whole) {
-                        if (r < f.nrows) {
-                            const int d = c < half0 ? h * half0 + c : n0 + h * half1 + c - half0;
+                    if (r >= f.nrows) {
+                    } else if (f.whole) {
+                        const int d = c < half0 ? h * half0 + c : n0 + h * half1 + c - half0;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t o[4];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t o[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    o[e] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * e]) * inv,
-                                                       __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-                                *reinterpret_cast<uint4*>(dst + d + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                o[e] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * e]) * inv,
+                                                   __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4*>(dst + d + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                     } else {
                         // [4 columns][lane]: a warp writes 512 bytes in a row
@@ -445,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4*>(part + ((c / 4 + i) * 128 + h * 64 + r) * 4) =
                                 make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     }
+                    __syncwarp();
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -464,40 +538,123 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // States of a cut unit, joined in the order of its keys:
 //   M = max m_i,  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// CTA (i, y): merge i, 8 values of each lane y holds.  A thread reads its values of every
-// state (16 bytes, neighbours side by side) and writes 16 bytes of a row.
-__global__ void __launch_bounds__(128) latent_merge_kernel(Params p) {
+// One wave of CTAs, resident before the attention ends.  Every CTA lists the cut units for
+// itself; a warp takes 32 lanes and 8 columns of a unit at a time and asks for the states
+// of eight CTAs at once, so that what it waits for is one trip to L2 (reading state by
+// state took 13 us for 64 requests of 512 to 4096 tokens, this 6).  Where there are fewer
+// such items than warps, 2, 4 or 8 warps of a CTA share one, each with a share of the
+// states, and meet in shared memory.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeBatch = 8;
+
+__global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(Params p, int ctas) {
+    __shared__ LatentMerge list[kMergeThreads];
+    __shared__ int counts[kMergeWarps], tall;
+    __shared__ float shared[kMergeWarps][10][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int latent = p.b.latent, pairs = latent / 16, team = p.b.team;
+    const int64_t stride = int64_t(kLatentRowTile) * latent;
+    const int n0 = min(256, latent), half0 = n0 / 2, half1 = (latent - n0) / 2;
     pdl_wait_prerequisites();
-    const LatentMerge e = p.ws.merge[blockIdx.x];
-    const int r = threadIdx.x & 63, h = threadIdx.x >> 6;
-    if (r >= e.nrows) return;
-    float big = -INFINITY;
-    for (int c = e.first; c <= e.last; ++c)
-        big = fmaxf(big, p.ws.ml[(c == e.first ? e.first_slot : 2 * c) * kLatentRowTile + r].x);
-    float acc[8] = {}, sum = 0.f;
-    const int64_t stride = int64_t(kLatentRowTile) * p.b.latent;
-    const int at = (blockIdx.y * 2 * 128 + threadIdx.x) * 4;
-    for (int c = e.first; c <= e.last; ++c) {
-        const int slot = c == e.first ? e.first_slot : 2 * c;
-        const float2 ml = p.ws.ml[slot * kLatentRowTile + r];
-        if (!(ml.y != 0.f)) continue;                     // no visible keys: nothing was written
-        const float w = exp2f(ml.x - big);
-        sum += w * ml.y;
-        const float* o = p.ws.o + slot * stride + at;
-        const float4 a = *reinterpret_cast<const float4*>(o), b = *reinterpret_cast<const float4*>(o + 512);
-        acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
-        acc[4] += w * b.x; acc[5] += w * b.y; acc[6] += w * b.z; acc[7] += w * b.w;
+    for (int base = 0; base < ctas; base += kMergeThreads) {
+        LatentMerge e{};
+        if (base + int(threadIdx.x) < ctas) e = p.ws.merge[base + threadIdx.x];
+        const unsigned mask = __ballot_sync(0xffffffffu, e.nrows > 0);
+        if (lane == 0) counts[warp] = __popc(mask);
+        if (threadIdx.x == 0) tall = 0;
+        __syncthreads();
+        int at = __popc(mask & ((1u << lane) - 1)), units = 0;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            if (w < warp) at += counts[w];
+            units += counts[w];
+        }
+        if (e.nrows > 0) list[at] = e;
+        if (e.nrows > 32) tall = 1;
+        __syncthreads();
+        const int quarters = tall ? 4 : 2;                // of a unit's 128 lanes
+        const int items = units * pairs * quarters, all = int(gridDim.x) * kMergeWarps;
+        const int share = items * 8 <= all ? 8 : items * 4 <= all ? 4 : items * 2 <= all ? 2 : 1;
+        const int per_cta = kMergeWarps / share, mine = warp % share;
+        for (int i0 = blockIdx.x * per_cta; i0 < items; i0 += gridDim.x * per_cta) {
+            const int item = i0 + warp / share;
+            const bool live = item < items;
+            const int u = live ? item / (pairs * quarters) : 0, rest = live ? item - u * pairs * quarters : 0;
+            const int pair = rest / quarters, q = rest - pair * quarters;
+            const LatentMerge m = list[u];
+            // quarters of rows 0-31 first: lanes 0, 64, 32, 96 ..
+            const int h = q & 1, r = (q >> 1) * 32 + lane;
+            const bool row = live && r < m.nrows;
+            const float* o0 = p.ws.o + (pair * 256 + h * 64 + r) * 4;
+            float acc[8] = {}, sum = 0.f, big = -INFINITY;
+            const int n = (m.last - m.first) / team + 1;
+            for (int c0 = mine; row && c0 < n; c0 += kMergeBatch * share) {
+                float2 ml[kMergeBatch];
+                float4 o[kMergeBatch][2];
+#pragma unroll
+                for (int i = 0; i < kMergeBatch; ++i) {
+                    const int c = c0 + i * share, slot = c == 0 ? m.first_slot : 2 * (m.first + c * team);
+                    ml[i] = make_float2(-INFINITY, 0.f);
+                    if (c < n) {
+                        ml[i] = p.ws.ml[slot * kLatentRowTile + r];
+                        o[i][0] = *reinterpret_cast<const float4*>(o0 + slot * stride);
+                        o[i][1] = *reinterpret_cast<const float4*>(o0 + slot * stride + 512);
+                    }
+                }
+                float top = big;
+#pragma unroll
+                for (int i = 0; i < kMergeBatch; ++i) top = fmaxf(top, ml[i].x);
+                const float a = top == -INFINITY ? 1.f : exp2f(big - top);
+                big = top;
+                sum *= a;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] *= a;
+#pragma unroll
+                for (int i = 0; i < kMergeBatch; ++i) {
+                    if (!(ml[i].y != 0.f)) continue;      // no visible keys: nothing was written
+                    const float w = exp2f(ml[i].x - big);
+                    sum += w * ml[i].y;
+                    acc[0] += w * o[i][0].x; acc[1] += w * o[i][0].y;
+                    acc[2] += w * o[i][0].z; acc[3] += w * o[i][0].w;
+                    acc[4] += w * o[i][1].x; acc[5] += w * o[i][1].y;
+                    acc[6] += w * o[i][1].z; acc[7] += w * o[i][1].w;
+                }
+            }
+            if (share > 1) {
+                float (*mem)[32] = shared[warp];
+                mem[8][lane] = sum;
+                mem[9][lane] = big;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mem[i][lane] = acc[i];
+                __syncthreads();
+                if (mine == 0) {
+                    float top = big;
+                    for (int w = 1; w < share; ++w) top = fmaxf(top, shared[warp + w][9][lane]);
+                    const float a = top == -INFINITY ? 1.f : exp2f(big - top);
+                    sum *= a;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] *= a;
+                    for (int w = 1; w < share; ++w) {
+                        const float b = shared[warp + w][9][lane], l = shared[warp + w][8][lane];
+                        if (!(l != 0.f)) continue;
+                        const float f = exp2f(b - top);
+                        sum += f * l;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[i] += f * shared[warp + w][i][lane];
+                    }
+                }
+                __syncthreads();
+            }
+            if (mine != 0 || !row) continue;
+            const float inv = 1.f / sum;
+            const int c = pair * 8;
+            const int d = c < half0 ? h * half0 + c : n0 + h * half1 + c - half0;
+            *reinterpret_cast<uint4*>(p.out + int64_t(m.row0 + r) * latent + d) =
+                make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                           pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        }
+        __syncthreads();
     }
-    const float inv = 1.f / sum;
-    const int n0 = min(256, p.b.latent), half0 = n0 / 2, half1 = (p.b.latent - n0) / 2;
-    const int c = blockIdx.y * 8;
-    const int d = c < half0 ? h * half0 + c : n0 + h * half1 + c - half0;
-    uint4 v;
-    v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-    v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4*>(p.out + int64_t(e.row0 + r) * p.b.latent + d) = v;
 }
 
 }  // namespace
@@ -513,15 +670,22 @@ int launch_latent_bf16(const LatentArgs& a) {
     p.b = a.batch;
     p.ws = a.ws;
     p.out = static_cast<__nv_bfloat16*>(a.out);
-    const int smem = 3 * kGroups * cols * 1024 + kPBytes + int(sizeof(Smem)) + 1024;
-    static_assert(3 * kGroups * 9 * 1024 + kPBytes + sizeof(Smem) + 1024 <= 232448, "shared memory");
+    p.b.team = latent_team(p.b, kRows);
+    // query rows of a unit: all 64, or those of the longest sequence if it has fewer (a
+    // call of one token a sequence; with offsets the rows of a sequence are not known here)
+    const int64_t rows = a.batch.query_start_loc ? kRows : std::min<int64_t>(kRows, a.batch.heads);
+    p.q_groups = int(rows + 7) / 8;
+    const int group = cols * 1024, rest = int(sizeof(Smem)) + 1024 + kPBytes + p.q_groups * group;
+    static_assert(kPBytes + (8 + 4 * kGroups) * 9 * 1024 + sizeof(Smem) + 1024 <= 232448, "shared memory");
+    p.slots = std::min(kMostSlots, (232448 - rest) / (kGroups * group));
+    const int smem = rest + p.slots * kGroups * group;
     // one limit for all latent_dims
     if (kernel_occupancy<latent_kernel>(kThreads, 232448) < 1) return PKV_ERR_CUDA;
     cudaError_t e = launch_pdl(latent_kernel, dim3(num_sms()), dim3(kThreads), size_t(smem), a.stream, kv,
                                q, p);
     if (e != cudaSuccess) return cuda_status(e);
-    return cuda_status(launch_pdl(latent_merge_kernel, dim3(num_sms(), d->latent_dim / 16), dim3(128), 0,
-                                  a.stream, p));
+    return cuda_status(launch_pdl(latent_merge_kernel, dim3(2 * num_sms()), dim3(kMergeThreads), 0, a.stream,
+                                  p, num_sms()));
 }
 
 }  // namespace pkv

@@ -6,14 +6,17 @@
 // a . c + b . k and sums the c themselves:  out = sum_j p_j c_j.  All heads read the
 // same keys, so a row of the products is a (token, head) pair of one sequence.
 //
-// Split.  A unit is (sequence, tile of ROWS rows); it costs one step for each tile of
-// KEYS keys of its context.  The steps of all units, one after the other, are cut into
-// as many equal stretches as there are CTAs, so every SM reads the same number of
-// keys whatever the lengths.  A stretch is a run of fragments; one that holds all
-// keys of its unit writes the output, another one its partial state (max, sum,
-// output) to a slot of its CTA: only a CTA's first and last fragment can be partial,
-// so there are two slots a CTA and the workspace does not grow with the batch.
-// A merge kernel joins the states of each cut unit in the order of its keys.
+// Split.  CTAs work in teams: the members of a team take neighbouring tiles of ROWS rows
+// of the same sequence over the same keys at the same time, so that what one of them
+// brings into L2 the others find there (one after the other, 128 heads over more keys than
+// L2 holds read HBM twice).  A unit is (sequence, row tiles of a team); it costs one step
+// for each tile of KEYS keys of its context.  The steps of all units, one after the other,
+// are cut into as many equal stretches as there are teams, so every SM reads the same
+// number of keys whatever the lengths.  A stretch is a run of fragments; one that holds
+// all keys of its unit writes the output, another one its partial state (max, sum, output)
+// to a slot of its CTA: only a CTA's first and last fragment can be partial, so there are
+// two slots a CTA and the workspace does not grow with the batch.  A merge kernel joins
+// the states of each cut unit in the order of its keys.
 #pragma once
 
 #include <cuda.h>
@@ -37,14 +40,15 @@ struct LatentBatch {
     int32_t max_context_len;
     int32_t heads;
     int32_t latent;                        // latent_dim
+    int32_t team;                          // CTAs of a team
     float scale_log2;
     int* err;
 };
 
-// One merge: the unit's rows and the CTAs whose slots hold its fragments.
+// One merge: the rows of a cut unit and the CTAs whose slots hold its fragments.
 struct LatentMerge {
     int32_t row0, nrows;                   // rows of q and out ([token][head] order)
-    int32_t first, last;                   // CTAs; nrows 0: nothing to merge
+    int32_t first, last;                   // CTAs, a team's size apart; nrows 0: nothing to merge
     int32_t first_slot;                    // the first fragment's slot (the others': 2 c)
 };
 
@@ -101,27 +105,37 @@ struct LatentFrag {
     bool whole;                            // holds all keys of its unit
     bool starts;                           // begins with the unit's first key, but is cut
     int slot;
-    int last_cta;                          // the CTA of the unit's last key (starts)
+    int last_cta;                          // the CTA of the rows' last key (starts)
 };
+
+// a * b / c for values whose product stays below 2^63
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+    const uint64_t x = uint64_t(a) * uint64_t(b);
+    return (x >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(c)) : int64_t(x / uint64_t(c));
+}
 
 template <int ROWS, int KEYS>
 struct LatentWalk {
     int s;
     int64_t off;                           // step within sequence s
-    int64_t left;                          // steps left of this CTA's stretch
+    int64_t left;                          // steps left of this team's stretch
     int64_t pos, total;                    // position among all steps
-    int ctas;
+    int teams;
     bool begun;
 
+    __device__ static int groups(const LatentBatch& b, int rows) {
+        return ((rows + ROWS - 1) / ROWS + b.team - 1) / b.team;
+    }
     __device__ static int64_t steps(const LatentBatch& b, const LatentSeq& x) {
         if (x.qlen == 0 || x.zero) return 0;
-        const int64_t rt = (int64_t(x.qlen) * b.heads + ROWS - 1) / ROWS;
-        return rt * ((x.ctx + KEYS - 1) / KEYS);
+        return int64_t(groups(b, x.qlen * b.heads)) * ((x.ctx + KEYS - 1) / KEYS);
     }
-    // the stretch of CTA c begins at step c * total / ctas; the CTA of a step
-    __device__ static int64_t start_of(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
-    __device__ static int owner(int64_t step, int64_t total, int ctas) {
-        return int(((step + 1) * ctas - 1) / total);
+    // the stretch of team t begins at step t * total / teams; the team of a step
+    __device__ static int64_t start_of(int64_t t, int64_t total, int teams) { return mul_div(t, total, teams); }
+    __device__ static int owner(int64_t step, int64_t total, int teams) {
+        // the last t with t * total / teams <= step
+        int t = int(mul_div(step + 1, teams, total));
+        return mul_div(t, total, teams) <= step && t < teams ? t : t - 1;
     }
 
     __device__ bool next(const LatentBatch& b, LatentFrag& f) {
@@ -130,30 +144,38 @@ struct LatentWalk {
         while (steps(b, x) == 0) x = latent_seq<false>(b, ++s);
         const int rows = x.qlen * b.heads;
         const int kt = (x.ctx + KEYS - 1) / KEYS;
-        const int rt = int(off / kt);
-        f.kt0 = int(off - int64_t(rt) * kt);
+        const int group = int(off / kt);
+        f.kt0 = int(off - int64_t(group) * kt);
         int n = kt - f.kt0;
         if (n > left) n = int(left);
-        const int r0 = rt * ROWS;
+        const int r0 = (group * b.team + int(blockIdx.x) % b.team) * ROWS;
         f.seq = s;
         f.ctx = x.ctx;
-        f.nrows = min(ROWS, rows - r0);
+        f.nrows = max(0, min(ROWS, rows - r0));
         f.row0 = x.q0 * b.heads + r0;
         f.t0 = r0 / b.heads;
         f.rest = r0 - f.t0 * b.heads;
         f.first_pos = x.ctx - x.qlen;
-        const int last_tok = (r0 + f.nrows - 1) / b.heads;
-        const int want = (f.first_pos + last_tok) / KEYS + 1;   // tiles that any row sees
-        f.n = max(0, min(f.kt0 + n, want) - f.kt0);
         f.whole = f.kt0 == 0 && n == kt;
         f.starts = f.kt0 == 0 && n < kt;
         f.slot = 2 * int(blockIdx.x) + (begun ? 1 : 0);
-        f.last_cta = f.starts ? owner(pos + kt - 1, total, ctas) : 0;
+        f.last_cta = 0;
+        f.n = 0;
+        if (f.nrows == 0) {                // this member has no rows of the unit
+            f.whole = true;
+            f.starts = false;
+        } else {
+            const int last_tok = (r0 + f.nrows - 1) / b.heads;
+            const int want = (f.first_pos + last_tok) / KEYS + 1;   // tiles that any row sees
+            f.n = max(0, min(f.kt0 + n, want) - f.kt0);
+            if (f.starts)
+                f.last_cta = owner(pos + kt - 1, total, teams) * b.team + int(blockIdx.x) % b.team;
+        }
         begun = true;
         left -= n;
         pos += n;
         off += n;
-        if (off == int64_t((rows + ROWS - 1) / ROWS) * kt) {
+        if (off == int64_t(groups(b, rows)) * kt) {
             off = 0;
             ++s;
         }
@@ -163,7 +185,7 @@ struct LatentWalk {
 
 // Every CTA sums the steps of all sequences for itself and finds the sequence that
 // its stretch begins in: threads 0 .. T-1 take runs of sequences, `sums` is shared
-// memory for T / 32 + 2 values.  Steps fewer than `least` a CTA go to fewer CTAs.
+// memory for T / 32 + 2 values.  Steps fewer than `least` a team go to fewer teams.
 // (All T threads call it; CTA 0 flags bad lengths.)
 template <int ROWS, int KEYS, int T>
 __device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch& b, int64_t* sums,
@@ -192,27 +214,36 @@ __device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch&
     }
     Walk x;
     x.total = total;
-    x.ctas = int(max(int64_t(1), min(int64_t(gridDim.x), total / least)));
+    const int team = int(blockIdx.x) / b.team;
+    x.teams = int(max(int64_t(1), min(int64_t(gridDim.x) / b.team, total / least)));
     x.begun = false;
-    const int64_t from = Walk::start_of(blockIdx.x, total, x.ctas);
-    x.left = int(blockIdx.x) < x.ctas ? Walk::start_of(blockIdx.x + 1, total, x.ctas) - from : 0;
+    const int64_t from = Walk::start_of(team, total, x.teams);
+    x.left = team < x.teams ? Walk::start_of(team + 1, total, x.teams) - from : 0;
     x.pos = from;
     if (x.left > 0 && from < upto && from >= upto - mine) {
         int64_t at = upto - mine;
-        for (int s = s0; s < s1; ++s) {
-            const int64_t n = Walk::steps(b, latent_seq<false>(b, s));
-            if (from < at + n) {
-                sums[kWarps] = s;
-                sums[kWarps + 1] = from - at;
-                break;
+        int s = s0;
+        if (per > 1) {                     // (a run of one is the sequence itself)
+            for (;; ++s) {
+                const int64_t n = Walk::steps(b, latent_seq<false>(b, s));
+                if (from < at + n) break;
+                at += n;
             }
-            at += n;
         }
+        sums[kWarps] = s;
+        sums[kWarps + 1] = from - at;
     }
     __syncthreads();
     x.s = int(sums[kWarps]);
     x.off = sums[kWarps + 1];
     return x;
+}
+
+// CTAs of a team: the row tiles of a sequence, on average; at most 8 (152 CTAs make whole
+// teams of most sizes up to there, and L2 holds what lies between two members)
+inline int latent_team(const LatentBatch& b, int rows) {
+    const int64_t of = int64_t(ceil_div(b.num_query_tokens, b.num_seqs)) * b.heads;
+    return int(of <= rows ? 1 : of >= 8 * int64_t(rows) ? 8 : (of + rows - 1) / rows);
 }
 
 // ---- tcgen05 and TMA ---------------------------------------------------------
@@ -225,6 +256,16 @@ __device__ __forceinline__ uint64_t tc_smem_desc(uint32_t saddr, uint32_t lbo, u
 __host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool b_mn_major) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+// One lane of a converged warp.  Products are issued inside a branch on this and not on a
+// lane's number: only then does the compiler know that one thread is active, and takes
+// their operands to uniform registers once instead of looping over the lanes (measured: a
+// product costs 45 cycles to issue in a branch on the lane's number, whatever its size;
+// 24 and less in this one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile(

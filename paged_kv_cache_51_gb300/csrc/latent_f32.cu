@@ -230,11 +230,11 @@ __global__ void __launch_bounds__(128) latent_f32_merge_kernel(Params p) {
     const int r = at / vecs, c = at - r * vecs;
     if (r >= e.nrows) return;
     float big = -INFINITY;
-    for (int i = e.first; i <= e.last; ++i)
+    for (int i = e.first; i <= e.last; i += p.b.team)
         big = fmaxf(big, p.ws.ml[(i == e.first ? e.first_slot : 2 * i) * kLatentRowTile + r].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int i = e.first; i <= e.last; ++i) {
+    for (int i = e.first; i <= e.last; i += p.b.team) {
         const int slot = i == e.first ? e.first_slot : 2 * i;
         const float2 ml = p.ws.ml[slot * kLatentRowTile + r];
         if (!(ml.y != 0.f)) continue;
@@ -273,6 +273,7 @@ int launch_latent_f32(const LatentArgs& a) {
     static_assert(smem_floats(512, 16) * 4 <= 232448, "shared memory");
     // rows of a sequence, on average
     const int64_t rows = int64_t(ceil_div(p.b.num_query_tokens, p.b.num_seqs)) * p.b.heads;
+    p.b.team = latent_team(p.b, rows <= 8 ? 8 : 16);
     const int groups = std::max(1, kThreads / (p.b.latent / 2));   // threads of one pair of dimensions
     if (rows <= 8)
         return groups == 1 ? launch<8, 8>(a, p) : groups == 2 ? launch<8, 4>(a, p) : launch<8, 2>(a, p);
