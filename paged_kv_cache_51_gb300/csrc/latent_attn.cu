@@ -77,7 +77,7 @@ struct Smem {                              // behind the operands
     uint64_t bars[B_COUNT];
     int64_t sums[kThreads / 32 + 2];
     float alpha[2][kRows];                 // [tile parity]
-    int need[2][kSoftWarps];
+    uint8_t need[2][kSoftWarps];
     float m[kRows], l[kRows];              // at the end of a fragment
     uint32_t tmem;
     int abort;
@@ -230,13 +230,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_load_3d(q_at + uint32_t(lane) * group, &map_q, 0, t.f.row0 + lane * 8, 0,
                                &bars[B_Q_FULL]);
             }
-            ok = __all_sync(0xffffffffu,
-                            t.g < slots || mbar_wait(&bars[B_O_DONE + at.slot], at.phase ^ 1, err));
-            if (!ok || *abort_flag) break;
             const bool good = lane < groups && blk >= 0 && blk < p.b.num_blocks;
             if (lane < groups && !good) flag_error(err, PKV_DEV_BAD_BLOCK_ID);
             const unsigned mask = __ballot_sync(0xffffffffu, good);
             uint64_t* full = &bars[B_K_FULL + at.slot];
+            const bool stop = *abort_flag;
+            ok = __all_sync(0xffffffffu, !stop && (t.g < slots || mbar_wait(&bars[B_O_DONE + at.slot],
+                                                                             at.phase ^ 1, err)));
+            if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(__popc(mask)) * group);
             ++k_loads;
             __syncwarp();
@@ -261,27 +262,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t idesc = tc_idesc(kRows, kKeys, false);
             const uint64_t qd = tc_smem_desc(q_at, 16, group);
             const uint64_t kd = tc_smem_desc(k_at, 16, group);
+            // The pipe idles for whatever this thread does between two tiles beyond the other
+            // issuer's products, so the next tile's barriers are tested before this one's
+            // last products go out and the answer is looked at behind them.
             Tiles t;
             Ring at;
-            bool ok = true;
+            bool ok = true, ready = false;
             for (t.start(p.b, plan); t.live; t.next(p.b)) {
                 const uint32_t sb = t.g & (kSBufs - 1);
                 const uint32_t d = tmem + kSCol + sb * 32;
                 const uint64_t k0 = kd + uint64_t(at.slot * (tile >> 4));
-                ok = (t.j != 0 || mbar_wait(&bars[B_Q_FULL], t.k & 1, err)) &&
-                     (t.g < kSBufs || mbar_wait(&bars[B_S_EMPTY + sb], ((t.g / kSBufs) & 1) ^ 1, err)) &&
-                     mbar_wait(&bars[B_K_FULL + at.slot], at.phase, err);
-                if (!ok || *abort_flag) break;
+                if (t.j == 0) ok = !*abort_flag && mbar_wait(&bars[B_Q_FULL], t.k & 1, err);
+                if (!ready)
+                    ok = ok &&
+                         (t.g < kSBufs || mbar_wait(&bars[B_S_EMPTY + sb], ((t.g / kSBufs) & 1) ^ 1, err)) &&
+                         mbar_wait(&bars[B_K_FULL + at.slot], at.phase, err);
+                if (!ok) break;
                 tc_fence_after();
-                for (int c = 0; c < cols; ++c) {
+                uint64_t qa = qd, ka = k0;
+                for (int c = 0; c < cols - 1; ++c, qa += 64, ka += 64) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_plain(d, qd + uint64_t(c * 64 + i * 2), k0 + uint64_t(c * 64 + i * 2), idesc,
-                                  (c | i) != 0);
+                    for (int i = 0; i < 4; ++i) mma_plain(d, qa + uint64_t(i * 2), ka + uint64_t(i * 2), idesc,
+                                                          (c | i) != 0);
                 }
+                at.next(slots);
+                const uint32_t nb = (t.g + 1) & (kSBufs - 1);
+                ready = mbar_test2(&bars[B_K_FULL + at.slot], at.phase, &bars[B_S_EMPTY + nb],
+                                   (((t.g + 1) / kSBufs) & 1) ^ 1) && t.g + 1 >= kSBufs;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_plain(d, qa + uint64_t(i * 2), ka + uint64_t(i * 2), idesc, 1);
                 tc_commit(&bars[B_S_FULL + sb]);
                 if (t.j == t.f.n - 1) tc_commit(&bars[B_Q_EMPTY]);
-                at.next(slots);
             }
             if (t.live) *abort_flag = 1;
             tc_commit(&bars[B_DRAIN]);
@@ -300,9 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (t.start(p.b, plan); t.live; t.next(p.b)) {
                 const uint64_t v0 = vd + uint64_t(at.slot * (tile >> 4));
                 const uint64_t p0 = pd + uint64_t((t.g & 1) * 4);
-                ok = (t.j != 0 || t.k == 0 || mbar_wait(&bars[B_O_EMPTY], (t.k - 1) & 1, err)) &&
-                     mbar_wait(&bars[B_P_FULL + (t.g & 1)], (t.g >> 1) & 1, err);
-                if (!ok || *abort_flag) break;
+                if (t.j == 0)
+                    ok = !*abort_flag && (t.k == 0 || mbar_wait(&bars[B_O_EMPTY], (t.k - 1) & 1, err));
+                ok = ok && mbar_wait(&bars[B_P_FULL + (t.g & 1)], (t.g >> 1) & 1, err);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i) {
@@ -355,8 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int j = 0; j < f.n; ++j, ++g) {
                 const uint32_t sb = g & (kSBufs - 1);
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_S_FULL + sb], (g / kSBufs) & 1, err));
-                if (!ok) break;
+                // (that the P buffer is free, the tile before the last, is nearly always so)
+                const bool free = g < 2 || mbar_test(&bars[B_O_DONE + prev2.slot], prev2.phase);
+                ok = mbar_wait(&bars[B_S_FULL + sb], (g / kSBufs) & 1, err);
+                __syncwarp();
                 tc_fence_after();
                 float s[16];
                 {
@@ -364,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_ld_16x32(tmem + lanes + kSCol + sb * 32, v);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(v[i]) * p.b.scale_log2;
+                    for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(v[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -384,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 1; i < 4; ++i) mx = fmaxf(mx, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float m_new = fmaxf(m[e], mx);
+                    const float m_new = fmaxf(m[e], mx * p.b.scale_log2);
                     alpha[e] = 1.f;
                     if (m_new > m[e] + kRescale) {         // first visible keys included
                         alpha[e] = exp2_fast(m[e] - m_new);
@@ -409,14 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int e = i & 1;
-                    pk[i] = pack_bf16x2(exp2_fast(s[2 * i] + neg_m[e]), exp2_fast(s[2 * i + 1] + neg_m[e]));
+                    pk[i] = pack_bf16x2(exp2_fast(fmaf(s[2 * i], p.b.scale_log2, neg_m[e])),
+                                        exp2_fast(fmaf(s[2 * i + 1], p.b.scale_log2, neg_m[e])));
                     l[e] += __uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xffff0000u);
                 }
-                // the P buffer was read by the tile before the last
-                if (g >= 2) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev2.slot], prev2.phase, err));
-                    if (!ok) break;
-                }
+                if (!free) ok = mbar_wait(&bars[B_O_DONE + prev2.slot], prev2.phase, err) && ok;
                 // (row & 7) is lane / 4 for both rows
                 unsigned char* row = p_ptr + ra * 128 + quad * 4;
 #pragma unroll
@@ -439,15 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fence_proxy_async_shared();
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_NEED], g & 1, err));
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_NEED], g & 1, err) && ok);
                 if (!ok) break;
-                const volatile int* any = sh.need[g & 1];
-                if (any[0] | any[1] | any[2] | any[3]) {
+                const uint32_t any = *reinterpret_cast<const volatile uint32_t*>(sh.need[g & 1]);
+                if (any) {
                     // the previous tile's P C adds to O
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev.slot], prev.phase, err));
                     if (!ok) break;
                     tc_fence_after();
-                    const float a = any[r >> 4] ? sh.alpha[g & 1][r] : 1.f;
+                    const float a = (any >> (8 * (r >> 4))) & 0xff ? sh.alpha[g & 1][r] : 1.f;
                     for (int c = 0; c < ocols; c += 32) {
                         uint32_t v[32];
                         const uint32_t to = tmem + lanes + (c < half0 ? c : 128 + c - half0);

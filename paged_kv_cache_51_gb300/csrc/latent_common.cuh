@@ -331,6 +331,18 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Tests of two barriers' phases side by side (a round trip of one costs about 90 cycles).
+__device__ __forceinline__ bool mbar_test2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+    uint32_t x, y;
+    asm volatile(
+        "{\n .reg .pred p, q;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%2], %3;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 q, [%4], %5;\n"
+        " selp.u32 %0, 1, 0, p;\n selp.u32 %1, 1, 0, q;\n}\n"
+        : "=r"(x), "=r"(y)
+        : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+        : "memory");
+    return x != 0 && y != 0;
+}
 // a -> low half, b -> high half
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
