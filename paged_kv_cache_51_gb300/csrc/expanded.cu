@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
 // ---- single precision -------------------------------------------------------------
 // A CTA takes 64 query rows of one head and tiles of 64 keys; a thread keeps a 4 x 4 part
 // of the scores and 4 rows x D / 16 values of the output in registers.  Bound by the FMA
-// rate with shared memory close behind (8 reads of 16 bytes for 64 FMAs).
+// rate with shared memory close behind (8 reads of 16 bytes for 64 FMAs).  Where units of
+// 64 rows would not give every SM two, they have 16 (a 1 x 4 part): the tiles of a unit
+// follow one another, and six prompts of up to 300 tokens with 4 heads took 52 us.
 struct F32Params {
     ExpandedWorkspace ws;
     const float *q, *k, *v, *k_rope;
@@ -95,12 +97,12 @@ struct F32Params {
     float scale_log2;
 };
 
-constexpr int kT = 64;                     // rows and keys of a tile
+constexpr int kT = 64;                     // keys of a tile
 constexpr int kPPitch = kT + 4;
 
-template <int D>
+template <int D, int RI>
 constexpr int f32_smem_floats() {
-    return 2 * kT * (D + kExpandedRope + 4) + kT * (D + 4) + kT * kPPitch;
+    return (16 * RI + kT) * (D + kExpandedRope + 4) + kT * (D + 4) + 16 * RI * kPPitch;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -109,13 +111,15 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
                  : "memory");
 }
 
-template <int D>
+// RI: rows of a thread; a unit has 16 of them.
+template <int D, int RI>
 __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
+    constexpr int kRows = 16 * RI;
     constexpr int kDim = D + kExpandedRope, kPitch = kDim + 4, kVPitch = D + 4;
     constexpr int kCols = D / 16;          // output values of a thread in a row
     extern __shared__ float4 smem4[];
     float* qs = reinterpret_cast<float*>(smem4);
-    float* ks = qs + kT * kPitch;
+    float* ks = qs + kRows * kPitch;
     float* vs = ks + kT * kPitch;
     float* ps = vs + kT * kVPitch;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -126,16 +130,16 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
     const ExpandedItem x = p.ws.items[item];
     const int keys = max(x.keys, 0);
 
-    for (int i = tid; i < kT * (kDim / 4); i += 256) {
+    for (int i = tid; i < kRows * (kDim / 4); i += 256) {
         const int r = i / (kDim / 4), c = i - r * (kDim / 4);
         cp_async16(smem_u32(qs + r * kPitch + 4 * c),
                    p.q + ((int64_t(x.q0) + min(r, x.rows - 1)) * p.heads + h) * kDim + 4 * c, r < x.rows);
     }
     // rows ty + 16 i, keys and values tx + 16 j (in fours)
-    float m[4], l[4], o[4][kCols];
-    int limit[4];
+    float m[RI], l[RI], o[RI][kCols];
+    int limit[RI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
         const int r = ty + 16 * i;
@@ -162,23 +166,24 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        float s[4][4] = {};
+        float s[RI][4] = {};
 #pragma unroll 2
         for (int c = 0; c < kDim / 4; ++c) {
-            float4 a[4], b[4];
+            float4 a[RI], b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RI; ++i)
                 a[i] = *reinterpret_cast<const float4*>(qs + (ty + 16 * i) * kPitch + 4 * c);
-                b[i] = *reinterpret_cast<const float4*>(ks + (tx + 16 * i) * kPitch + 4 * c);
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
+                b[i] = *reinterpret_cast<const float4*>(ks + (tx + 16 * i) * kPitch + 4 * c);
+#pragma unroll
+            for (int i = 0; i < RI; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RI; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -207,9 +212,9 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
         __syncwarp();                      // a row's 16 threads are one half of a warp
 #pragma unroll 2
         for (int k = 0; k < kT; k += 4) {
-            float4 e[4];
+            float4 e[RI];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < RI; ++i)
                 e[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * kPPitch + k);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
                 for (int c = 0; c < kCols; c += 4) {
                     const float4 v = *reinterpret_cast<const float4*>(vs + (k + kk) * kVPitch + 16 * c + 4 * tx);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < RI; ++i) {
                         const float w = kk == 0 ? e[i].x : kk == 1 ? e[i].y : kk == 2 ? e[i].z : e[i].w;
                         o[i][c] = fmaf(w, v.x, o[i][c]);
                         o[i][c + 1] = fmaf(w, v.y, o[i][c + 1]);
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
         const int r = ty + 16 * i;
         if (r >= x.rows) continue;
         const float inv = limit[i] >= 0 ? 1.f / l[i] : 0.f;      // a query without keys: zeros
@@ -242,14 +247,17 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
     }
 }
 
-template <int D>
+template <int D, int RI>
 int launch_f32(const ExpandedArgs& a, const F32Params& p) {
-    constexpr int smem = f32_smem_floats<D>() * int(sizeof(float));
+    constexpr int smem = f32_smem_floats<D, RI>() * int(sizeof(float));
     static_assert(smem <= 232448, "shared memory");
-    if (kernel_occupancy<expanded_f32_kernel<D>>(256, smem) < 1) return PKV_ERR_CUDA;
-    const int64_t grid = int64_t(a.ws.max_items) * a.desc->num_heads;
+    const int st = launch_expanded_plan(a, 16 * RI);
+    if (st != PKV_OK) return st;
+    if (kernel_occupancy<expanded_f32_kernel<D, RI>>(256, smem) < 1) return PKV_ERR_CUDA;
+    const int64_t items = std::min<int64_t>(a.ws.max_items, ceil_div(a.num_query_tokens, 16 * RI) + int64_t(a.num_seqs));
+    const int64_t grid = items * a.desc->num_heads;
     if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    return cuda_status(launch_pdl(expanded_f32_kernel<D>, dim3(unsigned(grid)), dim3(256), size_t(smem),
+    return cuda_status(launch_pdl(expanded_f32_kernel<D, RI>, dim3(unsigned(grid)), dim3(256), size_t(smem),
                                   a.stream, p));
 }
 
@@ -262,6 +270,7 @@ int check_expanded_desc(const pkv_expanded_desc* d) {
     return PKV_OK;
 }
 
+// rows of the smallest unit (sizes the workspace)
 int row_tile(const pkv_expanded_desc* d) {
     return d->dtype == PKV_BF16 ? kExpandedRowsBf16 : kExpandedRowsF32;
 }
@@ -298,7 +307,10 @@ int launch_expanded_f32(const ExpandedArgs& a) {
                 a.desc->v_head_stride,
                 a.desc->num_heads,
                 float(double(a.scale) * 1.4426950408889634)};
-    return a.desc->head_dim == 128 ? launch_f32<128>(a, p) : launch_f32<64>(a, p);
+    const int64_t units = int64_t(a.num_query_tokens) * a.desc->num_heads / 64;
+    if (units >= 2 * std::max(num_sms(), 1))
+        return a.desc->head_dim == 128 ? launch_f32<128, 4>(a, p) : launch_f32<64, 4>(a, p);
+    return a.desc->head_dim == 128 ? launch_f32<128, 1>(a, p) : launch_f32<64, 1>(a, p);
 }
 
 }  // namespace pkv
@@ -340,8 +352,6 @@ extern "C" int pkv_attention_expanded(void* out, const void* q, const void* k, c
     const size_t need = layout(desc, num_seqs, num_query_tokens, workspace, &a.ws);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PKV_ERR_WORKSPACE;
     a.err = device_error_ptr(&st);
-    if (st != PKV_OK) return st;
-    st = launch_expanded_plan(a, row_tile(desc));
     if (st != PKV_OK) return st;
     return desc->dtype == PKV_BF16 ? launch_expanded_bf16(a) : launch_expanded_f32(a);
 }

@@ -509,6 +509,8 @@ int launch(const ExpandedArgs& a) {
         !make_strided_tensor_map(&mr, none ? a.q : a.k_rope, kExpandedRope, 1, keys, kExpandedRope, kExpandedRope, kT) ||
         !make_strided_tensor_map(&mv, none ? a.q : a.v, D, H, keys, vh, vt, kT / 2))
         return PKV_ERR_CUDA;
+    const int st = launch_expanded_plan(a, kExpandedRowsBf16);
+    if (st != PKV_OK) return st;
     Params p{a.ws, static_cast<__nv_bfloat16*>(a.out), H, float(double(a.scale) * 1.4426950408889634), a.err};
     if (kernel_occupancy<expanded_kernel<D>>(kThreads, Shape<D>::kSmem) < 1) return PKV_ERR_CUDA;
     const int64_t units = int64_t(a.ws.max_items) * H;

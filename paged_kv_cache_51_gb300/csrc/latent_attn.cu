@@ -36,6 +36,7 @@
 #include <cmath>
 
 #include "latent_common.cuh"
+#include "latent_merge.cuh"
 #include "launch_cache.h"
 
 namespace pkv {
@@ -547,127 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
 }
 
-// States of a cut unit, joined in the order of its keys:
-//   M = max m_i,  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// One wave of CTAs, resident before the attention ends.  Every CTA lists the cut units for
-// itself; a warp takes 32 lanes and 8 columns of a unit at a time and asks for the states
-// of eight CTAs at once, so that what it waits for is one trip to L2 (reading state by
-// state took 13 us for 64 requests of 512 to 4096 tokens, this 6).  Where there are fewer
-// such items than warps, 2, 4 or 8 warps of a CTA share one, each with a share of the
-// states, and meet in shared memory.
-constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBatch = 8;
-
-__global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(Params p, int ctas) {
-    __shared__ LatentMerge list[kMergeThreads];
-    __shared__ int counts[kMergeWarps], tall;
-    __shared__ float shared[kMergeWarps][10][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int latent = p.b.latent, pairs = latent / 16, team = p.b.team;
-    const int64_t stride = int64_t(kLatentRowTile) * latent;
-    const int n0 = min(256, latent), half0 = n0 / 2, half1 = (latent - n0) / 2;
-    pdl_wait_prerequisites();
-    for (int base = 0; base < ctas; base += kMergeThreads) {
-        LatentMerge e{};
-        if (base + int(threadIdx.x) < ctas) e = p.ws.merge[base + threadIdx.x];
-        const unsigned mask = __ballot_sync(0xffffffffu, e.nrows > 0);
-        if (lane == 0) counts[warp] = __popc(mask);
-        if (threadIdx.x == 0) tall = 0;
-        __syncthreads();
-        int at = __popc(mask & ((1u << lane) - 1)), units = 0;
-#pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) {
-            if (w < warp) at += counts[w];
-            units += counts[w];
-        }
-        if (e.nrows > 0) list[at] = e;
-        if (e.nrows > 32) tall = 1;
-        __syncthreads();
-        const int quarters = tall ? 4 : 2;                // of a unit's 128 lanes
-        const int items = units * pairs * quarters, all = int(gridDim.x) * kMergeWarps;
-        const int share = items * 8 <= all ? 8 : items * 4 <= all ? 4 : items * 2 <= all ? 2 : 1;
-        const int per_cta = kMergeWarps / share, mine = warp % share;
-        for (int i0 = blockIdx.x * per_cta; i0 < items; i0 += gridDim.x * per_cta) {
-            const int item = i0 + warp / share;
-            const bool live = item < items;
-            const int u = live ? item / (pairs * quarters) : 0, rest = live ? item - u * pairs * quarters : 0;
-            const int pair = rest / quarters, q = rest - pair * quarters;
-            const LatentMerge m = list[u];
-            // quarters of rows 0-31 first: lanes 0, 64, 32, 96 ..
-            const int h = q & 1, r = (q >> 1) * 32 + lane;
-            const bool row = live && r < m.nrows;
-            const float* o0 = p.ws.o + (pair * 256 + h * 64 + r) * 4;
-            float acc[8] = {}, sum = 0.f, big = -INFINITY;
-            const int n = (m.last - m.first) / team + 1;
-            for (int c0 = mine; row && c0 < n; c0 += kMergeBatch * share) {
-                float2 ml[kMergeBatch];
-                float4 o[kMergeBatch][2];
-#pragma unroll
-                for (int i = 0; i < kMergeBatch; ++i) {
-                    const int c = c0 + i * share, slot = c == 0 ? m.first_slot : 2 * (m.first + c * team);
-                    ml[i] = make_float2(-INFINITY, 0.f);
-                    if (c < n) {
-                        ml[i] = p.ws.ml[slot * kLatentRowTile + r];
-                        o[i][0] = *reinterpret_cast<const float4*>(o0 + slot * stride);
-                        o[i][1] = *reinterpret_cast<const float4*>(o0 + slot * stride + 512);
-                    }
-                }
-                float top = big;
-#pragma unroll
-                for (int i = 0; i < kMergeBatch; ++i) top = fmaxf(top, ml[i].x);
-                const float a = top == -INFINITY ? 1.f : exp2f(big - top);
-                big = top;
-                sum *= a;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] *= a;
-#pragma unroll
-                for (int i = 0; i < kMergeBatch; ++i) {
-                    if (!(ml[i].y != 0.f)) continue;      // no visible keys: nothing was written
-                    const float w = exp2f(ml[i].x - big);
-                    sum += w * ml[i].y;
-                    acc[0] += w * o[i][0].x; acc[1] += w * o[i][0].y;
-                    acc[2] += w * o[i][0].z; acc[3] += w * o[i][0].w;
-                    acc[4] += w * o[i][1].x; acc[5] += w * o[i][1].y;
-                    acc[6] += w * o[i][1].z; acc[7] += w * o[i][1].w;
-                }
-            }
-            if (share > 1) {
-                float (*mem)[32] = shared[warp];
-                mem[8][lane] = sum;
-                mem[9][lane] = big;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mem[i][lane] = acc[i];
-                __syncthreads();
-                if (mine == 0) {
-                    float top = big;
-                    for (int w = 1; w < share; ++w) top = fmaxf(top, shared[warp + w][9][lane]);
-                    const float a = top == -INFINITY ? 1.f : exp2f(big - top);
-                    sum *= a;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] *= a;
-                    for (int w = 1; w < share; ++w) {
-                        const float b = shared[warp + w][9][lane], l = shared[warp + w][8][lane];
-                        if (!(l != 0.f)) continue;
-                        const float f = exp2f(b - top);
-                        sum += f * l;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[i] += f * shared[warp + w][i][lane];
-                    }
-                }
-                __syncthreads();
-            }
-            if (mine != 0 || !row) continue;
-            const float inv = 1.f / sum;
-            const int c = pair * 8;
-            const int d = c < half0 ? h * half0 + c : n0 + h * half1 + c - half0;
-            *reinterpret_cast<uint4*>(p.out + int64_t(m.row0 + r) * latent + d) =
-                make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                           pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-        }
-        __syncthreads();
-    }
-}
-
 }  // namespace
 
 int launch_latent_bf16(const LatentArgs& a) {
@@ -695,8 +575,7 @@ int launch_latent_bf16(const LatentArgs& a) {
     cudaError_t e = launch_pdl(latent_kernel, dim3(num_sms()), dim3(kThreads), size_t(smem), a.stream, kv,
                                q, p);
     if (e != cudaSuccess) return cuda_status(e);
-    return cuda_status(launch_pdl(latent_merge_kernel, dim3(2 * num_sms()), dim3(kMergeThreads), 0, a.stream,
-                                  p, num_sms()));
+    return launch_latent_merge<__nv_bfloat16>(a.stream, p.b, p.ws, p.out);
 }
 
 }  // namespace pkv

@@ -248,15 +248,16 @@ struct GatherParams {
     int32_t num_seqs;
     int32_t num_keys;
     int32_t num_blocks;
-    int32_t vecs;             // 16-byte vectors of a cached row, and of its first part
-    int32_t latent_vecs;
     int* err;
 };
 
 constexpr int kGatherRows = 8;             // rows a warp
 
 // A warp moves 8 rows in a row: lanes 0-7 look their rows up (a search over the offsets,
-// then the table), and all lanes copy the rows' vectors one after the other.
+// then the table), and all lanes copy the rows' vectors one after the other.  VECS: 16-byte
+// vectors of a cached row, RVECS of its rotary part (with sizes known at run time only, two
+// divisions a vector made the kernel instruction-bound: 65 us for 131072 rows of 1152 bytes).
+template <int VECS, int RVECS>
 __global__ void __launch_bounds__(256) latent_gather_kernel(GatherParams p) {
     pdl_wait_prerequisites();
     pdl_launch_dependents();
@@ -292,26 +293,28 @@ __global__ void __launch_bounds__(256) latent_gather_kernel(GatherParams p) {
         }
     }
     __syncwarp();
-    constexpr int kUnroll = 6;             // vecs / 4 vectors a lane: 6 to 36, in sixes or less
-    const int total = p.vecs * kGatherRows;
-    for (int v0 = lane; v0 < total; v0 += 32 * kUnroll) {
+    constexpr int kLatent = VECS - RVECS, kTotal = VECS * kGatherRows;
+    constexpr int kUnroll = kTotal / 32 % 9 == 0 ? 9 : kTotal / 32 % 6 == 0 ? 6 : kTotal / 32 % 7 == 0 ? 7 : 5;
+    static_assert(kTotal % (32 * kUnroll) == 0, "whole passes");
+    uint4* latent = p.latent + t0 * kLatent;
+    uint4* rope = p.rope + t0 * RVECS;
+#pragma unroll
+    for (int pass = 0; pass < kTotal / 32 / kUnroll; ++pass) {
         uint4 x[kUnroll];
-        int64_t from[kUnroll];
+        bool there[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int v = v0 + 32 * u;
-            const int r = v / p.vecs;      // (past the last row: not read)
-            const int64_t src = __shfl_sync(0xffffffffu, row, r & 7);
-            from[u] = v < total ? src : -1;
-            if (from[u] >= 0) x[u] = __ldg(p.cache + from[u] * p.vecs + (v - r * p.vecs));
+            const uint32_t v = lane + 32 * (pass * kUnroll + u), r = v / VECS;
+            const int64_t src = __shfl_sync(0xffffffffu, row, int(r));
+            there[u] = src >= 0;
+            if (there[u]) x[u] = __ldg(p.cache + src * VECS + (v - r * VECS));
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (from[u] < 0) continue;
-            const int v = v0 + 32 * u;
-            const int r = v / p.vecs, c = v - r * p.vecs;
-            if (c < p.latent_vecs) p.latent[(t0 + r) * p.latent_vecs + c] = x[u];
-            else p.rope[(t0 + r) * (p.vecs - p.latent_vecs) + c - p.latent_vecs] = x[u];
+            const uint32_t v = lane + 32 * (pass * kUnroll + u), r = v / VECS, c = v - r * VECS;
+            if (!there[u]) continue;
+            if (c < kLatent) latent[r * kLatent + c] = x[u];
+            else rope[r * RVECS + c - kLatent] = x[u];
         }
     }
 }
@@ -436,11 +439,21 @@ extern "C" int paged_latent_gather(void* latent_out, void* rope_out, const void*
     p.num_seqs = num_seqs;
     p.num_keys = num_keys;
     p.num_blocks = desc->num_blocks;
-    p.vecs = (desc->latent_dim + desc->rope_dim) / per;
-    p.latent_vecs = desc->latent_dim / per;
+    const auto kern = [&]() -> void (*)(GatherParams) {
+        switch ((desc->latent_dim + desc->rope_dim) / per) {
+            case 24: return latent_gather_kernel<24, 8>;
+            case 40: return latent_gather_kernel<40, 8>;
+            case 56: return latent_gather_kernel<56, 8>;
+            case 72: return latent_gather_kernel<72, 8>;
+            case 48: return latent_gather_kernel<48, 16>;
+            case 80: return latent_gather_kernel<80, 16>;
+            case 112: return latent_gather_kernel<112, 16>;
+            default: return latent_gather_kernel<144, 16>;
+        }
+    }();
     const int rows = kGatherRows * 8;
-    return cuda_status(launch_pdl(latent_gather_kernel, dim3(unsigned((int64_t(num_keys) + rows - 1) / rows)),
-                                  dim3(256), 0, static_cast<cudaStream_t>(stream), p));
+    return cuda_status(launch_pdl(kern, dim3(unsigned((int64_t(num_keys) + rows - 1) / rows)), dim3(256), 0,
+                                  static_cast<cudaStream_t>(stream), p));
 }
 
 extern "C" size_t pkv_latent_workspace_bytes(const pkv_latent_desc* desc, int32_t num_seqs,

@@ -19,6 +19,7 @@
 #include <cmath>
 
 #include "latent_common.cuh"
+#include "latent_merge.cuh"
 #include "launch_cache.h"
 
 namespace pkv {
@@ -221,34 +222,6 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
     }
 }
 
-// The states of a cut unit joined (see latent_attn.cu); here they lie row by row.
-// CTA (i, y): merge i, 128 vectors of 4 values.
-__global__ void __launch_bounds__(128) latent_f32_merge_kernel(Params p) {
-    pdl_wait_prerequisites();
-    const LatentMerge e = p.ws.merge[blockIdx.x];
-    const int at = blockIdx.y * 128 + threadIdx.x, vecs = p.b.latent / 4;
-    const int r = at / vecs, c = at - r * vecs;
-    if (r >= e.nrows) return;
-    float big = -INFINITY;
-    for (int i = e.first; i <= e.last; i += p.b.team)
-        big = fmaxf(big, p.ws.ml[(i == e.first ? e.first_slot : 2 * i) * kLatentRowTile + r].x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int i = e.first; i <= e.last; i += p.b.team) {
-        const int slot = i == e.first ? e.first_slot : 2 * i;
-        const float2 ml = p.ws.ml[slot * kLatentRowTile + r];
-        if (!(ml.y != 0.f)) continue;
-        const float w = exp2f(ml.x - big);
-        sum += w * ml.y;
-        const float4 o = *reinterpret_cast<const float4*>(
-            p.ws.o + (int64_t(slot) * kLatentRowTile + r) * p.b.latent + 4 * c);
-        acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w;
-    }
-    const float inv = 1.f / sum;
-    *reinterpret_cast<float4*>(p.out + (int64_t(e.row0) + r) * p.b.latent + 4 * c) =
-        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-}
-
 template <int ROWS, int RPT>
 int launch(const LatentArgs& a, const Params& p) {
     const int smem = smem_floats(a.desc->latent_dim, ROWS) * int(sizeof(float));
@@ -257,8 +230,7 @@ int launch(const LatentArgs& a, const Params& p) {
     cudaError_t e = launch_pdl(latent_f32_kernel<ROWS, RPT>, dim3(num_sms()), dim3(kThreads), size_t(smem),
                                a.stream, p);
     if (e != cudaSuccess) return cuda_status(e);
-    return cuda_status(launch_pdl(latent_f32_merge_kernel, dim3(num_sms(), ROWS * a.desc->latent_dim / 512),
-                                  dim3(128), 0, a.stream, p));
+    return launch_latent_merge<float>(a.stream, p.b, p.ws, p.out);
 }
 
 }  // namespace
