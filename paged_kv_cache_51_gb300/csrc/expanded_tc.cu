@@ -52,8 +52,8 @@ enum {
     B_Q_FULL = B_V_EMPTY + 2,              // [stream]
     B_Q_EMPTY = B_Q_FULL + 2,              // the unit's last S of the stream is complete
     B_S_FULL = B_Q_EMPTY + 2,
-    B_P_FULL = B_S_FULL + 2,
-    B_O_FULL = B_P_FULL + 2,               // the unit's last P V of the stream is complete
+    B_P_FULL = B_S_FULL + 2,               // [stream][half of the keys]
+    B_O_FULL = B_P_FULL + 4,               // the unit's last P V of the stream is complete
     B_O_EMPTY = B_O_FULL + 2,
     B_U_FULL = B_O_EMPTY + 2,              // [unit parity]
     B_U_EMPTY = B_U_FULL + 2,
@@ -91,6 +91,7 @@ struct Params {
     ExpandedWorkspace ws;
     __nv_bfloat16* out;
     int32_t heads;
+    bool whole_sectors;                    // out begins on 32 bytes
     float scale_log2;
     int* err;
 };
@@ -311,12 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = mbar_wait(&bars[B_V_FULL + (t & 1)], (t >> 1) & 1, err);
                     for (int x = 0; x < 2 && ok; ++x) {
                         if (j >= tiles[x]) continue;
-                        ok = mbar_wait(&bars[B_P_FULL + x], steps[x] & 1, err) &&
+                        ok = mbar_wait(&bars[B_P_FULL + 2 * x], steps[x] & 1, err) &&
                              (j != 0 || used[x] == 0 || mbar_wait(&bars[B_O_EMPTY + x], (used[x] - 1) & 1, err));
                         if (!ok) break;
                         tc_fence_after();
                         mma_ts4(tmem + kOCol + x * kT, tmem + x * kT, vd + uint64_t(v_at * (kBox >> 4)), idesc_o,
                                 j != 0);
+                        ok = mbar_wait(&bars[B_P_FULL + 2 * x + 1], steps[x] & 1, err);
+                        if (!ok) break;
+                        tc_fence_after();
                         mma_ts4(tmem + kOCol + x * kT, tmem + x * kT + 32,
                                 vd + (D == 128 ? uint64_t(wrap(v_at + 1) * (kBox >> 4))
                                                : uint64_t(v_at * (kBox >> 4) + (kBox >> 5))),
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || !u.live) break;
             const int mine = tiles_of(u, x), most = max(mine, tiles_of(u, x ^ 1));
             const int row = x * kT + r;                    // of the unit
-            const int limit = row < u.rows ? u.keys - u.rows + row : -1;   // last key that it sees
+            const int limit = min(row, u.rows - 1) + u.keys - u.rows;   // last key that it sees
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < mine; ++j, ++steps) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_S_FULL + x], steps & 1, err));
@@ -406,25 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_st32(o_at + c, v);
                     }
                 }
-                // P = 2^(s scale - m) in bf16 (2^-8 of a weight at most), over S's own columns;
-                // the sum is of the weights before that rounding
-                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), ref2 = make_float2(ref, ref);
-                float2 sum[4] = {};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int at = 64 * c + 2 * i;
-                        const float2 e = __ffma2_rn(make_float2(s[at], s[at + 1]), sc2, ref2);
-                        const float p0 = exp2_fast(e.x), p1 = exp2_fast(e.y);
-                        sum[i & 3] = __fadd2_rn(sum[i & 3], make_float2(p0, p1));
-                        w[i] = pack_bf16x2(p0, p1);
-                    }
-                    tc_st32(s_at + 32 * c, w);
-                }
-                l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
-                     ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
                 // values behind the unit's keys are another sequence's or nothing's: zeroed,
                 // since 0 times anything must stay 0 (by both streams, each before its P V)
                 const int keys = u.keys - key0;
@@ -443,10 +428,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_shared();
                 }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_P_FULL + x]);
+                // P = 2^(s scale - m) in bf16 (2^-8 of a weight at most), over S's own columns;
+                // the sum is of the weights before that rounding
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2); 
+                // (keeps the arithmetic of the second half behind the store of the first)
+                float refc = ref;
+                float2 sum[4] = {};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    asm volatile("" : "+f"(refc));
+                    const float2 ref2 = make_float2(refc, refc);
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int at = 64 * c + 2 * i;
+                        const float2 e = __ffma2_rn(make_float2(s[at], s[at + 1]), sc2, ref2);
+                        const float p0 = exp2_fast(e.x), p1 = exp2_fast(e.y);
+                        sum[i & 3] = __fadd2_rn(sum[i & 3], make_float2(p0, p1));
+                        w[i] = pack_bf16x2(p0, p1);
+                    }
+                    tc_st32(s_at + 32 * c, w);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[B_P_FULL + 2 * x + c]);
+                }
+                l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
+                     ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
             }
             if (!ok) break;
             __nv_bfloat16* dst = p.out + ((int64_t(u.q0) + row) * p.heads + u.head) * D;
@@ -462,16 +470,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_wait_ld();
                     if (row < u.rows) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t o[4];
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t o[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
+                            for (int e = 0; e < 8; ++e)
                                 o[e] = limit < 0 ? 0u
-                                                 : pack_bf16x2(__uint_as_float(v[8 * i + 2 * e]) * inv,
-                                                               __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4*>(dst + c + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                                                 : pack_bf16x2(__uint_as_float(v[16 * i + 2 * e]) * inv,
+                                                               __uint_as_float(v[16 * i + 2 * e + 1]) * inv);
+                            store_sector(dst + c + 16 * i, o, p.whole_sectors);
                         }
                     }
+                    __syncwarp();
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -511,7 +520,8 @@ int launch(const ExpandedArgs& a) {
         return PKV_ERR_CUDA;
     const int st = launch_expanded_plan(a, kExpandedRowsBf16);
     if (st != PKV_OK) return st;
-    Params p{a.ws, static_cast<__nv_bfloat16*>(a.out), H, float(double(a.scale) * 1.4426950408889634), a.err};
+    Params p{a.ws, static_cast<__nv_bfloat16*>(a.out), H, (reinterpret_cast<uintptr_t>(a.out) & 31) == 0,
+             float(double(a.scale) * 1.4426950408889634), a.err};
     if (kernel_occupancy<expanded_kernel<D>>(kThreads, Shape<D>::kSmem) < 1) return PKV_ERR_CUDA;
     const int64_t units = int64_t(a.ws.max_items) * H;
     if (units > INT32_MAX - 1024) return PKV_ERR_UNSUPPORTED;

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int groups = (min(kKeys, t.f.ctx - key0) + 7) / 8;
             const int blk = lane < groups ? __ldg(table + key0 / kBlockTokens + (lane >> 1)) : 0;
             if (t.j == 0) {
-                ok = __all_sync(0xffffffffu, t.k == 0 || mbar_wait(&bars[B_Q_EMPTY], (t.k - 1) & 1, err));
+                ok = __all_sync(0xffffffffu, t.k == 0 || mbar_wait_asleep(&bars[B_Q_EMPTY], (t.k - 1) & 1, err));
                 if (!ok || *abort_flag) break;
                 const int rows = (t.f.nrows + 7) / 8;
                 if (lane == 0) mbar_arrive_expect_tx(&bars[B_Q_FULL], uint32_t(rows) * group);
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned mask = __ballot_sync(0xffffffffu, good);
             uint64_t* full = &bars[B_K_FULL + at.slot];
             const bool stop = *abort_flag;
-            ok = __all_sync(0xffffffffu, !stop && (t.g < slots || mbar_wait(&bars[B_O_DONE + at.slot],
+            ok = __all_sync(0xffffffffu, !stop && (t.g < slots || mbar_wait_asleep(&bars[B_O_DONE + at.slot],
                                                                              at.phase ^ 1, err)));
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(__popc(mask)) * group);
@@ -251,10 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t.live) *abort_flag = 1;
         // never leave with copies in flight
         if (lane == 0) {
-            if (q_loads > 0) mbar_wait(&bars[B_Q_FULL], (q_loads - 1) & 1, err);
+            if (q_loads > 0) mbar_wait_asleep(&bars[B_Q_FULL], (q_loads - 1) & 1, err);
             for (uint32_t i = 0; i < slots && i < k_loads; ++i) {
                 const uint32_t last = k_loads - 1 - i;
-                mbar_wait(&bars[B_K_FULL + last % slots], (last / slots) & 1, err);
+                mbar_wait_asleep(&bars[B_K_FULL + last % slots], (last / slots) & 1, err);
             }
         }
         __syncwarp();
@@ -273,11 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t sb = t.g & (kSBufs - 1);
                 const uint32_t d = tmem + kSCol + sb * 32;
                 const uint64_t k0 = kd + uint64_t(at.slot * (tile >> 4));
-                if (t.j == 0) ok = !*abort_flag && mbar_wait(&bars[B_Q_FULL], t.k & 1, err);
+                if (t.j == 0) ok = !*abort_flag && mbar_wait_asleep(&bars[B_Q_FULL], t.k & 1, err);
                 if (!ready)
                     ok = ok &&
-                         (t.g < kSBufs || mbar_wait(&bars[B_S_EMPTY + sb], ((t.g / kSBufs) & 1) ^ 1, err)) &&
-                         mbar_wait(&bars[B_K_FULL + at.slot], at.phase, err);
+                         (t.g < kSBufs || mbar_wait_asleep(&bars[B_S_EMPTY + sb], ((t.g / kSBufs) & 1) ^ 1, err)) &&
+                         mbar_wait_asleep(&bars[B_K_FULL + at.slot], at.phase, err);
                 if (!ok) break;
                 tc_fence_after();
                 uint64_t qa = qd, ka = k0;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (t.live) *abort_flag = 1;
             tc_commit(&bars[B_DRAIN]);
-            mbar_wait(&bars[B_DRAIN], 0, err);
+            mbar_wait_asleep(&bars[B_DRAIN], 0, err);
         }
         __syncwarp();
     } else if (warp == kPcWarp) {
@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t v0 = vd + uint64_t(at.slot * (tile >> 4));
                 const uint64_t p0 = pd + uint64_t((t.g & 1) * 4);
                 if (t.j == 0)
-                    ok = !*abort_flag && (t.k == 0 || mbar_wait(&bars[B_O_EMPTY], (t.k - 1) & 1, err));
-                ok = ok && mbar_wait(&bars[B_P_FULL + (t.g & 1)], (t.g >> 1) & 1, err);
+                    ok = !*abort_flag && (t.k == 0 || mbar_wait_asleep(&bars[B_O_EMPTY], (t.k - 1) & 1, err));
+                ok = ok && mbar_wait_asleep(&bars[B_P_FULL + (t.g & 1)], (t.g >> 1) & 1, err);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (t.live) *abort_flag = 1;
             tc_commit(&bars[B_DRAIN + 1]);
-            mbar_wait(&bars[B_DRAIN + 1], 0, err);
+            mbar_wait_asleep(&bars[B_DRAIN + 1], 0, err);
         }
         __syncwarp();
     } else if (warp < kSoftWarp0) {
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t sb = g & (kSBufs - 1);
                 // (that the P buffer is free, the tile before the last, is nearly always so)
                 const bool free = g < 2 || mbar_test(&bars[B_O_DONE + prev2.slot], prev2.phase);
-                ok = mbar_wait(&bars[B_S_FULL + sb], (g / kSBufs) & 1, err);
+                ok = mbar_wait_asleep(&bars[B_S_FULL + sb], (g / kSBufs) & 1, err);
                 __syncwarp();
                 tc_fence_after();
                 float s[16];
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         exp2_fast(fmaf(s[2 * i + 1], p.b.scale_log2, neg_m[e])));
                     l[e] += __uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xffff0000u);
                 }
-                if (!free) ok = mbar_wait(&bars[B_O_DONE + prev2.slot], prev2.phase, err) && ok;
+                if (!free) ok = mbar_wait_asleep(&bars[B_O_DONE + prev2.slot], prev2.phase, err) && ok;
                 // (row & 7) is lane / 4 for both rows
                 unsigned char* row = p_ptr + ra * 128 + quad * 4;
 #pragma unroll
@@ -451,12 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fence_proxy_async_shared();
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_NEED], g & 1, err) && ok);
+                ok = __all_sync(0xffffffffu, mbar_wait_asleep(&bars[B_NEED], g & 1, err) && ok);
                 if (!ok) break;
                 const uint32_t any = *reinterpret_cast<const volatile uint32_t*>(sh.need[g & 1]);
                 if (any) {
                     // the previous tile's P C adds to O
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev.slot], prev.phase, err));
+                    ok = __all_sync(0xffffffffu, mbar_wait_asleep(&bars[B_O_DONE + prev.slot], prev.phase, err));
                     if (!ok) break;
                     tc_fence_after();
                     const float a = (any >> (8 * (r >> 4))) & 0xff ? sh.alpha[g & 1][r] : 1.f;
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_SUM]);
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_DONE + prev.slot], prev.phase, err) &&
-                                                 mbar_wait(&bars[B_SUM], k & 1, err));
+                ok = __all_sync(0xffffffffu, mbar_wait_asleep(&bars[B_O_DONE + prev.slot], prev.phase, err) &&
+                                                 mbar_wait_asleep(&bars[B_SUM], k & 1, err));
                 if (!ok) break;
                 tc_fence_after();
                 mr = sh.m[r];

@@ -331,6 +331,29 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// As mbar_wait, but asleep while it waits: the attempt is given a time that the hardware may
+// suspend the thread for.  Without it an attempt comes back soon, and the warps that wait
+// take issue slots and shared-memory cycles from the ones that work.
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity, int* err) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            flag_error(err, PKV_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // Tests of two barriers' phases side by side (a round trip of one costs about 90 cycles).
 __device__ __forceinline__ bool mbar_test2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
     uint32_t x, y;
@@ -347,6 +370,18 @@ __device__ __forceinline__ bool mbar_test2(uint64_t* a, uint32_t pa, uint64_t* b
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+// 32 bytes of a row by one thread; a row a thread, so that the halves of a sector written
+// one after the other would be two transactions
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t (&v)[8], bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                     "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 // 2^x in one instruction (a few ulps, subnormal results flushed to zero): softmax
 // weights and rescale factors only
