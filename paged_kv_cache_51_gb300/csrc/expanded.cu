@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
 // A CTA takes 64 query rows of one head and tiles of 64 keys; a thread keeps a 4 x 4 part
 // of the scores and 4 rows x D / 16 values of the output in registers.  Bound by the FMA
 // rate with shared memory close behind (8 reads of 16 bytes for 64 FMAs).  Where units of
-// 64 rows would not give every SM two, they have 16 (a 1 x 4 part): the tiles of a unit
+// 64 rows would not give every SM two, they have 32 (a 2 x 4 part), and two groups of 256
+// threads take every second tile of the keys and meet at the end: the tiles of a unit
 // follow one another, and six prompts of up to 300 tokens with 4 heads took 52 us.
 struct F32Params {
     ExpandedWorkspace ws;
@@ -100,9 +101,10 @@ struct F32Params {
 constexpr int kT = 64;                     // keys of a tile
 constexpr int kPPitch = kT + 4;
 
-template <int D, int RI>
+template <int D, int RI, int GROUPS>
 constexpr int f32_smem_floats() {
-    return (16 * RI + kT) * (D + kExpandedRope + 4) + kT * (D + 4) + 16 * RI * kPPitch;
+    return 16 * RI * (D + kExpandedRope + 4) +
+           GROUPS * (kT * (D + kExpandedRope + 4) + kT * (D + 4) + 16 * RI * kPPitch);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -112,17 +114,19 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 }
 
 // RI: rows of a thread; a unit has 16 of them.
-template <int D, int RI>
-__global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
+template <int D, int RI, int GROUPS>
+__global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p) {
     constexpr int kRows = 16 * RI;
     constexpr int kDim = D + kExpandedRope, kPitch = kDim + 4, kVPitch = D + 4;
     constexpr int kCols = D / 16;          // output values of a thread in a row
     extern __shared__ float4 smem4[];
+    constexpr int kGroup = kT * kPitch + kT * kVPitch + kRows * kPPitch;
+    const int group = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
     float* qs = reinterpret_cast<float*>(smem4);
-    float* ks = qs + kRows * kPitch;
+    float* ks = qs + kRows * kPitch + group * kGroup;
     float* vs = ks + kT * kPitch;
     float* ps = vs + kT * kVPitch;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    auto sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); };
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int item = blockIdx.x / p.heads, h = blockIdx.x - item * p.heads;
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
     const ExpandedItem x = p.ws.items[item];
     const int keys = max(x.keys, 0);
 
-    for (int i = tid; i < kRows * (kDim / 4); i += 256) {
+    for (int i = threadIdx.x; i < kRows * (kDim / 4); i += 256 * GROUPS) {
         const int r = i / (kDim / 4), c = i - r * (kDim / 4);
         cp_async16(smem_u32(qs + r * kPitch + 4 * c),
                    p.q + ((int64_t(x.q0) + min(r, x.rows - 1)) * p.heads + h) * kDim + 4 * c, r < x.rows);
@@ -147,8 +151,11 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) o[i][c] = 0.f;
     }
-    for (int k0 = 0; k0 < keys; k0 += kT) {
-        __syncthreads();                   // the last tile's readers are done
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    for (int k0 = group * kT; k0 < keys; k0 += GROUPS * kT) {
+        sync();                            // the last tile's readers are done
         for (int i = tid; i < kT * (kDim / 4); i += 256) {
             const int r = i / (kDim / 4), c = i - r * (kDim / 4);
             const bool there = k0 + r < keys;
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
+        sync();
         float s[RI][4] = {};
 #pragma unroll 2
         for (int c = 0; c < kDim / 4; ++c) {
@@ -233,7 +240,40 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
             }
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (GROUPS > 1) {
+        // the other groups' states: a thread's rows and columns are the same in all of them
+        constexpr int kState = RI * (kCols + 2);
+        float* mem = qs + kRows * kPitch;
+        __syncthreads();
+        if (group > 0) {
+            float* mine = mem + ((group - 1) * 256 + tid) * kState;
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                mine[i * (kCols + 2)] = m[i];
+                mine[i * (kCols + 2) + 1] = l[i];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) mine[i * (kCols + 2) + 2 + c] = o[i][c];
+            }
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+            float top = m[i];
+            for (int g = 0; g < GROUPS - 1; ++g) top = fmaxf(top, mem[(g * 256 + tid) * kState + i * (kCols + 2)]);
+            const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m[i] - ref);
+            l[i] *= a;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[i][c] *= a;
+            for (int g = 0; g < GROUPS - 1; ++g) {
+                const float* other = mem + (g * 256 + tid) * kState + i * (kCols + 2);
+                const float f = exp2f(other[0] - ref);
+                l[i] += f * other[1];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) o[i][c] += f * other[2 + c];
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
         const int r = ty + 16 * i;
@@ -247,17 +287,17 @@ __global__ void __launch_bounds__(256) expanded_f32_kernel(F32Params p) {
     }
 }
 
-template <int D, int RI>
+template <int D, int RI, int GROUPS>
 int launch_f32(const ExpandedArgs& a, const F32Params& p) {
-    constexpr int smem = f32_smem_floats<D, RI>() * int(sizeof(float));
+    constexpr int smem = f32_smem_floats<D, RI, GROUPS>() * int(sizeof(float));
     static_assert(smem <= 232448, "shared memory");
     const int st = launch_expanded_plan(a, 16 * RI);
     if (st != PKV_OK) return st;
-    if (kernel_occupancy<expanded_f32_kernel<D, RI>>(256, smem) < 1) return PKV_ERR_CUDA;
+    if (kernel_occupancy<expanded_f32_kernel<D, RI, GROUPS>>(256 * GROUPS, smem) < 1) return PKV_ERR_CUDA;
     const int64_t items = std::min<int64_t>(a.ws.max_items, ceil_div(a.num_query_tokens, 16 * RI) + int64_t(a.num_seqs));
     const int64_t grid = items * a.desc->num_heads;
     if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    return cuda_status(launch_pdl(expanded_f32_kernel<D, RI>, dim3(unsigned(grid)), dim3(256), size_t(smem),
+    return cuda_status(launch_pdl(expanded_f32_kernel<D, RI, GROUPS>, dim3(unsigned(grid)), dim3(256 * GROUPS), size_t(smem),
                                   a.stream, p));
 }
 
@@ -309,8 +349,8 @@ int launch_expanded_f32(const ExpandedArgs& a) {
                 float(double(a.scale) * 1.4426950408889634)};
     const int64_t units = int64_t(a.num_query_tokens) * a.desc->num_heads / 64;
     if (units >= 2 * std::max(num_sms(), 1))
-        return a.desc->head_dim == 128 ? launch_f32<128, 4>(a, p) : launch_f32<64, 4>(a, p);
-    return a.desc->head_dim == 128 ? launch_f32<128, 1>(a, p) : launch_f32<64, 1>(a, p);
+        return a.desc->head_dim == 128 ? launch_f32<128, 4, 1>(a, p) : launch_f32<64, 4, 1>(a, p);
+    return a.desc->head_dim == 128 ? launch_f32<128, 2, 2>(a, p) : launch_f32<64, 2, 2>(a, p);
 }
 
 }  // namespace pkv

@@ -35,7 +35,7 @@ struct ExpandedArgs {
 };
 
 constexpr int kExpandedRope = 64;
-constexpr int kExpandedRowsF32 = 16;       // query rows of a unit (fp32: 16 or 64)
+constexpr int kExpandedRowsF32 = 32;       // query rows of a unit (fp32: 32 or 64)
 constexpr int kExpandedRowsBf16 = 256;
 
 int launch_expanded_plan(const ExpandedArgs& a, int rows);

@@ -130,6 +130,7 @@ struct Params {
     __nv_bfloat16* out;
     int32_t q_groups;                      // 8-row groups of the query buffer
     int32_t slots;
+    bool whole_sectors;                    // out begins on 32 bytes
 };
 
 using Walk = LatentWalk<kRows, kKeys>;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = ra + 8 * e;
-                limit[e] = row < f.nrows ? f.first_pos + f.t0 + (f.rest + row) / p.b.heads : -1;
+                limit[e] = f.first_pos + f.t0 + (f.rest + min(row, f.nrows - 1)) / p.b.heads;
             }
             for (int j = 0; j < f.n; ++j, ++g) {
                 const uint32_t sb = g & (kSBufs - 1);
@@ -515,13 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (f.whole) {
                         const int d = c < half0 ? h * half0 + c : n0 + h * half1 + c - half0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t o[4];
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t o[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[e] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * e]) * inv,
-                                                   __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4*>(dst + d + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = pack_bf16x2(__uint_as_float(v[16 * i + 2 * e]) * inv,
+                                                   __uint_as_float(v[16 * i + 2 * e + 1]) * inv);
+                            store_sector(dst + d + 16 * i, o, p.whole_sectors);
                         }
                     } else {
                         // [4 columns][lane]: a warp writes 512 bytes in a row
@@ -562,6 +563,7 @@ int launch_latent_bf16(const LatentArgs& a) {
     p.ws = a.ws;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.b.team = latent_team(p.b, kRows);
+    p.whole_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     // query rows of a unit: all 64, or those of the longest sequence if it has fewer (a
     // call of one token a sequence; with offsets the rows of a sequence are not known here)
     const int64_t rows = a.batch.query_start_loc ? kRows : std::min<int64_t>(kRows, a.batch.heads);

@@ -80,24 +80,25 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
 
     LatentFrag f;
     while (w.next(p.b, f)) {
-        auto load = [&](int j) {
-            float* dst = kt + (j & 1) * kKeys * pitch;
-            const int key0 = (f.kt0 + j) * kKeys;
-            for (int i = tid; i < kKeys * vecs; i += kThreads) {
-                const int r = i / vecs, c = i - r * vecs;
-                const int key = key0 + r;
-                const float* src = p.cache;
-                bool there = key < f.ctx;
-                if (there) {
-                    const int blk = __ldg(p.b.block_tables + int64_t(f.seq) * p.b.table_stride + key / kBlockTokens);
-                    there = blk >= 0 && blk < p.b.num_blocks;
-                    if (there) src += (int64_t(blk) * kBlockTokens + key % kBlockTokens) * D + 4 * c;
-                    else flag_error(p.b.err, PKV_DEV_BAD_BLOCK_ID);
-                }
-                cp_async16(smem_u32(dst + r * pitch + 4 * c), src, there);
-            }
+        // a warp loads four of a tile's 32 rows; their block's id is asked for a tile ahead
+        const int32_t* table = p.b.block_tables + int64_t(f.seq) * p.b.table_stride;
+        auto block_of = [&](int j) {
+            const int key = (f.kt0 + j) * kKeys + warp * 4;   // (four rows are of one block)
+            return j < f.n && key < f.ctx ? __ldg(table + key / kBlockTokens) : 0;
+        };
+        auto load = [&](int j, int blk) {
+            float* dst = kt + (j & 1) * kKeys * pitch + warp * 4 * pitch;
+            const int key0 = (f.kt0 + j) * kKeys + warp * 4;
+            const bool good = blk >= 0 && blk < p.b.num_blocks;
+            if (!good && lane == 0 && key0 < f.ctx) flag_error(p.b.err, PKV_DEV_BAD_BLOCK_ID);
+            const float* src = p.cache + (int64_t(good ? blk : 0) * kBlockTokens + key0 % kBlockTokens) * D;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                for (int c = lane; c < vecs; c += 32)
+                    cp_async16(smem_u32(dst + r * pitch + 4 * c), src + r * D + 4 * c, good && key0 + r < f.ctx);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        int blk = block_of(0);
         __syncthreads();                                   // the last fragment's readers are done
         for (int i = tid; i < ROWS * vecs && f.n > 0; i += kThreads) {
             const int r = i / vecs, c = i - r * vecs;
@@ -105,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
             cp_async16(smem_u32(qs + r * pitch + 4 * c),
                        p.q + (there ? (int64_t(f.row0) + r) * D + 4 * c : 0), there);
         }
-        if (f.n > 0) load(0);
+        if (f.n > 0) load(0, blk);
+        blk = block_of(1);
 
         float acc[RPT][2];
 #pragma unroll
@@ -125,7 +127,8 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
         }
 
         for (int j = 0; j < f.n; ++j) {
-            if (j + 1 < f.n) load(j + 1);
+            if (j + 1 < f.n) load(j + 1, blk);
+            blk = block_of(j + 2);
             if (j + 1 < f.n) asm volatile("cp.async.wait_group 1;" ::: "memory");
             else asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncthreads();
