@@ -30,6 +30,8 @@ Modules
   splitfuse    token-budget composition of one forward pass (decodes + prompt chunks)
   rope         rotate-half rotary embedding fused into the append (fp32, bf16 rounding)
   quant        8-bit KV cache: per-(token, head) symmetric int8 codes and decode over them
+  latent       latent attention over a paged cache: append with norm and rotation, gather,
+               absorbed and expanded attention
   sparse       block tables served from a stack of free ids, key bounds of blocks, block
                selection by them and attention over listed blocks
 
@@ -38,5 +40,5 @@ values the pages print, closed forms, brute force on unpaged data, or
 invariants; none is marked "parity unpinned".
 """
 
-from . import (attention, block_pool, cache, kv_size, numerics, online, quant, rope,  # noqa: F401
-               sketch, sparse, splitfuse)
+from . import (attention, block_pool, cache, kv_size, latent, numerics, online, quant,  # noqa: F401
+               rope, sketch, sparse, splitfuse)

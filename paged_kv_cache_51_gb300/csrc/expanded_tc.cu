@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(smem + S::kRing + sl * kBox + at) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_shared();
+                    __syncwarp();                          // the TMEM stores want all lanes at once
                 }
                 // P = 2^(s scale - m) in bf16 (2^-8 of a weight at most), over S's own columns;
                 // the sum is of the weights before that rounding

@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!f.whole && h == 0) p.ws.ml[f.slot * kLatentRowTile + r] = make_float2(mr, lr);
             if (f.starts && int(threadIdx.x) == kSoftWarp0 * 32)
                 p.ws.merge[blockIdx.x] = LatentMerge{f.row0, f.nrows, int(blockIdx.x), f.last_cta, f.slot};
+            __syncwarp();                                  // the TMEM reads want all lanes at once
             if (f.n > 0) {
                 const float inv = 1.f / lr;
                 __nv_bfloat16* dst = p.out + int64_t(f.row0 + r) * p.b.latent;

@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(256) latent_gather_kernel(GatherParams p) {
             if (__ldg(p.starts + mid) <= t) lo = mid;
             else hi = mid;
         }
-        const int first = __ldg(p.starts + lo);
-        if (first > t || first < 0 || __ldg(p.starts + lo + 1) <= t) {
+        const int first = __ldg(p.starts + lo), next = __ldg(p.starts + lo + 1);
+        if (first > t || first < 0 || next <= t || next > end) {
             flag_error(p.err, PKV_DEV_BAD_QUERY_LAYOUT);
         } else {
             const int pos = t - first, blk_at = pos / kBlockTokens;
