@@ -135,33 +135,7 @@ struct Params {
 
 using Walk = LatentWalk<kRows, kKeys>;
 
-// The fragments' tiles one after the other, skipping fragments without any.
-struct Tiles {
-    Walk w;
-    LatentFrag f;
-    int j;                                 // tile of the fragment
-    uint32_t g, k;                         // tiles and fragments (of any tiles) so far
-    bool live;
-    __device__ void start(const LatentBatch& b, const Walk& from) {
-        w = from;
-        g = k = 0;
-        live = false;
-        frag(b);
-    }
-    __device__ void frag(const LatentBatch& b) {
-        j = 0;
-        do {
-            live = w.next(b, f);
-        } while (live && f.n == 0);
-    }
-    __device__ void next(const LatentBatch& b) {
-        ++g;
-        if (++j == f.n) {
-            ++k;
-            frag(b);
-        }
-    }
-};
+using Tiles = LatentTiles<kRows, kKeys>;
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
@@ -206,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     tc_fence_before();
-    const Walk plan = latent_plan<kRows, kKeys, kThreads>(p.b, sh.sums, kLeastSteps);
+    const Walk plan = latent_plan<kRows, kKeys, kThreads>(p.b, sh.sums, kLeastSteps, blockIdx.x, gridDim.x);
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
@@ -554,10 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int launch_latent_bf16(const LatentArgs& a) {
     const pkv_latent_desc* d = a.desc;
+    // more rows than a unit's go to pairs of CTAs (latent 512, us here and there: 96 requests of
+    // 1k to 8k keys with 128 rows 161 and 127, 32 with 72 rows 65 and 58)
+    if (latent_rows(a.batch) > kRows) return launch_latent_pair(a);
     const int cols = d->latent_dim / 64 + 1;
     CUtensorMap kv, q;
-    if (!make_latent_tensor_map(&kv, a.cache, int64_t(d->num_blocks) * kBlockTokens, cols, 8) ||
-        !make_latent_tensor_map(&q, a.q, int64_t(a.batch.num_query_tokens) * d->num_q_heads, cols, 8))
+    if (!make_latent_tensor_map(&kv, a.cache, int64_t(d->num_blocks) * kBlockTokens, cols, 8, cols) ||
+        !make_latent_tensor_map(&q, a.q, int64_t(a.batch.num_query_tokens) * d->num_q_heads, cols, 8, cols))
         return PKV_ERR_CUDA;
     Params p;
     p.b = a.batch;
@@ -578,7 +555,8 @@ int launch_latent_bf16(const LatentArgs& a) {
     cudaError_t e = launch_pdl(latent_kernel, dim3(num_sms()), dim3(kThreads), size_t(smem), a.stream, kv,
                                q, p);
     if (e != cudaSuccess) return cuda_status(e);
-    return launch_latent_merge<__nv_bfloat16>(a.stream, p.b, p.ws, p.out);
+    return launch_latent_merge<__nv_bfloat16>(a.stream, p.b, p.ws, p.out, num_sms(),
+                                              std::min(256, d->latent_dim) / 2);
 }
 
 }  // namespace pkv

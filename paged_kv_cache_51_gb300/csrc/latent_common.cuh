@@ -121,6 +121,7 @@ struct LatentWalk {
     int64_t left;                          // steps left of this team's stretch
     int64_t pos, total;                    // position among all steps
     int teams;
+    int cta;                               // (of the kernel's work; a pair counts as one)
     bool begun;
 
     __device__ static int groups(const LatentBatch& b, int rows) {
@@ -148,7 +149,7 @@ struct LatentWalk {
         f.kt0 = int(off - int64_t(group) * kt);
         int n = kt - f.kt0;
         if (n > left) n = int(left);
-        const int r0 = (group * b.team + int(blockIdx.x) % b.team) * ROWS;
+        const int r0 = (group * b.team + cta % b.team) * ROWS;
         f.seq = s;
         f.ctx = x.ctx;
         f.nrows = max(0, min(ROWS, rows - r0));
@@ -158,7 +159,7 @@ struct LatentWalk {
         f.first_pos = x.ctx - x.qlen;
         f.whole = f.kt0 == 0 && n == kt;
         f.starts = f.kt0 == 0 && n < kt;
-        f.slot = 2 * int(blockIdx.x) + (begun ? 1 : 0);
+        f.slot = 2 * cta + (begun ? 1 : 0);
         f.last_cta = 0;
         f.n = 0;
         if (f.nrows == 0) {                // this member has no rows of the unit
@@ -169,7 +170,7 @@ struct LatentWalk {
             const int want = (f.first_pos + last_tok) / KEYS + 1;   // tiles that any row sees
             f.n = max(0, min(f.kt0 + n, want) - f.kt0);
             if (f.starts)
-                f.last_cta = owner(pos + kt - 1, total, teams) * b.team + int(blockIdx.x) % b.team;
+                f.last_cta = owner(pos + kt - 1, total, teams) * b.team + cta % b.team;
         }
         begun = true;
         left -= n;
@@ -189,7 +190,7 @@ struct LatentWalk {
 // (All T threads call it; CTA 0 flags bad lengths.)
 template <int ROWS, int KEYS, int T>
 __device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch& b, int64_t* sums,
-                                                             int least) {
+                                                             int least, int cta, int ctas) {
     using Walk = LatentWalk<ROWS, KEYS>;
     constexpr int kWarps = T / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -214,8 +215,9 @@ __device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch&
     }
     Walk x;
     x.total = total;
-    const int team = int(blockIdx.x) / b.team;
-    x.teams = int(max(int64_t(1), min(int64_t(gridDim.x) / b.team, total / least)));
+    x.cta = cta;
+    const int team = cta / b.team;
+    x.teams = int(max(int64_t(1), min(int64_t(ctas) / b.team, total / least)));
     x.begun = false;
     const int64_t from = Walk::start_of(team, total, x.teams);
     x.left = team < x.teams ? Walk::start_of(team + 1, total, x.teams) - from : 0;
@@ -239,12 +241,45 @@ __device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch&
     return x;
 }
 
+// rows of a sequence, on average
+inline int64_t latent_rows(const LatentBatch& b) {
+    return int64_t(ceil_div(b.num_query_tokens, b.num_seqs)) * b.heads;
+}
 // CTAs of a team: the row tiles of a sequence, on average; at most 8 (152 CTAs make whole
 // teams of most sizes up to there, and L2 holds what lies between two members)
 inline int latent_team(const LatentBatch& b, int rows) {
-    const int64_t of = int64_t(ceil_div(b.num_query_tokens, b.num_seqs)) * b.heads;
+    const int64_t of = latent_rows(b);
     return int(of <= rows ? 1 : of >= 8 * int64_t(rows) ? 8 : (of + rows - 1) / rows);
 }
+
+// The fragments' tiles one after the other, skipping fragments without any.
+template <int ROWS, int KEYS>
+struct LatentTiles {
+    LatentWalk<ROWS, KEYS> w;
+    LatentFrag f;
+    int j;                                 // tile of the fragment
+    uint32_t g, k;                         // tiles and fragments (of any tiles) so far
+    bool live;
+    __device__ void start(const LatentBatch& b, const LatentWalk<ROWS, KEYS>& from) {
+        w = from;
+        g = k = 0;
+        live = false;
+        frag(b);
+    }
+    __device__ void frag(const LatentBatch& b) {
+        j = 0;
+        do {
+            live = w.next(b, f);
+        } while (live && f.n == 0);
+    }
+    __device__ void next(const LatentBatch& b) {
+        ++g;
+        if (++j == f.n) {
+            ++k;
+            frag(b);
+        }
+    }
+};
 
 // ---- tcgen05 and TMA ---------------------------------------------------------
 __device__ __forceinline__ uint64_t tc_smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -404,13 +439,14 @@ struct LatentArgs {
     cudaStream_t stream;
 };
 int launch_latent_bf16(const LatentArgs& a);
+int launch_latent_pair(const LatentArgs& a);
 int launch_latent_f32(const LatentArgs& a);
 
 // tmap.cu: rows of (latent / 64 + 1) x 64 bf16 values, row_bytes apart, as a 3-D tensor
-// (64 values, rows, 64-value columns); a box is `box_rows` rows of all columns and lands
-// column by column, each row's 128 bytes swizzled
+// (64 values, rows, 64-value columns); a box is `box_rows` rows of `box_columns` columns and
+// lands column by column, each row's 128 bytes swizzled
 bool make_latent_tensor_map(struct CUtensorMap_st* map, const void* base, int64_t rows,
-                            int32_t columns, int32_t box_rows);
+                            int32_t columns, int32_t box_rows, int32_t box_columns);
 // tmap.cu: bf16 [tokens][heads][dim] with strides in elements, as (dims, heads, tokens); a
 // box is 64 dims of one head, `box_tokens` tokens
 bool make_strided_tensor_map(struct CUtensorMap_st* map, const void* base, int32_t dim,

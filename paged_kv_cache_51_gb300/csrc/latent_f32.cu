@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
 
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    LatentWalk<ROWS, kKeys> w = latent_plan<ROWS, kKeys, kThreads>(p.b, sums, kLeastSteps);
+    LatentWalk<ROWS, kKeys> w = latent_plan<ROWS, kKeys, kThreads>(p.b, sums, kLeastSteps, blockIdx.x, gridDim.x);
     if (tid == 0) p.ws.merge[blockIdx.x].nrows = 0;
     // sequences with lengths that the call does not allow: zeros
     for (int s = blockIdx.x; s < p.b.num_seqs; s += gridDim.x) {
@@ -233,7 +233,7 @@ int launch(const LatentArgs& a, const Params& p) {
     cudaError_t e = launch_pdl(latent_f32_kernel<ROWS, RPT>, dim3(num_sms()), dim3(kThreads), size_t(smem),
                                a.stream, p);
     if (e != cudaSuccess) return cuda_status(e);
-    return launch_latent_merge<float>(a.stream, p.b, p.ws, p.out);
+    return launch_latent_merge<float>(a.stream, p.b, p.ws, p.out, num_sms(), 0);
 }
 
 }  // namespace

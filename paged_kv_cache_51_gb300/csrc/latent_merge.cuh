@@ -9,8 +9,9 @@
 // shared memory.
 //
 // An item's values lie as the attention left them.  bf16: [4 columns][128 lanes][4], lane
-// h * 64 + r being row r and half h of each product's columns; an item is 32 lanes and 8
-// columns.  fp32: [row][latent]; an item is (up to) 256 values of a row.
+// h * 64 + r being row r and half h of each product's columns (half0 of the first, the
+// others of the second); an item is 32 lanes and 8 columns.  fp32: [row][latent]; an item is
+// (up to) 256 values of a row.
 #pragma once
 
 #include "latent_common.cuh"
@@ -25,7 +26,7 @@ constexpr int kMergeCtas = 3;              // of an SM
 
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads, kMergeCtas)
-    latent_merge_kernel(LatentBatch b, LatentWorkspace ws, T* out, int ctas) {
+    latent_merge_kernel(LatentBatch b, LatentWorkspace ws, T* out, int ctas, int half0) {
     constexpr bool kWide = sizeof(T) == 4;
     __shared__ LatentMerge list[kMergeThreads];
     __shared__ int counts[kMergeWarps], tallest;
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int latent = b.latent, team = b.team;
     const int64_t stride = int64_t(kLatentRowTile) * latent;
-    const int n0 = min(256, latent), half0 = n0 / 2, half1 = (latent - n0) / 2;
+    const int n0 = 2 * half0, half1 = (latent - n0) / 2;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     for (int base = 0; base < ctas; base += kMergeThreads) {
@@ -162,9 +163,10 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas)
 }
 
 template <typename T>
-int launch_latent_merge(cudaStream_t stream, const LatentBatch& b, const LatentWorkspace& ws, T* out) {
+int launch_latent_merge(cudaStream_t stream, const LatentBatch& b, const LatentWorkspace& ws, T* out, int ctas,
+                        int half0) {
     return cuda_status(launch_pdl(latent_merge_kernel<T>, dim3(kMergeCtas * num_sms()), dim3(kMergeThreads), 0,
-                                  stream, b, ws, out, num_sms()));
+                                  stream, b, ws, out, ctas, half0));
 }
 
 }  // namespace

@@ -111,14 +111,14 @@ bool make_query_tensor_map(CUtensorMap* m, const void* q, int32_t num_tokens, in
 // `box_rows` rows and all columns lands as [column][row][128 bytes], 128-byte swizzled.
 // Rows past the end read as zero.
 bool make_latent_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int32_t columns,
-                            int32_t box_rows) {
-    const MapKey key{2, base, rows, columns, box_rows, 0};
+                            int32_t box_rows, int32_t box_columns) {
+    const MapKey key{2, base, rows, columns, box_rows, box_columns};
     if (map_lookup(key, m)) return true;
     auto fn = encode_fn();
     if (!fn || rows < 1 || rows >= (int64_t(1) << 31)) return false;
     const cuuint64_t gdim[3] = {64, cuuint64_t(rows), cuuint64_t(columns)};
     const cuuint64_t gstride[2] = {cuuint64_t(columns) * 128, 128};
-    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(columns)};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(box_columns)};
     const cuuint32_t estride[3] = {1, 1, 1};
     if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box,
            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
