@@ -86,9 +86,11 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
 // A CTA takes 64 query rows of one head and tiles of 64 keys; a thread keeps a 4 x 4 part
 // of the scores and 4 rows x D / 16 values of the output in registers.  Bound by the FMA
 // rate with shared memory close behind (8 reads of 16 bytes for 64 FMAs).  Where units of
-// 64 rows would not give every SM two, they have 32 (a 2 x 4 part), and two groups of 256
-// threads take every second tile of the keys and meet at the end: the tiles of a unit
-// follow one another, and six prompts of up to 300 tokens with 4 heads took 52 us.
+// 64 rows would not give every SM two, they have 32, of half as many threads, and a cluster
+// of four CTAs takes turns at the tiles of the keys and meets at the end: the tiles of a unit
+// follow one another, and six prompts of up to 300 tokens with 4 heads took 52 us with one CTA
+// a unit and take 25 with four.  P lies over the keys that it was made of, so that three such CTAs (heads of 128:
+// two) fit on an SM.
 struct F32Params {
     ExpandedWorkspace ws;
     const float *q, *k, *v, *k_rope;
@@ -101,10 +103,9 @@ struct F32Params {
 constexpr int kT = 64;                     // keys of a tile
 constexpr int kPPitch = kT + 4;
 
-template <int D, int RI, int GROUPS>
+template <int D, int THREADS>
 constexpr int f32_smem_floats() {
-    return 16 * RI * (D + kExpandedRope + 4) +
-           GROUPS * (kT * (D + kExpandedRope + 4) + kT * (D + 4) + 16 * RI * kPPitch);
+    return (THREADS / 4 + kT) * (D + kExpandedRope + 4) + kT * (D + 4);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -113,50 +114,60 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
                  : "memory");
 }
 
-// RI: rows of a thread; a unit has 16 of them.
-template <int D, int RI, int GROUPS>
-__global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p) {
-    constexpr int kRows = 16 * RI;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the value at this address of the cluster's CTA `rank`
+__device__ __forceinline__ float load_cluster(const float* at, int rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// A unit has THREADS / 4 rows; the CTAS of a cluster share one.
+template <int D, int THREADS, int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) expanded_f32_kernel(F32Params p) {
+    constexpr int RI = 4, kTy = THREADS / 16, kRows = kTy * RI;
     constexpr int kDim = D + kExpandedRope, kPitch = kDim + 4, kVPitch = D + 4;
     constexpr int kCols = D / 16;          // output values of a thread in a row
+    static_assert(kRows * kPPitch <= kT * kPitch, "P lies over the keys");
     extern __shared__ float4 smem4[];
-    constexpr int kGroup = kT * kPitch + kT * kVPitch + kRows * kPPitch;
-    const int group = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     float* qs = reinterpret_cast<float*>(smem4);
-    float* ks = qs + kRows * kPitch + group * kGroup;
+    float* ks = qs + kRows * kPitch;
     float* vs = ks + kT * kPitch;
-    float* ps = vs + kT * kVPitch;
-    auto sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); };
+    float* ps = ks;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    const int item = blockIdx.x / p.heads, h = blockIdx.x - item * p.heads;
+    const int unit = blockIdx.x / CTAS, rank = blockIdx.x % CTAS;
+    const int item = unit / p.heads, h = unit - item * p.heads;
     if (item >= p.ws.counters[0]) return;
     const ExpandedItem x = p.ws.items[item];
     const int keys = max(x.keys, 0);
 
-    for (int i = threadIdx.x; i < kRows * (kDim / 4); i += 256 * GROUPS) {
+    for (int i = threadIdx.x; i < kRows * (kDim / 4); i += THREADS) {
         const int r = i / (kDim / 4), c = i - r * (kDim / 4);
         cp_async16(smem_u32(qs + r * kPitch + 4 * c),
                    p.q + ((int64_t(x.q0) + min(r, x.rows - 1)) * p.heads + h) * kDim + 4 * c, r < x.rows);
     }
-    // rows ty + 16 i, keys and values tx + 16 j (in fours)
+    // rows ty + kTy i, keys and values tx + 16 j (in fours)
     float m[RI], l[RI], o[RI][kCols];
     int limit[RI];
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
-        const int r = ty + 16 * i;
+        const int r = ty + kTy * i;
         limit[i] = r < x.rows ? x.keys - x.rows + r : -1;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) o[i][c] = 0.f;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    for (int k0 = group * kT; k0 < keys; k0 += GROUPS * kT) {
-        sync();                            // the last tile's readers are done
-        for (int i = tid; i < kT * (kDim / 4); i += 256) {
+    for (int k0 = rank * kT; k0 < keys; k0 += CTAS * kT) {
+        __syncthreads();                   // the last tile's readers are done
+        for (int i = tid; i < kT * (kDim / 4); i += THREADS) {
             const int r = i / (kDim / 4), c = i - r * (kDim / 4);
             const bool there = k0 + r < keys;
             const int64_t row = int64_t(x.k0) + (there ? k0 + r : 0);
@@ -164,22 +175,23 @@ __global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p)
                                          : p.k_rope + row * kExpandedRope + 4 * (c - D / 4);
             cp_async16(smem_u32(ks + r * kPitch + 4 * c), src, there);
         }
-        for (int i = tid; i < kT * (D / 4); i += 256) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int i = tid; i < kT * (D / 4); i += THREADS) {
             const int r = i / (D / 4), c = i - r * (D / 4);
             const bool there = k0 + r < keys;
             const int64_t row = int64_t(x.k0) + (there ? k0 + r : 0);
             cp_async16(smem_u32(vs + r * kVPitch + 4 * c), p.v + row * p.v_token + h * p.v_head + 4 * c, there);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        sync();
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
         float s[RI][4] = {};
 #pragma unroll 2
         for (int c = 0; c < kDim / 4; ++c) {
             float4 a[RI], b[4];
 #pragma unroll
             for (int i = 0; i < RI; ++i)
-                a[i] = *reinterpret_cast<const float4*>(qs + (ty + 16 * i) * kPitch + 4 * c);
+                a[i] = *reinterpret_cast<const float4*>(qs + (ty + kTy * i) * kPitch + 4 * c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 b[i] = *reinterpret_cast<const float4*>(ks + (tx + 16 * i) * kPitch + 4 * c);
@@ -189,6 +201,7 @@ __global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p)
                 for (int j = 0; j < 4; ++j)
                     s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
         }
+        __syncthreads();                   // the keys have been read
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
             float mx = -INFINITY;
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float e = exp2f(s[i][j] - ref);
-                ps[(ty + 16 * i) * kPPitch + tx + 16 * j] = e;
+                ps[(ty + kTy * i) * kPPitch + tx + 16 * j] = e;
                 sum += e;
             }
 #pragma unroll
@@ -216,13 +229,14 @@ __global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p)
 #pragma unroll
             for (int c = 0; c < kCols; ++c) o[i][c] *= a;
         }
-        __syncwarp();                      // a row's 16 threads are one half of a warp
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
 #pragma unroll 2
         for (int k = 0; k < kT; k += 4) {
             float4 e[RI];
 #pragma unroll
             for (int i = 0; i < RI; ++i)
-                e[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * kPPitch + k);
+                e[i] = *reinterpret_cast<const float4*>(ps + (ty + kTy * i) * kPPitch + k);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
@@ -240,44 +254,49 @@ __global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p)
             }
         }
     }
-    if constexpr (GROUPS > 1) {
-        // the other groups' states: a thread's rows and columns are the same in all of them
-        constexpr int kState = RI * (kCols + 2);
-        float* mem = qs + kRows * kPitch;
-        __syncthreads();
-        if (group > 0) {
-            float* mine = mem + ((group - 1) * 256 + tid) * kState;
-#pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                mine[i * (kCols + 2)] = m[i];
-                mine[i * (kCols + 2) + 1] = l[i];
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) mine[i * (kCols + 2) + 2 + c] = o[i][c];
-            }
-        }
-        __syncthreads();
-        if (group > 0) return;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");   // (the queries, where there was no tile)
+    if constexpr (CTAS > 1) {
+        // the CTAs' states: a thread's rows and columns are the same in all of them.  CTA r of
+        // the cluster joins the rows i = r
+        constexpr int kState = kCols + 2;
+        static_assert(RI == CTAS && RI * kState * THREADS <= kT * kPitch, "states");
+        __syncthreads();                   // the last tile's readers are done
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
-            float top = m[i];
-            for (int g = 0; g < GROUPS - 1; ++g) top = fmaxf(top, mem[(g * 256 + tid) * kState + i * (kCols + 2)]);
-            const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m[i] - ref);
-            l[i] *= a;
+            float* mine = ks + i * kState * THREADS + tid;
+            mine[0] = m[i];
+            mine[THREADS] = l[i];
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) o[i][c] *= a;
-            for (int g = 0; g < GROUPS - 1; ++g) {
-                const float* other = mem + (g * 256 + tid) * kState + i * (kCols + 2);
-                const float f = exp2f(other[0] - ref);
-                l[i] += f * other[1];
+            for (int c = 0; c < kCols; ++c) mine[(2 + c) * THREADS] = o[i][c];
+        }
+        cluster_sync();
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) o[i][c] += f * other[2 + c];
+        for (int i = 0; i < RI; ++i) {
+            if (i != rank) continue;
+            float part[CTAS][kState];
+#pragma unroll
+            for (int q = 0; q < CTAS; ++q)
+#pragma unroll
+                for (int c = 0; c < kState; ++c) part[q][c] = load_cluster(ks + (i * kState + c) * THREADS + tid, q);
+            const float top = fmaxf(fmaxf(part[0][0], part[1][0]), fmaxf(part[2][0], part[3][0]));
+            const float ref = top == -INFINITY ? 0.f : top;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[i][c] = 0.f;
+#pragma unroll
+            for (int q = 0; q < CTAS; ++q) {
+                const float f = exp2f(part[q][0] - ref);
+                l[i] += f * part[q][1];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) o[i][c] += f * part[q][2 + c];
             }
         }
+        cluster_sync();                    // nobody leaves while its states are being read
     }
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= x.rows) continue;
+        const int r = ty + kTy * i;
+        if (r >= x.rows || (CTAS > 1 && i != rank)) continue;
         const float inv = limit[i] >= 0 ? 1.f / l[i] : 0.f;      // a query without keys: zeros
         float* dst = p.out + ((int64_t(x.q0) + r) * p.heads + h) * D + 4 * tx;
 #pragma unroll
@@ -287,18 +306,18 @@ __global__ void __launch_bounds__(256 * GROUPS) expanded_f32_kernel(F32Params p)
     }
 }
 
-template <int D, int RI, int GROUPS>
+template <int D, int THREADS, int CTAS>
 int launch_f32(const ExpandedArgs& a, const F32Params& p) {
-    constexpr int smem = f32_smem_floats<D, RI, GROUPS>() * int(sizeof(float));
+    constexpr int smem = f32_smem_floats<D, THREADS>() * int(sizeof(float)), rows = THREADS / 4;
     static_assert(smem <= 232448, "shared memory");
-    const int st = launch_expanded_plan(a, 16 * RI);
+    const int st = launch_expanded_plan(a, rows);
     if (st != PKV_OK) return st;
-    if (kernel_occupancy<expanded_f32_kernel<D, RI, GROUPS>>(256 * GROUPS, smem) < 1) return PKV_ERR_CUDA;
-    const int64_t items = std::min<int64_t>(a.ws.max_items, ceil_div(a.num_query_tokens, 16 * RI) + int64_t(a.num_seqs));
-    const int64_t grid = items * a.desc->num_heads;
+    if (kernel_occupancy<expanded_f32_kernel<D, THREADS, CTAS>>(THREADS, smem) < 1) return PKV_ERR_CUDA;
+    const int64_t items = std::min<int64_t>(a.ws.max_items, ceil_div(a.num_query_tokens, rows) + int64_t(a.num_seqs));
+    const int64_t grid = items * a.desc->num_heads * CTAS;
     if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    return cuda_status(launch_pdl(expanded_f32_kernel<D, RI, GROUPS>, dim3(unsigned(grid)), dim3(256 * GROUPS), size_t(smem),
-                                  a.stream, p));
+    return cuda_status(launch_pdl(expanded_f32_kernel<D, THREADS, CTAS>, dim3(unsigned(grid)), dim3(THREADS),
+                                  size_t(smem), a.stream, p));
 }
 
 int check_expanded_desc(const pkv_expanded_desc* d) {
@@ -349,8 +368,8 @@ int launch_expanded_f32(const ExpandedArgs& a) {
                 float(double(a.scale) * 1.4426950408889634)};
     const int64_t units = int64_t(a.num_query_tokens) * a.desc->num_heads / 64;
     if (units >= 2 * std::max(num_sms(), 1))
-        return a.desc->head_dim == 128 ? launch_f32<128, 4, 1>(a, p) : launch_f32<64, 4, 1>(a, p);
-    return a.desc->head_dim == 128 ? launch_f32<128, 2, 2>(a, p) : launch_f32<64, 2, 2>(a, p);
+        return a.desc->head_dim == 128 ? launch_f32<128, 256, 1>(a, p) : launch_f32<64, 256, 1>(a, p);
+    return a.desc->head_dim == 128 ? launch_f32<128, 128, 4>(a, p) : launch_f32<64, 128, 4>(a, p);
 }
 
 }  // namespace pkv
