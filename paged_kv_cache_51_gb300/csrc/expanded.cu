@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
 // 64 rows would not give every SM two, they have 32, of half as many threads, and a cluster
 // of four CTAs takes turns at the tiles of the keys and meets at the end: the tiles of a unit
 // follow one another, and six prompts of up to 300 tokens with 4 heads took 52 us with one CTA
-// a unit and take 25 with four.  P lies over the keys that it was made of, so that three such CTAs (heads of 128:
-// two) fit on an SM.
+// a unit and take 25 with four.  P lies over the keys that it was made of, so that three such
+// CTAs (heads of 128: two) fit on an SM.
 struct F32Params {
     ExpandedWorkspace ws;
     const float *q, *k, *v, *k_rope;
