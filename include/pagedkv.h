@@ -746,7 +746,9 @@ PKV_API size_t pkv_latent_workspace_bytes(const pkv_latent_desc* desc, int32_t n
  * (PKV_DEV_TABLE_TOO_NARROW) gives zeros; a block id out of range sets
  * PKV_DEV_BAD_BLOCK_ID and leaves the sequence's outputs undefined; a sequence whose
  * offsets fall or pass num_query_tokens, and the first where they do not begin with 0,
- * is not computed (PKV_DEV_BAD_QUERY_LAYOUT). */
+ * is not computed (PKV_DEV_BAD_QUERY_LAYOUT).  Rows of the cache behind a sequence's
+ * context may hold anything.  A row of its own that is not finite may make NaN of all of
+ * the sequence's outputs, also of tokens in front of it: their weight for it is 0. */
 PKV_API int paged_attention_latent(void* out, const void* q, const void* latent_cache,
                                    const pkv_latent_desc* desc, const int32_t* block_tables,
                                    int32_t max_blocks_per_seq, const int32_t* query_start_loc,
@@ -781,8 +783,9 @@ PKV_API size_t pkv_expanded_workspace_bytes(const pkv_expanded_desc* desc, int32
  *   scale: above 0; usually 1 / sqrt(head_dim + 64)
  * Rows behind the last sequence are left as they are; a sequence whose offsets fall or
  * pass num_query_tokens or num_keys is not computed (PKV_DEV_BAD_QUERY_LAYOUT).  Keys and
- * values that no query of the call sees may hold anything.  Sums and softmax in fp32;
- * for PKV_BF16 the weights enter the second product in bf16.  workspace: 256-byte
+ * values that no query of the call sees may hold anything; a value that is not finite may
+ * make NaN of all outputs of its sequence and head, also of queries in front of it, whose
+ * weight for it is 0.  Sums and softmax in fp32; for PKV_BF16 the weights enter the second product in bf16.  workspace: 256-byte
  * aligned, not shared by concurrent calls. */
 PKV_API int pkv_attention_expanded(void* out, const void* q, const void* k, const void* v,
                                    const void* k_rope, const pkv_expanded_desc* desc,

@@ -97,6 +97,12 @@ def test_longer_prompts_and_chunks(pkv, dtype, d, h, new, keys):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_precision_with_units_for_every_sm(pkv, d):
+    """So many rows that a CTA takes 64 of them alone (fewer are shared by a cluster)."""
+    Case(np.random.default_rng(d), "f32", 110, d, [180, 1], [200, 90]).check(pkv)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("new,keys", [([10], [4]), ([300, 7], [20, 0]), ([3, 260, 2], [0, 131, 2]),
