@@ -1,18 +1,18 @@
 // Attention over a paged latent cache in single precision, on the CUDA cores.
 //
-// A CTA of eight warps takes ROWS (token, head) rows of one sequence and tiles of 32 keys,
+// A CTA of eight warps takes ROWS (token, head) rows of one sequence and tiles of KEYS keys,
 // two of them in flight (cp.async).  Products in fp32 have no tensor-core form that keeps
-// their bits, so what bounds it beyond a few heads is the FMA rate, and shared memory in
-// front of it: a thread therefore keeps a key's part (S) or a value's part (O) in
-// registers against all rows.
-//   S: warp w holds an eighth of the dimensions, lane = key, one sum per row: per 4
-//      dimensions one read of its own and ROWS reads that all lanes share.
-//      The eighths meet in shared memory.
-//   O: a thread owns two dimensions and ROWS (or, for short vectors, a share of the) rows.
-// Rows of keys lie four floats further apart than they are long, so that 32 lanes reading
-// 16 bytes of 32 rows meet no bank twice.
-// 8 rows where that covers a sequence's rows, else 16: with 16, half of the products of an
-// 8-head decode step would be for nothing.
+// their bits, so what bounds it beyond a few heads is the FMA rate, and in front of it what
+// shared memory returns: 128 bytes a cycle, so that a read of 16 bytes a lane costs a warp
+// four cycles even where all lanes read the same, the time of 16 FMAs of a warp.
+//   S: warp w holds an eighth of the dimensions of all ROWS x KEYS scores, a lane a part of
+//      RT x KT: RT + KT reads for 4 RT KT FMAs (rows against one key of a lane, 17 reads for
+//      64 FMAs, ran at 13 TFLOP/s).  The eighths meet in shared memory.
+//   O: a thread owns four dimensions of a share of the rows.
+// Rows of keys lie four floats further apart than they are long, so that 8 lanes reading 16
+// bytes of 8 rows meet no bank twice.
+// 8, 16 or 32 rows, the least that covers a sequence's rows: with more, products would be
+// for nothing.  32 rows of 512 + 64 dimensions leave room for tiles of 16 keys only.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,7 +25,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kKeys = 32;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLeastSteps = 2;
@@ -44,22 +43,29 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
                  : "memory");
 }
 
+// floats of a row of the eighths: the rows that a warp writes at once begin on different banks
+template <int KEYS>
+constexpr int kPartPitch = KEYS == 32 ? 40 : 20;
+
 // floats of shared memory: two key tiles, queries, eighths of S, P, alpha
-__host__ __device__ constexpr int smem_floats(int latent, int rows) {
-    return (2 * kKeys + rows) * (latent + kLatentRope + 4) + kWarps * rows * kKeys + kKeys * rows + 3 * rows;
+template <int ROWS, int KEYS>
+constexpr int smem_floats(int latent) {
+    return (2 * KEYS + ROWS) * (latent + kLatentRope + 4) + kWarps * ROWS * kPartPitch<KEYS> +
+           KEYS * (ROWS + 4) + 3 * ROWS;
 }
 
-// RPT: rows of a thread in the second product.
-template <int ROWS, int RPT>
+// RG: shares of the rows in the second product.
+template <int ROWS, int KEYS, int RG>
 __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
+    constexpr int RPT = ROWS / RG, kPtPitch = ROWS + 4, kPitch = kPartPitch<KEYS>;
     extern __shared__ float4 smem4[];
     float* smem = reinterpret_cast<float*>(smem4);
     const int R = p.b.latent, D = R + kLatentRope, pitch = D + 4;
-    float* kt = smem;                                      // [2][kKeys][pitch]
-    float* qs = kt + 2 * kKeys * pitch;                    // [ROWS][pitch]
-    float* part = qs + ROWS * pitch;                       // [kWarps][ROWS][kKeys]
-    float* pt = part + kWarps * ROWS * kKeys;              // [kKeys][ROWS]
-    float* alpha = pt + kKeys * ROWS;                      // [ROWS]
+    float* kt = smem;                                      // [2][KEYS][pitch]
+    float* qs = kt + 2 * KEYS * pitch;                     // [ROWS][pitch]
+    float* part = qs + ROWS * pitch;                       // [kWarps][ROWS][kPitch]
+    float* pt = part + kWarps * ROWS * kPitch;             // [KEYS][kPtPitch]
+    float* alpha = pt + KEYS * kPtPitch;                   // [ROWS]
     float* row_m = alpha + ROWS;                           // [ROWS], at the end of a fragment
     float* row_l = row_m + ROWS;
     __shared__ int64_t sums[kWarps + 2];
@@ -68,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
 
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    LatentWalk<ROWS, kKeys> w = latent_plan<ROWS, kKeys, kThreads>(p.b, sums, kLeastSteps, blockIdx.x, gridDim.x);
+    LatentWalk<ROWS, KEYS> w = latent_plan<ROWS, KEYS, kThreads>(p.b, sums, kLeastSteps, blockIdx.x, gridDim.x);
     if (tid == 0) p.ws.merge[blockIdx.x].nrows = 0;
     // sequences with lengths that the call does not allow: zeros
     for (int s = blockIdx.x; s < p.b.num_seqs; s += gridDim.x) {
@@ -80,20 +86,21 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
 
     LatentFrag f;
     while (w.next(p.b, f)) {
-        // a warp loads four of a tile's 32 rows; their block's id is asked for a tile ahead
+        // a warp loads an eighth of a tile's rows; their block's id is asked for a tile ahead
+        constexpr int kLoad = KEYS / kWarps;               // (of one block)
         const int32_t* table = p.b.block_tables + int64_t(f.seq) * p.b.table_stride;
         auto block_of = [&](int j) {
-            const int key = (f.kt0 + j) * kKeys + warp * 4;   // (four rows are of one block)
+            const int key = (f.kt0 + j) * KEYS + warp * kLoad;
             return j < f.n && key < f.ctx ? __ldg(table + key / kBlockTokens) : 0;
         };
         auto load = [&](int j, int blk) {
-            float* dst = kt + (j & 1) * kKeys * pitch + warp * 4 * pitch;
-            const int key0 = (f.kt0 + j) * kKeys + warp * 4;
+            float* dst = kt + ((j & 1) * KEYS + warp * kLoad) * pitch;
+            const int key0 = (f.kt0 + j) * KEYS + warp * kLoad;
             const bool good = blk >= 0 && blk < p.b.num_blocks;
             if (!good && lane == 0 && key0 < f.ctx) flag_error(p.b.err, PKV_DEV_BAD_BLOCK_ID);
             const float* src = p.cache + (int64_t(good ? blk : 0) * kBlockTokens + key0 % kBlockTokens) * D;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < kLoad; ++r)
                 for (int c = lane; c < vecs; c += 32)
                     cp_async16(smem_u32(dst + r * pitch + 4 * c), src + r * D + 4 * c, good && key0 + r < f.ctx);
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -109,20 +116,24 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
         if (f.n > 0) load(0, blk);
         blk = block_of(1);
 
-        float acc[RPT][2];
+        float acc[RPT][4];
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = 0.f;
-        const int pairs = R / 2;
-        const int d2 = tid % pairs, rg = tid / pairs;      // a thread's dimensions and rows
-        const bool owner = rg * RPT < ROWS;
-        constexpr int kMine = ROWS / kWarps;               // softmax rows of a warp
-        float m[kMine], l[kMine];
-        int limit[kMine];
+        for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        const int fours = R / 4;
+        const int d4 = tid % fours, rg = tid / fours;      // a thread's dimensions and rows
+        const bool owner = rg < RG;
+        // softmax: KEYS lanes a row, kOnce rows of a warp at once
+        constexpr int kOnce = 32 / KEYS, kMine = ROWS / kWarps, kTurns = kMine / kOnce;
+        static_assert(kTurns * kOnce == kMine, "rows of a warp");
+        const int key_lane = lane % KEYS;
+        float m[kTurns], l[kTurns];
+        int limit[kTurns];
+        auto row_of = [&](int i) { return warp * kMine + i * kOnce + lane / KEYS; };
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
+        for (int i = 0; i < kTurns; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
-            const int r = warp * kMine + i;
+            const int r = row_of(i);
             limit[i] = r < f.nrows ? f.first_pos + f.t0 + (f.rest + r) / p.b.heads : -1;
         }
 
@@ -132,74 +143,97 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
             if (j + 1 < f.n) asm volatile("cp.async.wait_group 1;" ::: "memory");
             else asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncthreads();
-            const float* kb = kt + (j & 1) * kKeys * pitch;
+            const float* kb = kt + (j & 1) * KEYS * pitch;
             {
-                float s[ROWS];
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i) s[i] = 0.f;
+                // lanes: kLr by kLk; a lane's rows kLr apart, its keys kLk apart
+                constexpr int kLr = KEYS == 32 ? 4 : 8, kLk = 32 / kLr, RT = ROWS / kLr, KT = KEYS / kLk;
+                const int lr = lane / kLk, lk = lane % kLk;
+                float s[RT][KT] = {};
                 const int c1 = vecs / kWarps;              // (D is a multiple of 32)
-                const float4* krow = reinterpret_cast<const float4*>(kb + lane * pitch) + warp * c1;
-                const float4* qrow = reinterpret_cast<const float4*>(qs) + warp * c1;
+                const float* krow = kb + lk * pitch + 4 * warp * c1;
+                const float* qrow = qs + lr * pitch + 4 * warp * c1;
+#pragma unroll 2
                 for (int c = 0; c < c1; ++c) {
-                    const float4 k = krow[c];
+                    float4 q[RT], k[KT];
 #pragma unroll
-                    for (int i = 0; i < ROWS; ++i) {
-                        const float4 q = qrow[i * (pitch / 4) + c];
-                        s[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[i]))));
-                    }
+                    for (int i = 0; i < RT; ++i) q[i] = *reinterpret_cast<const float4*>(qrow + i * kLr * pitch + 4 * c);
+#pragma unroll
+                    for (int e = 0; e < KT; ++e) k[e] = *reinterpret_cast<const float4*>(krow + e * kLk * pitch + 4 * c);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int e = 0; e < KT; ++e)
+                            s[i][e] = fmaf(q[i].x, k[e].x, fmaf(q[i].y, k[e].y,
+                                          fmaf(q[i].z, k[e].z, fmaf(q[i].w, k[e].w, s[i][e]))));
                 }
 #pragma unroll
-                for (int i = 0; i < ROWS; ++i) part[(warp * ROWS + i) * kKeys + lane] = s[i];
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int e = 0; e < KT; ++e)
+                        part[(warp * ROWS + lr + i * kLr) * kPitch + lk + e * kLk] = s[i][e];
             }
             __syncthreads();
-            const int key = (f.kt0 + j) * kKeys + lane;
+            const int key = (f.kt0 + j) * KEYS + key_lane;
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int r = warp * kMine + i;
+            for (int i = 0; i < kTurns; ++i) {
+                const int r = row_of(i);
                 float s = 0.f;
 #pragma unroll
-                for (int e = 0; e < kWarps; ++e) s += part[(e * ROWS + r) * kKeys + lane];
+                for (int e = 0; e < kWarps; ++e) s += part[(e * ROWS + r) * kPitch + key_lane];
                 s = key <= limit[i] ? s * p.b.scale_log2 : -INFINITY;
                 float mx = s;
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                for (int d = KEYS / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                 const float m_new = fmaxf(m[i], mx);
                 const float a = m_new == -INFINITY ? 1.f : exp2f(m[i] - m_new);
                 const float e = exp2f(s - (m_new == -INFINITY ? 0.f : m_new));
                 float sum = e;
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                for (int d = KEYS / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 m[i] = m_new;
                 l[i] = l[i] * a + sum;
-                pt[lane * ROWS + r] = e;
-                if (lane == 0) alpha[r] = a;
+                pt[key_lane * kPtPitch + r] = e;
+                if (key_lane == 0) alpha[r] = a;
             }
             __syncthreads();
             if (owner) {
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
                     const float a = alpha[rg * RPT + i];
-                    acc[i][0] *= a;
-                    acc[i][1] *= a;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] *= a;
                 }
 #pragma unroll 4
-                for (int k = 0; k < kKeys; ++k) {
-                    const float2 v = *reinterpret_cast<const float2*>(kb + k * pitch + 2 * d2);
-                    const float* pk = pt + k * ROWS + rg * RPT;
+                for (int k = 0; k < KEYS; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(kb + k * pitch + 4 * d4);
+                    float w[RPT];
+                    const float* pk = pt + k * kPtPitch + rg * RPT;
+                    if constexpr (RPT % 4 == 0) {
+#pragma unroll
+                        for (int i = 0; i < RPT; i += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(pk + i);
+                            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < RPT; ++i) w[i] = pk[i];
+                    }
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {
-                        acc[i][0] = fmaf(pk[i], v.x, acc[i][0]);
-                        acc[i][1] = fmaf(pk[i], v.y, acc[i][1]);
+                        acc[i][0] = fmaf(w[i], v.x, acc[i][0]);
+                        acc[i][1] = fmaf(w[i], v.y, acc[i][1]);
+                        acc[i][2] = fmaf(w[i], v.z, acc[i][2]);
+                        acc[i][3] = fmaf(w[i], v.w, acc[i][3]);
                     }
                 }
             }
             __syncthreads();                               // the buffer may be filled again
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (lane == 0) {
+        if (key_lane == 0) {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int r = warp * kMine + i;
+            for (int i = 0; i < kTurns; ++i) {
+                const int r = row_of(i);
                 row_l[r] = l[i];
                 if (!f.whole) p.ws.ml[f.slot * kLatentRowTile + r] = make_float2(m[i], l[i]);
             }
@@ -215,25 +249,40 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
                 if (r >= f.nrows) continue;
                 if (f.whole) {
                     const float inv = 1.f / row_l[r];
-                    *reinterpret_cast<float2*>(p.out + (int64_t(f.row0) + r) * R + 2 * d2) =
-                        make_float2(acc[i][0] * inv, acc[i][1] * inv);
+                    *reinterpret_cast<float4*>(p.out + (int64_t(f.row0) + r) * R + 4 * d4) =
+                        make_float4(acc[i][0] * inv, acc[i][1] * inv, acc[i][2] * inv, acc[i][3] * inv);
                 } else {
-                    *reinterpret_cast<float2*>(part_o + r * R + 2 * d2) = make_float2(acc[i][0], acc[i][1]);
+                    *reinterpret_cast<float4*>(part_o + r * R + 4 * d4) =
+                        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
                 }
             }
         }
     }
 }
 
-template <int ROWS, int RPT>
-int launch(const LatentArgs& a, const Params& p) {
-    const int smem = smem_floats(a.desc->latent_dim, ROWS) * int(sizeof(float));
-    if (kernel_occupancy<latent_f32_kernel<ROWS, RPT>>(kThreads, smem_floats(512, ROWS) * int(sizeof(float))) < 1)
-        return PKV_ERR_CUDA;
-    cudaError_t e = launch_pdl(latent_f32_kernel<ROWS, RPT>, dim3(num_sms()), dim3(kThreads), size_t(smem),
+template <int ROWS, int KEYS, int RG>
+int launch(const LatentArgs& a, Params& p) {
+    p.b.team = latent_team(p.b, ROWS);
+    const int smem = smem_floats<ROWS, KEYS>(a.desc->latent_dim) * int(sizeof(float));
+    constexpr int most = RG == 8 ? 128 : RG == 4 ? 256 : ROWS == 32 && KEYS == 32 ? 384 : 512;
+    constexpr int limit = smem_floats<ROWS, KEYS>(most) * int(sizeof(float));
+    static_assert(limit + (kWarps + 2) * 8 <= 232448, "shared memory");
+    if (kernel_occupancy<latent_f32_kernel<ROWS, KEYS, RG>>(kThreads, limit) < 1) return PKV_ERR_CUDA;
+    cudaError_t e = launch_pdl(latent_f32_kernel<ROWS, KEYS, RG>, dim3(num_sms()), dim3(kThreads), size_t(smem),
                                a.stream, p);
     if (e != cudaSuccess) return cuda_status(e);
     return launch_latent_merge<float>(a.stream, p.b, p.ws, p.out, num_sms(), 0);
+}
+
+// threads of four dimensions: 256 of 32, 64, 96 or 128
+template <int ROWS>
+int launch_rows(const LatentArgs& a, Params& p) {
+    switch (a.desc->latent_dim) {
+        case 128: return launch<ROWS, 32, 8>(a, p);
+        case 256: return launch<ROWS, 32, 4>(a, p);
+        case 384: return launch<ROWS, 32, 2>(a, p);
+        default: return launch<ROWS, ROWS == 32 ? 16 : 32, 2>(a, p);
+    }
 }
 
 }  // namespace
@@ -245,14 +294,8 @@ int launch_latent_f32(const LatentArgs& a) {
     p.out = static_cast<float*>(a.out);
     p.q = static_cast<const float*>(a.q);
     p.cache = static_cast<const float*>(a.cache);
-    static_assert(smem_floats(512, 16) * 4 <= 232448, "shared memory");
-    // rows of a sequence, on average
-    const int64_t rows = int64_t(ceil_div(p.b.num_query_tokens, p.b.num_seqs)) * p.b.heads;
-    p.b.team = latent_team(p.b, rows <= 8 ? 8 : 16);
-    const int groups = std::max(1, kThreads / (p.b.latent / 2));   // threads of one pair of dimensions
-    if (rows <= 8)
-        return groups == 1 ? launch<8, 8>(a, p) : groups == 2 ? launch<8, 4>(a, p) : launch<8, 2>(a, p);
-    return groups == 1 ? launch<16, 16>(a, p) : groups == 2 ? launch<16, 8>(a, p) : launch<16, 4>(a, p);
+    const int64_t rows = latent_rows(p.b);
+    return rows <= 8 ? launch_rows<8>(a, p) : rows <= 16 ? launch_rows<16>(a, p) : launch_rows<32>(a, p);
 }
 
 }  // namespace pkv
