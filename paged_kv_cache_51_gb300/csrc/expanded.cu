@@ -19,7 +19,7 @@ struct PlanParams {
     const int32_t* q_start;
     const int32_t* k_start;
     int32_t num_seqs, num_query_tokens, num_keys, max_query_len;
-    int32_t rows;
+    int32_t rows, group;
     ExpandedWorkspace ws;
     int* err;
 };
@@ -47,17 +47,20 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
                 if (flag) flag_error(p.err, PKV_DEV_BAD_QUERY_LAYOUT);
                 continue;
             }
-            for (int r = 0; r < q1 - q0; r += p.rows) {
+            // groups from the sequence's last unit on, each in the bin of its longest
+            for (int left = (q1 - q0 + p.rows - 1) / p.rows; left > 0; left -= p.group) {
+                const int n = min(p.group, left), r = (left - 1) * p.rows;
                 ExpandedItem x;
                 x.q0 = q0 + r;
                 x.rows = min(p.rows, q1 - q0 - r);
                 x.k0 = k0;
                 x.keys = (k1 - k0) - (q1 - q0) + r + x.rows;
+                x.members = n;
                 take(x, kBins - 1 - min(kBins - 1, (max(x.keys, 0) + 127) / 128));
             }
         }
     };
-    each(true, [&](const ExpandedItem&, int b) { atomicAdd(&bin[b], 1); });
+    each(true, [&](const ExpandedItem& x, int b) { atomicAdd(&bin[b], x.members); });
     __syncthreads();
     // where each bin begins
     const int mine = bin[tid];
@@ -76,9 +79,16 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
         p.ws.counters[1] = 0;
     }
     __syncthreads();
-    each(false, [&](const ExpandedItem& x, int b) {
-        const int at = atomicAdd(&bin[b], 1);
-        if (at < p.ws.max_items) p.ws.items[at] = x;
+    each(false, [&](ExpandedItem x, int b) {
+        x.group = atomicAdd(&bin[b], x.members);
+        // (rows that offsets out of order name twice may leave no room)
+        x.members = min(x.members, p.ws.max_items - x.group);
+        for (int i = 0; i < x.members; ++i) {
+            p.ws.items[x.group + i] = x;
+            x.keys -= x.rows;              // the unit in front of it
+            x.q0 -= p.rows;
+            x.rows = p.rows;
+        }
     });
 }
 
@@ -142,9 +152,9 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) expanded
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int unit = blockIdx.x / CTAS, rank = blockIdx.x % CTAS;
-    const int item = unit / p.heads, h = unit - item * p.heads;
-    if (item >= p.ws.counters[0]) return;
-    const ExpandedItem x = p.ws.items[item];
+    if (unit / p.heads >= p.ws.counters[0]) return;
+    int h;
+    const ExpandedItem x = expanded_unit(p.ws, unit, p.heads, h);
     const int keys = max(x.keys, 0);
 
     for (int i = threadIdx.x; i < kRows * (kDim / 4); i += THREADS) {
@@ -348,8 +358,9 @@ size_t layout(const pkv_expanded_desc* d, int32_t num_seqs, int32_t num_query_to
 }  // namespace
 
 int launch_expanded_plan(const ExpandedArgs& a, int rows) {
+    const int64_t units = int64_t(ceil_div(a.num_query_tokens, rows)) * a.desc->num_heads;
     PlanParams p{a.query_start_loc, a.key_start_loc, a.num_seqs, a.num_query_tokens, a.num_keys,
-                 a.max_query_len, rows, a.ws, a.err};
+                 a.max_query_len, rows, units >= 8 * int64_t(num_sms()) ? 4 : 1, a.ws, a.err};
     return cuda_status(launch_pdl(expanded_plan_kernel, dim3(1), dim3(1024), 0, a.stream, p));
 }
 

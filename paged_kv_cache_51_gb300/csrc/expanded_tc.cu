@@ -211,9 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok || *abort_flag) break;
                 Unit u = {};
                 if (next < units) {
-                    const int item = next / p.heads;
-                    const ExpandedItem x = p.ws.items[item];
-                    u = Unit{1, next - item * p.heads, x.q0, x.rows, x.k0, x.keys};
+                    const ExpandedItem x = expanded_unit(p.ws, next, p.heads, u.head);
+                    u = Unit{1, u.head, x.q0, x.rows, x.k0, x.keys};
                 }
                 sh.unit[n & 1] = u;
                 mbar_arrive(&bars[B_U_FULL + (n & 1)]);

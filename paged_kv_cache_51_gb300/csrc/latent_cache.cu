@@ -145,10 +145,7 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
     const int c = lane & 3;
     float co[8], si[8];
     if (task > 0) {
-        if (!pos_ok) {
-            if (task == 1 && lane == 0) flag_error(p.err, PKV_DEV_BAD_POSITION);
-            return;
-        }
+        // the values are asked for next to the position, before it is looked at
         Values<T> v[2];
         int h[2];
 #pragma unroll
@@ -156,6 +153,10 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
             h[u] = (task - 1) * kHeadsPerWarp + u * 8 + (lane >> 2);
             const T* src = static_cast<const T*>(p.q) + t * p.q_token + h[u] * p.q_head;
             if (h[u] < p.heads) v[u].load(src + run_a<kInter>(c), src + run_b<kInter>(c));
+        }
+        if (!pos_ok) {
+            if (task == 1 && lane == 0) flag_error(p.err, PKV_DEV_BAD_POSITION);
+            return;
         }
         load_angles(p.cos_sin, pos, c, co, si);
 #pragma unroll
@@ -168,22 +169,12 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
         return;
     }
     const int64_t slot = __ldg(p.slots + t);
-    if (slot < 0 || slot >= p.num_slots) {
-        if (slot >= 0 && lane == 0) flag_error(p.err, PKV_DEV_BAD_SLOT);
-        return;
-    }
-    if (!pos_ok) {
-        if (lane == 0) flag_error(p.err, PKV_DEV_BAD_POSITION);
-        return;
-    }
-    T* row = static_cast<T*>(p.cache) + slot * (p.latent_dim + kLatentRope);
     const T* src = static_cast<const T*>(p.latent) + t * p.latent_stride;
-    // the key's loads go out with the vector's
+    // the vector and the key are asked for before slot and position are looked at
     Values<T> key;
     if (lane < 4) {
         const T* k = static_cast<const T*>(p.k_rope) + t * p.k_stride;
         key.load(k + run_a<kInter>(c), k + run_b<kInter>(c));
-        load_angles(p.cos_sin, pos, c, co, si);
     }
     constexpr int kPer = 16 / sizeof(T);                   // values of a vector
     constexpr int kMost = 512 / kPer / 32;                 // vectors of a lane at most
@@ -197,6 +188,16 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
             if (p.weight) w[i] = __ldg(static_cast<const uint4*>(p.weight) + at);
         }
     }
+    if (slot < 0 || slot >= p.num_slots) {
+        if (slot >= 0 && lane == 0) flag_error(p.err, PKV_DEV_BAD_SLOT);
+        return;
+    }
+    if (!pos_ok) {
+        if (lane == 0) flag_error(p.err, PKV_DEV_BAD_POSITION);
+        return;
+    }
+    T* row = static_cast<T*>(p.cache) + slot * (p.latent_dim + kLatentRope);
+    if (lane < 4) load_angles(p.cos_sin, pos, c, co, si);
     if (p.weight) {
         auto get = [](const uint4& v, int e) {
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
