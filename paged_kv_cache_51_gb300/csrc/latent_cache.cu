@@ -130,9 +130,11 @@ constexpr int kHeadsPerWarp = 16;          // 4 lanes a row, two rows a lane
 
 // One warp a task.  Task 0 of a token is its cache row: the lanes hold the latent
 // vector, sum its squares by shuffles and write it, and lanes 0-3 rotate the key.
-// The other tasks rotate 16 query heads each, 4 lanes a head.
+// The other tasks rotate 16 query heads each, 4 lanes a head.  Bound by how many loads are on
+// their way: 40 warps an SM at 48 registers and CTAs of four of them took 31.2 us for 16384
+// tokens of 32 heads, 32 warps at 64 in CTAs of eight 33.9, 32 heads a warp 33.3, 8 heads 42.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
+__global__ void __launch_bounds__(128, sizeof(T) == 2 ? 10 : 6) latent_append_kernel(AppendParams p) {
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -404,7 +406,7 @@ extern "C" int paged_latent_append(const void* latent, int64_t latent_stride, co
     p.max_position = max_position;
     p.eps = eps;
     // one warp a CTA while that leaves SMs free: a decode step's chain is short
-    const int warps = p.warps <= 2 * int64_t(std::max(num_sms(), 1)) ? 1 : 8;
+    const int warps = p.warps <= 2 * int64_t(std::max(num_sms(), 1)) ? 1 : 4;
     const int64_t blocks = (p.warps + warps - 1) / warps;
     if (blocks > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     const bool inter = rope_layout == PKV_ROPE_INTERLEAVED;
