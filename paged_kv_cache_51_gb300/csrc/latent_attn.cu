@@ -58,6 +58,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;            // S buffers: 32 columns each behind O
 constexpr float kRescale = 8.f;            // log2 units: O is rescaled when a row's max grows by more
 constexpr int kLeastSteps = 4;             // a CTA takes at least 128 keys
+constexpr int kStart = 4;                  // steps that a unit costs beside its tiles
 
 enum {
     B_K_FULL = 0,                          // [tile buffer]
@@ -133,9 +134,9 @@ struct Params {
     bool whole_sectors;                    // out begins on 32 bytes
 };
 
-using Walk = LatentWalk<kRows, kKeys>;
+using Walk = LatentWalk<kRows, kKeys, kStart>;
 
-using Tiles = LatentTiles<kRows, kKeys>;
+using Tiles = LatentTiles<kRows, kKeys, kStart>;
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     tc_fence_before();
-    const Walk plan = latent_plan<kRows, kKeys, kThreads>(p.b, sh.sums, kLeastSteps, blockIdx.x, gridDim.x);
+    const Walk plan = latent_plan<kRows, kKeys, kStart, kThreads>(p.b, sh.sums, kLeastSteps, blockIdx.x, gridDim.x);
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 

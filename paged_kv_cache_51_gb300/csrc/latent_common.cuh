@@ -12,7 +12,11 @@
 // L2 holds read HBM twice).  A unit is (sequence, row tiles of a team); it costs one step
 // for each tile of KEYS keys of its context.  The steps of all units, one after the other,
 // are cut into as many equal stretches as there are teams, so every SM reads the same
-// number of keys whatever the lengths.  A stretch is a run of fragments; one that holds
+// number of keys whatever the lengths.  A unit also costs START steps in front of its tiles,
+// in which nothing is done: they stand for the time of its queries, its output and the gap
+// between two units, so that the stretches with several short units do not end last (64
+// requests of 512 to 4096 tokens, 32 heads: 46.9 us without, 45.1 with four; 99 of 43 to 398
+// tokens, 48 heads: 22.3 and 18.5).  A stretch is a run of fragments; one that holds
 // all keys of its unit writes the output, another one its partial state (max, sum, output)
 // to a slot of its CTA: only a CTA's first and last fragment can be partial, so there are
 // two slots a CTA and the workspace does not grow with the batch.  A merge kernel joins
@@ -20,6 +24,8 @@
 #pragma once
 
 #include <cuda.h>
+
+#include <algorithm>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -114,7 +120,7 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
     return (x >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(c)) : int64_t(x / uint64_t(c));
 }
 
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int START>
 struct LatentWalk {
     int s;
     int64_t off;                           // step within sequence s
@@ -129,7 +135,7 @@ struct LatentWalk {
     }
     __device__ static int64_t steps(const LatentBatch& b, const LatentSeq& x) {
         if (x.qlen == 0 || x.zero) return 0;
-        return int64_t(groups(b, x.qlen * b.heads)) * ((x.ctx + KEYS - 1) / KEYS);
+        return int64_t(groups(b, x.qlen * b.heads)) * ((x.ctx + KEYS - 1) / KEYS + START);
     }
     // the stretch of team t begins at step t * total / teams; the team of a step
     __device__ static int64_t start_of(int64_t t, int64_t total, int teams) { return mul_div(t, total, teams); }
@@ -140,25 +146,43 @@ struct LatentWalk {
     }
 
     __device__ bool next(const LatentBatch& b, LatentFrag& f) {
-        if (left <= 0) return false;
+        for (;;) {
+            if (left <= 0) return false;
+            if (step(b, f)) return true;
+        }
+    }
+    // one unit's part of the stretch; false if that lies in front of the unit's tiles
+    __device__ bool step(const LatentBatch& b, LatentFrag& f) {
         LatentSeq x = latent_seq<false>(b, s);
         while (steps(b, x) == 0) x = latent_seq<false>(b, ++s);
+        const int seq = s;
         const int rows = x.qlen * b.heads;
-        const int kt = (x.ctx + KEYS - 1) / KEYS;
-        const int group = int(off / kt);
-        f.kt0 = int(off - int64_t(group) * kt);
-        int n = kt - f.kt0;
+        const int kt = (x.ctx + KEYS - 1) / KEYS, len = kt + START;
+        const int group = int((off >> 32) == 0 ? uint32_t(off) / uint32_t(len) : off / len);
+        const int at = int(off - int64_t(group) * len);    // step of the unit
+        int n = len - at;
         if (n > left) n = int(left);
+        const int64_t last = pos + len - at - 1;           // the unit's last step
+        left -= n;
+        pos += n;
+        off += n;
+        if (off == int64_t(groups(b, rows)) * len) {
+            off = 0;
+            ++s;
+        }
+        const int end = at + n - START;
+        if (end <= 0) return false;
+        f.kt0 = max(0, at - START);
         const int r0 = (group * b.team + cta % b.team) * ROWS;
-        f.seq = s;
+        f.seq = seq;
         f.ctx = x.ctx;
         f.nrows = max(0, min(ROWS, rows - r0));
         f.row0 = x.q0 * b.heads + r0;
         f.t0 = r0 / b.heads;
         f.rest = r0 - f.t0 * b.heads;
         f.first_pos = x.ctx - x.qlen;
-        f.whole = f.kt0 == 0 && n == kt;
-        f.starts = f.kt0 == 0 && n < kt;
+        f.whole = f.kt0 == 0 && end == kt;
+        f.starts = f.kt0 == 0 && end < kt;
         f.slot = 2 * cta + (begun ? 1 : 0);
         f.last_cta = 0;
         f.n = 0;
@@ -168,18 +192,11 @@ struct LatentWalk {
         } else {
             const int last_tok = (r0 + f.nrows - 1) / b.heads;
             const int want = (f.first_pos + last_tok) / KEYS + 1;   // tiles that any row sees
-            f.n = max(0, min(f.kt0 + n, want) - f.kt0);
+            f.n = max(0, min(end, want) - f.kt0);
             if (f.starts)
-                f.last_cta = owner(pos + kt - 1, total, teams) * b.team + cta % b.team;
+                f.last_cta = owner(last, total, teams) * b.team + cta % b.team;
         }
         begun = true;
-        left -= n;
-        pos += n;
-        off += n;
-        if (off == int64_t(groups(b, rows)) * kt) {
-            off = 0;
-            ++s;
-        }
         return true;
     }
 };
@@ -188,10 +205,10 @@ struct LatentWalk {
 // its stretch begins in: threads 0 .. T-1 take runs of sequences, `sums` is shared
 // memory for T / 32 + 2 values.  Steps fewer than `least` a team go to fewer teams.
 // (All T threads call it; CTA 0 flags bad lengths.)
-template <int ROWS, int KEYS, int T>
-__device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch& b, int64_t* sums,
+template <int ROWS, int KEYS, int START, int T>
+__device__ __forceinline__ LatentWalk<ROWS, KEYS, START> latent_plan(const LatentBatch& b, int64_t* sums,
                                                              int least, int cta, int ctas) {
-    using Walk = LatentWalk<ROWS, KEYS>;
+    using Walk = LatentWalk<ROWS, KEYS, START>;
     constexpr int kWarps = T / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (b.num_seqs + T - 1) / T;
@@ -245,22 +262,24 @@ __device__ __forceinline__ LatentWalk<ROWS, KEYS> latent_plan(const LatentBatch&
 inline int64_t latent_rows(const LatentBatch& b) {
     return int64_t(ceil_div(b.num_query_tokens, b.num_seqs)) * b.heads;
 }
-// CTAs of a team: the row tiles of a sequence, on average; at most 8 (152 CTAs make whole
-// teams of most sizes up to there, and L2 holds what lies between two members)
+// CTAs (or pairs) of a team: all row tiles of a sequence, on average, up to 8 of them; of more
+// tiles two, since a team's last tiles then seldom have members without rows (41 requests of 28
+// tiles: 185 us with two, 196 with eight; keys read by one CTA after the other, without teams:
+// 64 requests of two tiles over 2k to 8k tokens 173 us against 160)
 inline int latent_team(const LatentBatch& b, int rows) {
-    const int64_t of = latent_rows(b);
-    return int(of <= rows ? 1 : of >= 8 * int64_t(rows) ? 8 : (of + rows - 1) / rows);
+    const int64_t tiles = std::max<int64_t>(1, (latent_rows(b) + rows - 1) / rows);
+    return tiles <= 8 ? int(tiles) : 2;
 }
 
 // The fragments' tiles one after the other, skipping fragments without any.
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int START>
 struct LatentTiles {
-    LatentWalk<ROWS, KEYS> w;
+    LatentWalk<ROWS, KEYS, START> w;
     LatentFrag f;
     int j;                                 // tile of the fragment
     uint32_t g, k;                         // tiles and fragments (of any tiles) so far
     bool live;
-    __device__ void start(const LatentBatch& b, const LatentWalk<ROWS, KEYS>& from) {
+    __device__ void start(const LatentBatch& b, const LatentWalk<ROWS, KEYS, START>& from) {
         w = from;
         g = k = 0;
         live = false;

@@ -28,6 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLeastSteps = 2;
+constexpr int kStart = 1;                  // steps that a unit costs beside its tiles
 
 struct Params {
     LatentBatch b;
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
 
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    LatentWalk<ROWS, KEYS> w = latent_plan<ROWS, KEYS, kThreads>(p.b, sums, kLeastSteps, blockIdx.x, gridDim.x);
+    LatentWalk<ROWS, KEYS, kStart> w = latent_plan<ROWS, KEYS, kStart, kThreads>(p.b, sums, kLeastSteps, blockIdx.x, gridDim.x);
     if (tid == 0) p.ws.merge[blockIdx.x].nrows = 0;
     // sequences with lengths that the call does not allow: zeros
     for (int s = blockIdx.x; s < p.b.num_seqs; s += gridDim.x) {

@@ -45,6 +45,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;            // S buffers: 64 columns each behind O
 constexpr float kRescale = 8.f;            // log2 units
 constexpr int kLeastSteps = 1;
+constexpr int kStart = 2;                  // steps that a unit costs beside its tiles
 constexpr int kSmemMost = 232448;
 
 constexpr int kKCols = 3;                  // 64-value columns of a chunk of keys
@@ -87,8 +88,8 @@ struct Params {
     bool whole_sectors;
 };
 
-using Walk = LatentWalk<kRows, kKeys>;
-using Tiles = LatentTiles<kRows, kKeys>;
+using Walk = LatentWalk<kRows, kKeys, kStart>;
+using Tiles = LatentTiles<kRows, kKeys, kStart>;
 
 // ---- the pair ------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -203,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     tc_fence_before();
-    const Walk plan = latent_plan<kRows, kKeys, kThreads>(p.b, sh.sums, kLeastSteps, pair, int(gridDim.x) / 2);
+    const Walk plan = latent_plan<kRows, kKeys, kStart, kThreads>(p.b, sh.sums, kLeastSteps, pair, int(gridDim.x) / 2);
     pair_sync();                                          // the other CTA's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
