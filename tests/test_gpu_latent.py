@@ -581,3 +581,16 @@ def test_binding_refuses_on_the_gpu(pkv):
                                 pos.expand(2).contiguous(), tab, c, desc)
     torch.cuda.synchronize()
     assert pkv.device_error() == 0
+
+
+def test_single_precision_units_of_32_rows_cut_over_ctas(pkv):
+    """72 rows a sequence of the longest vectors, a context that many CTAs share."""
+    rng = np.random.default_rng(23)
+    ctx, start = [2500, 19, 3], [0, 2, 3, 4]
+    cache, t = batch(rng, "f32", 512, ctx)
+    q = values(rng, (4, 36, 576), "f32")
+    args = (q, cache, t, start, ctx, SCALE, "f32")
+    ref = latent.absorbed(*args)
+    out, code = attend(pkv, q, cache, t, ctx, "f32", start)
+    assert code == 0
+    assert_close(out, ref, absorbed_bound(*args, ref))
