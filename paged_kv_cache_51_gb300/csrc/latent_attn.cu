@@ -57,7 +57,7 @@ constexpr int kMostSlots = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;            // S buffers: 32 columns each behind O
 constexpr float kRescale = 8.f;            // log2 units: O is rescaled when a row's max grows by more
-constexpr int kLeastSteps = 4;             // a CTA takes at least 128 keys
+constexpr int kLeastSteps = 4;             // of a CTA
 constexpr int kStart = 4;                  // steps that a unit costs beside its tiles
 
 enum {

@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kLeastSteps = 2;
+constexpr int kLeastSteps = 1;             // of a CTA (one request of 8000 keys, 8 heads: 18.4 us, with two 21.4)
 constexpr int kStart = 1;                  // steps that a unit costs beside its tiles
 
 struct Params {
