@@ -93,14 +93,16 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(PlanParams p) {
 }
 
 // ---- single precision -------------------------------------------------------------
-// A CTA takes 64 query rows of one head and tiles of 64 keys; a thread keeps a 4 x 4 part
-// of the scores and 4 rows x D / 16 values of the output in registers.  Bound by the FMA
-// rate with shared memory close behind (8 reads of 16 bytes for 64 FMAs).  Where units of
-// 64 rows would not give every SM two, they have 32, of half as many threads, and a cluster
-// of four CTAs takes turns at the tiles of the keys and meets at the end: the tiles of a unit
-// follow one another, and six prompts of up to 300 tokens with 4 heads took 52 us with one CTA
-// a unit and take 25 with four.  P lies over the keys that it was made of, so that three such
-// CTAs (heads of 128: two) fit on an SM.
+// A CTA takes 64 or 128 query rows of one head and tiles of 64 keys; a thread keeps RI x 4
+// scores and RI rows x D / 16 values of the output in registers.  Bound by what shared memory
+// returns: a read of 16 bytes a lane costs a warp four cycles, the time of 16 FMAs, and there
+// are RI + 4 of them for 16 RI.  Eight rows a thread (two prompts of 1000 to 1500 tokens, 16
+// heads of 64: 294 us, 311 with four) leave a CTA of 64 rows four warps, too few where it is
+// alone on its SM (D = 128).  Where units of 64 rows would not give every SM two, they have 32
+// and a cluster of four CTAs takes turns at the tiles of the keys and meets at the end: the
+// tiles of a unit follow one another, and six prompts of up to 300 tokens with 4 heads took 52
+// us with one CTA a unit and take 25 with four.  P lies over the keys that it was made of, so
+// that three such CTAs (heads of 128: two) fit on an SM.
 struct F32Params {
     ExpandedWorkspace ws;
     const float *q, *k, *v, *k_rope;
@@ -113,9 +115,9 @@ struct F32Params {
 constexpr int kT = 64;                     // keys of a tile
 constexpr int kPPitch = kT + 4;
 
-template <int D, int THREADS>
+template <int D, int ROWS>
 constexpr int f32_smem_floats() {
-    return (THREADS / 4 + kT) * (D + kExpandedRope + 4) + kT * (D + 4);
+    return (ROWS + kT) * (D + kExpandedRope + 4) + kT * (D + 4);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -136,10 +138,10 @@ __device__ __forceinline__ float load_cluster(const float* at, int rank) {
     return v;
 }
 
-// A unit has THREADS / 4 rows; the CTAS of a cluster share one.
-template <int D, int THREADS, int CTAS>
+// RI: rows of a thread; a unit has THREADS / 16 as many.  CTAS of a cluster share a unit.
+template <int D, int THREADS, int RI, int CTAS>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) expanded_f32_kernel(F32Params p) {
-    constexpr int RI = 4, kTy = THREADS / 16, kRows = kTy * RI;
+    constexpr int kTy = THREADS / 16, kRows = kTy * RI;
     constexpr int kDim = D + kExpandedRope, kPitch = kDim + 4, kVPitch = D + 4;
     constexpr int kCols = D / 16;          // output values of a thread in a row
     static_assert(kRows * kPPitch <= kT * kPitch, "P lies over the keys");
@@ -316,17 +318,17 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) expanded
     }
 }
 
-template <int D, int THREADS, int CTAS>
+template <int D, int THREADS, int RI, int CTAS>
 int launch_f32(const ExpandedArgs& a, const F32Params& p) {
-    constexpr int smem = f32_smem_floats<D, THREADS>() * int(sizeof(float)), rows = THREADS / 4;
+    constexpr int rows = THREADS / 16 * RI, smem = f32_smem_floats<D, rows>() * int(sizeof(float));
     static_assert(smem <= 232448, "shared memory");
     const int st = launch_expanded_plan(a, rows);
     if (st != PKV_OK) return st;
-    if (kernel_occupancy<expanded_f32_kernel<D, THREADS, CTAS>>(THREADS, smem) < 1) return PKV_ERR_CUDA;
+    if (kernel_occupancy<expanded_f32_kernel<D, THREADS, RI, CTAS>>(THREADS, smem) < 1) return PKV_ERR_CUDA;
     const int64_t items = std::min<int64_t>(a.ws.max_items, ceil_div(a.num_query_tokens, rows) + int64_t(a.num_seqs));
     const int64_t grid = items * a.desc->num_heads * CTAS;
     if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    return cuda_status(launch_pdl(expanded_f32_kernel<D, THREADS, CTAS>, dim3(unsigned(grid)), dim3(THREADS),
+    return cuda_status(launch_pdl(expanded_f32_kernel<D, THREADS, RI, CTAS>, dim3(unsigned(grid)), dim3(THREADS),
                                   size_t(smem), a.stream, p));
 }
 
@@ -377,10 +379,15 @@ int launch_expanded_f32(const ExpandedArgs& a) {
                 a.desc->v_head_stride,
                 a.desc->num_heads,
                 float(double(a.scale) * 1.4426950408889634)};
+    const bool wide = a.desc->head_dim == 128;
     const int64_t units = int64_t(a.num_query_tokens) * a.desc->num_heads / 64;
-    if (units >= 2 * std::max(num_sms(), 1))
-        return a.desc->head_dim == 128 ? launch_f32<128, 256, 1>(a, p) : launch_f32<64, 256, 1>(a, p);
-    return a.desc->head_dim == 128 ? launch_f32<128, 128, 4>(a, p) : launch_f32<64, 128, 4>(a, p);
+    if (units < 2 * std::max(num_sms(), 1))
+        return wide ? launch_f32<128, 128, 4, 4>(a, p) : launch_f32<64, 128, 4, 4>(a, p);
+    if (!wide) return launch_f32<64, 128, 8, 1>(a, p);
+    // (two prompts of 1000 to 1500 tokens, 16 heads: 554 us with 64 rows, 484 with 128; six of up
+    // to 300, 32 heads: 172 and 199)
+    return ceil_div(a.num_query_tokens, a.num_seqs) >= 512 ? launch_f32<128, 256, 8, 1>(a, p)
+                                                           : launch_f32<128, 256, 4, 1>(a, p);
 }
 
 }  // namespace pkv

@@ -41,7 +41,7 @@ struct ExpandedArgs {
 };
 
 constexpr int kExpandedRope = 64;
-constexpr int kExpandedRowsF32 = 32;       // query rows of a unit (fp32: 32 or 64)
+constexpr int kExpandedRowsF32 = 32;       // query rows of a unit (fp32: 32, 64 or 128)
 constexpr int kExpandedRowsBf16 = 256;
 
 #ifdef __CUDACC__

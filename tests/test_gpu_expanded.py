@@ -103,6 +103,12 @@ def test_single_precision_with_units_for_every_sm(pkv, d):
     Case(np.random.default_rng(d), "f32", 110, d, [180, 1], [200, 90]).check(pkv)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_precision_long_prompts(pkv, d):
+    """Prompts of 512 tokens and more on average, a unit that ends inside its rows."""
+    Case(np.random.default_rng(d), "f32", 20, d, [530, 500], [560, 500]).check(pkv)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("new,keys", [([10], [4]), ([300, 7], [20, 0]), ([3, 260, 2], [0, 131, 2]),
