@@ -21,13 +21,19 @@ namespace pkv {
 namespace {
 
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBatch = 4;             // states in flight a warp
-constexpr int kMergeCtas = 3;              // of an SM
+// states in flight a warp and CTAs of an SM: many warps of few states where there are many
+// short lists (bf16, 96 requests with 128 heads, the whole call: 125.1 us with 2 and 4, 126.2
+// with 4 and 3, 130.5 with 2 and 6), few of many in single precision's small calls (17.5 and 18)
+template <typename T>
+constexpr int kMergeBatch = sizeof(T) == 4 ? 4 : 2;
+template <typename T>
+constexpr int kMergeCtas = sizeof(T) == 4 ? 3 : 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kMergeThreads, kMergeCtas)
+__global__ void __launch_bounds__(kMergeThreads, kMergeCtas<T>)
     latent_merge_kernel(LatentBatch b, LatentWorkspace ws, T* out, int ctas, int half0) {
     constexpr bool kWide = sizeof(T) == 4;
+    constexpr int kBatch = kMergeBatch<T>;
     __shared__ LatentMerge list[kMergeThreads];
     __shared__ int counts[kMergeWarps], tallest;
     __shared__ float shared[kMergeWarps][10][32];
@@ -86,30 +92,30 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas)
             constexpr int kSecond = kWide ? 128 : 512;
             float acc[8] = {}, sum = 0.f, big = -INFINITY;
             const int n = (m.last - m.first) / team + 1;
-            for (int c0 = mine; live && c0 < n; c0 += kMergeBatch * share) {
-                float2 ml[kMergeBatch];
-                float4 o[kMergeBatch][2];
+            for (int c0 = mine; live && c0 < n; c0 += kBatch * share) {
+                float2 ml[kBatch];
+                float4 o[kBatch][2];
 #pragma unroll
-                for (int i = 0; i < kMergeBatch; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     const int c = c0 + i * share, slot = c == 0 ? m.first_slot : 2 * (m.first + c * team);
                     ml[i] = make_float2(-INFINITY, 0.f);
                     o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (c < n) {
                         ml[i] = ws.ml[slot * kLatentRowTile + r];
-                        o[i][0] = *reinterpret_cast<const float4*>(o0 + slot * stride);
-                        if (second) o[i][1] = *reinterpret_cast<const float4*>(o0 + slot * stride + kSecond);
+                        o[i][0] = __ldcg(reinterpret_cast<const float4*>(o0 + slot * stride));
+                        if (second) o[i][1] = __ldcg(reinterpret_cast<const float4*>(o0 + slot * stride + kSecond));
                     }
                 }
                 float top = big;
 #pragma unroll
-                for (int i = 0; i < kMergeBatch; ++i) top = fmaxf(top, ml[i].x);
+                for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
                 const float a = top == -INFINITY ? 1.f : exp2f(big - top);
                 big = top;
                 sum *= a;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] *= a;
 #pragma unroll
-                for (int i = 0; i < kMergeBatch; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     if (!(ml[i].y != 0.f)) continue;      // no visible keys: nothing was written
                     const float w = exp2f(ml[i].x - big);
                     sum += w * ml[i].y;
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas)
 template <typename T>
 int launch_latent_merge(cudaStream_t stream, const LatentBatch& b, const LatentWorkspace& ws, T* out, int ctas,
                         int half0) {
-    return cuda_status(launch_pdl(latent_merge_kernel<T>, dim3(kMergeCtas * num_sms()), dim3(kMergeThreads), 0,
+    return cuda_status(launch_pdl(latent_merge_kernel<T>, dim3(kMergeCtas<T> * num_sms()), dim3(kMergeThreads), 0,
                                   stream, b, ws, out, ctas, half0));
 }
 
