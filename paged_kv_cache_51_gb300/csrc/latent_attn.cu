@@ -7,7 +7,8 @@
 // staged once in shared memory and is both operands: K-major for the first product,
 // and, through another descriptor over the same bytes, MN-major for the second.
 //
-// Shapes.  A CTA takes 64 (token, head) rows of one sequence and tiles of 32 keys.
+// Shapes.  A CTA takes 64 (token, head) rows of one sequence and tiles of 32 keys (batches of
+// more rows a sequence go to pairs of CTAs, latent_pair.cu).
 // Products of this size are bound by the shared memory they read (128 bytes a cycle;
 // measured, in cycles: 64 x 32 x 16 takes 24, 64 x 64 x 16 32, 64 x 256 x 16 80 in the .ws
 // form, which spreads the halves of the columns over all 128 TMEM lanes, and 128 in the

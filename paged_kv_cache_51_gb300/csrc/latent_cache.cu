@@ -478,8 +478,8 @@ extern "C" int paged_attention_latent(void* out, const void* q, const void* late
         !(scale > 0.f && std::isfinite(scale)) || (!query_start_loc && num_query_tokens != num_seqs))
         return PKV_ERR_INVALID;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
-    // rows of q are counted in 32 bits
-    if (int64_t(num_query_tokens) * desc->num_q_heads >= (int64_t(1) << 31) - 64) return PKV_ERR_UNSUPPORTED;
+    // rows of q are counted in 32 bits, with up to 8 tiles of 128 behind the last
+    if (int64_t(num_query_tokens) * desc->num_q_heads >= (int64_t(1) << 31) - 2048) return PKV_ERR_UNSUPPORTED;
     if (!out || !q || !latent_cache || !block_tables || !context_lens || !aligned(out, 16) ||
         !aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4) || !aligned(query_start_loc, 4))

@@ -50,7 +50,7 @@ constexpr int kSmemMost = 232448;
 
 constexpr int kKCols = 3;                  // 64-value columns of a chunk of keys
 constexpr int kVKeys = 32;                 // keys of a chunk of values
-constexpr int kMostK = 6, kMostV = 8;      // chunks
+constexpr int kMostK = 4, kMostV = 8;      // chunks
 
 enum {
     B_K_FULL = 0,                          // [key chunk]       (first CTA)
@@ -622,7 +622,7 @@ int launch_latent_pair(const LatentArgs& a) {
     static_assert(1024 + sizeof(Smem) + kPBytes + 9 * 8192 + 3 * kchunk + 4 * 16384 <= kSmemMost, "shared memory");
     // two tiles where they fit; at the longest latent vectors one
     const int chunks = (cols + kKCols - 1) / kKCols;
-    p.k_slots = fixed + 2 * chunks * kchunk + 4 * vchunk <= kSmemMost ? std::min(kMostK, 2 * chunks) : chunks;
+    p.k_slots = fixed + 2 * chunks * kchunk + 4 * vchunk <= kSmemMost ? 2 * chunks : chunks;
     p.v_slots = std::min(kMostV, (kSmemMost - fixed - p.k_slots * kchunk) / vchunk);
     const int smem = fixed + p.k_slots * kchunk + p.v_slots * vchunk;
     if (kernel_occupancy<latent_pair_kernel>(kThreads, kSmemMost) < 1) return PKV_ERR_CUDA;
