@@ -19,7 +19,11 @@
 // their use: 3 slots of a key tile (64 dimensions each), 2 of a value tile (64 keys each);
 // 8 slots are 1.6 tiles, where a ring each for keys and values would have held 1.3 and 2.
 //
-// Units come longest first from a ticket.
+// Units come longest first from a ticket.  Where there are so few that four or two CTAs for
+// each find SMs, a cluster shares one: every CTA takes its part of the key tiles, and they
+// meet through one another's shared memory at the end (one head of 16 queries over 16k keys
+// took 180 us with one CTA and takes 52 with four, 8 heads over 4k 51 and 19; two sequences
+// of 256 queries over 3256 keys, 16 heads, 55 and 37 with two).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -65,6 +69,7 @@ constexpr int kUnitReaders = 1 + 8;        // issuer, softmax warps
 struct Unit {
     int32_t live;                          // 0: no more work
     int32_t head, q0, rows, k0, keys;
+    int32_t most;                          // key tiles at most (a cluster's CTA: its share)
 };
 
 struct Smem {                              // behind the operands
@@ -101,7 +106,7 @@ __device__ __forceinline__ int tiles_of(const Unit& u, int x) {
     const int rows = min(kT, u.rows - x * kT);
     if (rows <= 0) return 0;
     const int keys = u.keys - u.rows + x * kT + rows;
-    return keys <= 0 ? 0 : (keys + kT - 1) / kT;
+    return keys <= 0 ? 0 : min(u.most, (keys + kT - 1) / kT);
 }
 
 // four K = 16 steps over one 64-value column of both operands
@@ -145,8 +150,38 @@ __device__ __forceinline__ bool read_unit(Smem& sh, uint32_t n, int* err, Unit& 
     return true;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float load_cluster(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+// The parts of a cluster's unit, in shared memory where queries and ring were: O of 256 rows,
+// then their maxima and sums.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+struct Parts {
+    float o[2 * kT][D + 4];
+    float m[2 * kT], l[2 * kT];
+};
+
+template <int D, int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     expanded_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v,
                     Params p) {
@@ -190,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp && lane == 0) {
             const int units = p.ws.counters[0] * p.heads;
-            int next = blockIdx.x;
+            int next = blockIdx.x / CTAS;
             uint32_t tile = 0, box = 0;                    // tiles and boxes so far
             uint32_t used[2] = {0, 0};                     // units with tiles of each stream
             bool ok = true;
@@ -212,12 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Unit u = {};
                 if (next < units) {
                     const ExpandedItem x = expanded_unit(p.ws, next, p.heads, u.head);
-                    u = Unit{1, u.head, x.q0, x.rows, x.k0, x.keys};
+                    u = Unit{1, u.head, x.q0, x.rows, x.k0, x.keys, INT32_MAX};
+                    if (CTAS > 1) {
+                        u.most = ((max(x.keys, 0) + kT - 1) / kT + CTAS - 1) / CTAS;
+                        const int skip = int(blockIdx.x % CTAS) * u.most * kT;
+                        u.k0 += skip;
+                        u.keys -= skip;
+                    }
                 }
                 sh.unit[n & 1] = u;
                 mbar_arrive(&bars[B_U_FULL + (n & 1)]);
                 if (!u.live) break;
-                next = int(gridDim.x) + atomicAdd(p.ws.counters + 1, 1);
+                next = CTAS > 1 ? units : int(gridDim.x) + atomicAdd(p.ws.counters + 1, 1);
                 const int tiles[2] = {tiles_of(u, 0), tiles_of(u, 1)};
                 const int most = max(tiles[0], tiles[1]);
                 auto load_q = [&](int x) {
@@ -342,6 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&bars[B_DRAIN], 0, err);
         }
         __syncwarp();
+        if (CTAS > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int x = warp >> 2;                           // stream
@@ -350,6 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_at = tmem + lanes + x * kT, o_at = tmem + lanes + kOCol + x * kT;
         uint32_t tile = 0, slot0 = 0, steps = 0, used = 0;
         bool ok = true;
+        Parts<D>& parts = *reinterpret_cast<Parts<D>*>(smem);
+        static_assert(sizeof(Parts<D>) <= S::kRing + S::kSlots * kBox, "shared memory");
+        Unit whole = {};                                   // (a cluster's)
+        float last_m = -INFINITY, last_l = 0.f;
         for (uint32_t n = 0;; ++n) {
             Unit u;
             ok = __all_sync(0xffffffffu, read_unit(sh, n, err, u));
@@ -457,6 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                      ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
             }
             if (!ok) break;
+            if (CTAS > 1) {                                // the only one
+                whole = u;
+                last_m = m;
+                last_l = l;
+                used = mine;
+                continue;
+            }
             __nv_bfloat16* dst = p.out + ((int64_t(u.q0) + row) * p.heads + u.head) * D;
             if (mine > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_O_FULL + x], used & 1, err));
@@ -493,6 +549,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             slot0 = (slot0 + uint32_t(most) * S::kBoxes) % S::kSlots;
         }
         if (!ok) *abort_flag = 1;
+        if (CTAS > 1) {
+            // once all products are complete, queries and ring are free
+            const int row = x * kT + r;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[B_DRAIN], 0, err)) && ok;
+            tc_fence_after();
+            if (used > 0) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    tc_ld32(o_at + c, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(&parts.o[row][c + 4 * i]) =
+                            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            parts.m[row] = last_m;
+            parts.l[row] = last_l;
+            cluster_sync();
+            // a warp a row, every CTAS-th row each
+            const int rank = blockIdx.x % CTAS;
+            for (int y = rank + CTAS * warp; y < whole.rows && ok; y += CTAS * 8) {
+                float pm[CTAS], pl[CTAS], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int q = 0; q < CTAS; ++q) {
+                    pm[q] = load_cluster(in_cta(&parts.m[y], q));
+                    pl[q] = load_cluster(in_cta(&parts.l[y], q));
+                }
+#pragma unroll
+                for (int q = 0; q < CTAS; ++q) top = fmaxf(top, pm[q]);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < CTAS; ++q) {
+                    if (!(pl[q] != 0.f)) continue;         // saw no key: nothing was written
+                    const float4 v = lane < D / 4 ? load_cluster4(in_cta(&parts.o[y][lane * 4], q)) : acc;
+                    const float w = exp2f(pm[q] - top);
+                    sum += w * pl[q];
+                    acc.x += w * v.x;
+                    acc.y += w * v.y;
+                    acc.z += w * v.z;
+                    acc.w += w * v.w;
+                }
+                const float inv = sum != 0.f ? 1.f / sum : 0.f;    // a query without keys: zeros
+                if (lane < D / 4)
+                    *reinterpret_cast<uint2*>(p.out + ((int64_t(whole.q0) + y) * p.heads + whole.head) * D + lane * 4) =
+                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            }
+            __syncwarp();
+            cluster_sync();                                // nobody leaves while its parts are being read
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -502,7 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
 }
 
-template <int D>
+// units of a batch whose rows belong to one sequence each: ceil(q / 256) <= 1 + (q - 1) / 256
+int64_t fewest_units(const ExpandedArgs& a) {
+    const int64_t items = a.num_seqs + int64_t(std::max(0, a.num_query_tokens - a.num_seqs)) / kExpandedRowsBf16;
+    return std::min<int64_t>(items, a.ws.max_items) * a.desc->num_heads;
+}
+
+template <int D, int CTAS>
 int launch(const ExpandedArgs& a) {
     const pkv_expanded_desc* d = a.desc;
     const int H = d->num_heads, dim = D + kExpandedRope;
@@ -522,18 +635,25 @@ int launch(const ExpandedArgs& a) {
     if (st != PKV_OK) return st;
     Params p{a.ws, static_cast<__nv_bfloat16*>(a.out), H, (reinterpret_cast<uintptr_t>(a.out) & 31) == 0,
              float(double(a.scale) * 1.4426950408889634), a.err};
-    if (kernel_occupancy<expanded_kernel<D>>(kThreads, Shape<D>::kSmem) < 1) return PKV_ERR_CUDA;
-    const int64_t units = int64_t(a.ws.max_items) * H;
+    if (kernel_occupancy<expanded_kernel<D, CTAS>>(kThreads, Shape<D>::kSmem) < 1) return PKV_ERR_CUDA;
+    const int64_t units = CTAS > 1 ? fewest_units(a) : int64_t(a.ws.max_items) * H;
     if (units > INT32_MAX - 1024) return PKV_ERR_UNSUPPORTED;
-    const int64_t grid = std::min<int64_t>(num_sms(), units);
-    return cuda_status(launch_pdl(expanded_kernel<D>, dim3(unsigned(grid)), dim3(kThreads),
+    const int64_t grid = CTAS > 1 ? CTAS * units : std::min<int64_t>(num_sms(), units);
+    return cuda_status(launch_pdl(expanded_kernel<D, CTAS>, dim3(unsigned(grid)), dim3(kThreads),
                                   size_t(Shape<D>::kSmem), a.stream, mq, mk, mr, mv, p));
 }
 
 }  // namespace
 
 int launch_expanded_bf16(const ExpandedArgs& a) {
-    return a.desc->head_dim == 128 ? launch<128>(a) : launch<64>(a);
+    // a cluster for a unit where all find SMs and the keys are tiles enough to share (one head
+    // set of 30 units over 556 keys: 18 us by two CTAs, 15 by one)
+    const bool wide = a.desc->head_dim == 128;
+    if (a.num_keys >= 1024 * int64_t(a.num_seqs)) {
+        if (4 * fewest_units(a) <= num_sms()) return wide ? launch<128, 4>(a) : launch<64, 4>(a);
+        if (2 * fewest_units(a) <= num_sms()) return wide ? launch<128, 2>(a) : launch<64, 2>(a);
+    }
+    return wide ? launch<128, 1>(a) : launch<64, 1>(a);
 }
 
 }  // namespace pkv

@@ -98,6 +98,24 @@ def test_longer_prompts_and_chunks(pkv, dtype, d, h, new, keys):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,new,keys", [
+    (1, [1], [1100]),
+    (3, [16], [2000]),                            # a CTA of each cluster without tiles of its own
+    (2, [300, 5, 0, 129], [2500, 613, 600, 640]),
+    (1, [1300], [1200]),                          # queries that see no key
+    (9, [1, 1, 1, 40], [4100, 1, 2, 41]),         # units without keys for every CTA
+    (25, [300], [1030]),                          # by two CTAs
+    (1, [1025], [1025]),
+])
+def test_few_units_share_a_cluster(pkv, d, h, new, keys):
+    """So few units that four CTAs take the keys of each, twice the same."""
+    c = Case(np.random.default_rng(h + d), "bf16", h, d, new, keys)
+    out = c.check(pkv)
+    again, _ = c.run(pkv, ws_byte=0x11)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_single_precision_with_units_for_every_sm(pkv, d):
     """So many rows that a CTA takes 64 of them alone (fewer are shared by a cluster)."""
     Case(np.random.default_rng(d), "f32", 110, d, [180, 1], [200, 90]).check(pkv)
