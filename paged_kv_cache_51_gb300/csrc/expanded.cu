@@ -198,7 +198,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) expanded
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
         float s[RI][4] = {};
-#pragma unroll 2
+#pragma unroll 4
         for (int c = 0; c < kDim / 4; ++c) {
             float4 a[RI], b[4];
 #pragma unroll
@@ -243,7 +243,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) expanded
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < kT; k += 4) {
             float4 e[RI];
 #pragma unroll

@@ -30,6 +30,10 @@
 // Warps: 0 loads (queries, tiles), 1 issues S, 2 P C, 3 zeroes the rows of sequences that
 // the call does not allow, 4-7 are the softmax.  (One thread that issued both took 1727
 // cycles a tile, 450 of them its own waits and bookkeeping between the two.)
+//
+// Measured, with the merge: 4 requests of 32k tokens, 64 heads, 42 us; 64 of 512 to 4096, 32
+// heads, 44 us.  The tiles run at HBM's rate, 1650 cycles each; a start of 5 us, outputs of
+// 2.5 and the merge of 6 are the rest.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -21,6 +21,10 @@
 // first CTA issue S and P C for both.  Loads count on the first CTA's barriers, which expect
 // both CTAs' bytes (always whole chunks of keys: rows behind the context are read from some
 // block and masked in S); a product's completion arrives in both CTAs.
+//
+// Measured: 96 requests of 1k to 8k tokens, latent 512, 128 heads: 126 us with the merge (4.3
+// TB/s, 980 TFLOP/s); a step takes 4150 cycles, what L2 delivers to an SM 2570 of them and
+// chunks that are 3000 on their way the rest.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
