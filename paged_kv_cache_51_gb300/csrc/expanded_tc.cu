@@ -18,6 +18,10 @@
 // (D = 128: 96 KB) and a ring of 16 KB slots that takes keys and values in the order of
 // their use: 3 slots of a key tile (64 dimensions each), 2 of a value tile (64 keys each);
 // 8 slots are 1.6 tiles, where a ring each for keys and values would have held 1.3 and 2.
+// A slot is given back on its own, the first half of the values before the second (chunks:
+// 91.5 us where all of a tile's values came back together, 87.5).  Landing is told by the
+// tile: a wait for each slot costs the issuer more than it gains where units are short (50
+// prompts of up to 976 tokens, 26 heads: 223 us against 182).
 //
 // Units come longest first from a ticket.  Where there are so few that four or two CTAs for
 // each find SMs, a cluster shares one: every CTA takes its part of the key tiles, and they
@@ -26,7 +30,7 @@
 // of 256 queries over 3256 keys, 16 heads, 55 and 37 with two).
 //
 // Measured, D = 128, 32 heads: 8 prompts of 1700 to 4096 tokens 540 us (1350 TFLOP/s, at the
-// power limit), 4 chunks of about 450 over 512 to 3584 cached 83 to 93 us.  A tile of both
+// power limit), 4 chunks of about 450 over 512 to 3584 cached 83 to 88 us.  A tile of both
 // streams takes 3350 to 3600 cycles, of which products 2560: a stream's softmax (1500 to 1600)
 // and its products (1280) cannot overlap, since S and P share their columns.
 #include <cuda.h>
@@ -53,12 +57,13 @@ constexpr float kRescale = 8.f;            // log2 units: O is rescaled when a r
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "register split");
 
+constexpr int kMostSlots = 8;
+
 enum {
     B_K_FULL = 0,                          // [tile parity]
-    B_K_EMPTY = B_K_FULL + 2,
-    B_V_FULL = B_K_EMPTY + 2,
-    B_V_EMPTY = B_V_FULL + 2,
-    B_Q_FULL = B_V_EMPTY + 2,              // [stream]
+    B_V_FULL = B_K_FULL + 2,
+    B_EMPTY = B_V_FULL + 2,                // [slot]: its products are complete
+    B_Q_FULL = B_EMPTY + kMostSlots,                // [stream]
     B_Q_EMPTY = B_Q_FULL + 2,              // the unit's last S of the stream is complete
     B_S_FULL = B_Q_EMPTY + 2,
     B_P_FULL = B_S_FULL + 2,               // [stream][half of the keys]
@@ -237,9 +242,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
             // the slot of the next box, once the box that it held is done with
             auto slot = [&](uint32_t& dst) {
                 if (box >= uint32_t(S::kSlots)) {
-                    const uint32_t old = box - S::kSlots, t = old / S::kBoxes;
-                    const int bar = old % S::kBoxes < uint32_t(S::kKBoxes) ? B_K_EMPTY : B_V_EMPTY;
-                    ok = ok && mbar_wait(&bars[bar + (t & 1)], (t >> 1) & 1, err);
+                    ok = ok && mbar_wait(&bars[B_EMPTY + box % S::kSlots], (box / S::kSlots - 1) & 1, err);
                 }
                 dst = base + S::kRing + (box % S::kSlots) * kBox;
                 ++box;
@@ -340,7 +343,10 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_commit(&bars[B_S_FULL + x]);
                     if (j == tiles[x] - 1) tc_commit(&bars[B_Q_EMPTY + x]);
                     // the last stream that takes the tile gives it back
-                    if (x == 1 || j >= tiles[1]) tc_commit(&bars[B_K_EMPTY + ((tile + j) & 1)]);
+                    if (x == 1 || j >= tiles[1]) {
+#pragma unroll
+                        for (int c = 0; c < S::kKBoxes; ++c) tc_commit(&bars[B_EMPTY + wrap(at + c)]);
+                    }
                 };
                 if (most > 0) {
                     ok = mbar_wait(&bars[B_K_FULL + (tile & 1)], (tile >> 1) & 1, err);
@@ -363,6 +369,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         mma_ts4(tmem + kOCol + x * kT, tmem + x * kT, vd + uint64_t(v_at * (kBox >> 4)), idesc_o,
                                 j != 0);
+                        const bool last = x == 1 || j >= tiles[1];
+                        if (last && D == 128) tc_commit(&bars[B_EMPTY + v_at]);
                         ok = mbar_wait(&bars[B_P_FULL + 2 * x + 1], steps[x] & 1, err);
                         if (!ok) break;
                         tc_fence_after();
@@ -372,7 +380,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                                 idesc_o, 1);
                         ++steps[x];
                         if (j == tiles[x] - 1) tc_commit(&bars[B_O_FULL + x]);
-                        if (x == 1 || j >= tiles[1]) tc_commit(&bars[B_V_EMPTY + (t & 1)]);
+                        if (last) tc_commit(&bars[B_EMPTY + (D == 128 ? wrap(v_at + 1) : v_at)]);
                         if (j + 1 < tiles[x]) {
                             ok = mbar_wait(&bars[B_K_FULL + ((t + 1) & 1)], ((t + 1) >> 1) & 1, err);
                             if (ok) issue_s(x, j + 1, k_next);
