@@ -731,7 +731,8 @@ PKV_API size_t pkv_latent_workspace_bytes(const pkv_latent_desc* desc, int32_t n
 
 /* Attention over the cached rows (absorbed form): for query token t and head h
  *   out[t][h] = sum_j p_j c_j,  p = softmax_j(scale * (a . c_j + b . k_j)),  q[t][h] = (a, b)
- * over the keys that the row sees.  Rows: query_start_loc NULL is one query token per
+ * over the keys that the row sees (NaN where its scores are all -inf).  Rows:
+ * query_start_loc NULL is one query token per
  * sequence, its last; otherwise the layout of paged_attention_varlen, and row i of a
  * sequence sees keys 0 .. context_lens - qlen + i.  Rows behind the last sequence are
  * left as they are.
@@ -771,7 +772,8 @@ PKV_API size_t pkv_expanded_workspace_bytes(const pkv_expanded_desc* desc, int32
 
 /* Ragged causal attention over expanded keys: sequence s owns query rows
  * query_start_loc[s] .. and key rows key_start_loc[s] .. ; with n keys and m queries,
- * query i sees keys 0 .. n - m + i (a query that sees none, m > n, gives zeros):
+ * query i sees keys 0 .. n - m + i (a query that sees none, m > n, gives zeros; one whose
+ * scores are all -inf has no softmax either and gives NaN):
  *   out[t][h] = sum_j p_j v[j][h],
  *   p = softmax_j(scale * (q[t][h][0 .. D-1] . k[j][h] + q[t][h][D .. D+63] . k_rope[j]))
  *   out: device [num_query_tokens][num_heads][D]

@@ -584,6 +584,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
             cluster_sync();
             // a warp a row, every CTAS-th row each
             const int rank = blockIdx.x % CTAS;
+            const int keys = whole.keys + rank * whole.most * kT;   // of the unit, not of this CTA's part
             for (int y = rank + CTAS * warp; y < whole.rows && ok; y += CTAS * 8) {
                 float pm[CTAS], pl[CTAS], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -605,7 +606,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                     acc.z += w * v.z;
                     acc.w += w * v.w;
                 }
-                const float inv = sum != 0.f ? 1.f / sum : 0.f;    // a query without keys: zeros
+                // a query without keys: zeros (one whose scores are all -inf: 0 / 0, as in a CTA alone)
+                const float inv = y + keys >= whole.rows ? 1.f / sum : 0.f;
                 if (lane < D / 4)
                     *reinterpret_cast<uint2*>(p.out + ((int64_t(whole.q0) + y) * p.heads + whole.head) * D + lane * 4) =
                         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
