@@ -740,7 +740,8 @@ PKV_API size_t pkv_latent_workspace_bytes(const pkv_latent_desc* desc, int32_t n
  *   q:    device [num_query_tokens][num_q_heads][latent_dim + 64]
  *   scale: above 0; 1 / sqrt(the expanded key's size), which the cache does not tell
  *   workspace: 256-byte aligned, not shared by concurrent calls
- * Sums and softmax in fp32; for PKV_BF16 the weights enter the second product in bf16.
+ * Sums and softmax in fp32; for PKV_BF16 the weights enter the second product in bf16, and
+ * are summed as they enter it.
  * The work is cut where the batch's keys divide evenly over the SMs, so a sequence's
  * result depends on the batch by roundings.  A context outside [qlen, max_context_len]
  * (PKV_DEV_BAD_CONTEXT_LEN) or of more blocks than max_blocks_per_seq
@@ -787,8 +788,9 @@ PKV_API size_t pkv_expanded_workspace_bytes(const pkv_expanded_desc* desc, int32
  * pass num_query_tokens or num_keys is not computed (PKV_DEV_BAD_QUERY_LAYOUT).  Keys and
  * values that no query of the call sees may hold anything; a value that is not finite may
  * make NaN of all outputs of its sequence and head, also of queries in front of it, whose
- * weight for it is 0.  Sums and softmax in fp32; for PKV_BF16 the weights enter the second product in bf16.  workspace: 256-byte
- * aligned, not shared by concurrent calls. */
+ * weight for it is 0.  Sums and softmax in fp32; for PKV_BF16 the weights enter the second
+ * product in bf16, and are summed as they enter it.  workspace: 256-byte aligned, not shared
+ * by concurrent calls. */
 PKV_API int pkv_attention_expanded(void* out, const void* q, const void* k, const void* v,
                                    const void* k_rope, const pkv_expanded_desc* desc,
                                    const int32_t* query_start_loc, const int32_t* key_start_loc,

@@ -490,9 +490,10 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                     fence_proxy_async_shared();
                     __syncwarp();                          // the TMEM stores want all lanes at once
                 }
-                // P = 2^(s scale - m) in bf16 (2^-8 of a weight at most), over S's own columns;
-                // the sum is of the weights before that rounding
-                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2); 
+                // P = 2^(s scale - m) in bf16 (2^-8 of a weight at most), over S's own columns; the
+                // sum is taken of the same rounded weights, so that what is lost does not shift the
+                // weighted mean (of equal values too)
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
                 // (keeps the arithmetic of the second half behind the store of the first)
                 float refc = ref;
                 float2 sum[4] = {};
@@ -505,9 +506,9 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) {
                         const int at = 64 * c + 2 * i;
                         const float2 e = __ffma2_rn(make_float2(s[at], s[at + 1]), sc2, ref2);
-                        const float p0 = exp2_fast(e.x), p1 = exp2_fast(e.y);
-                        sum[i & 3] = __fadd2_rn(sum[i & 3], make_float2(p0, p1));
-                        w[i] = pack_bf16x2(p0, p1);
+                        w[i] = pack_bf16x2(exp2_fast(e.x), exp2_fast(e.y));
+                        sum[i & 3] = __fadd2_rn(sum[i & 3], make_float2(__uint_as_float(w[i] << 16),
+                                                                        __uint_as_float(w[i] & 0xffff0000u)));
                     }
                     tc_st32(s_at + 32 * c, w);
                     tc_wait_st();
