@@ -411,7 +411,7 @@ extern "C" int pkv_attention_expanded(void* out, const void* q, const void* k, c
     if (num_seqs < 0 || num_query_tokens < 0 || num_keys < 0 || max_query_len < 0 ||
         !(scale > 0.f && std::isfinite(scale)))
         return PKV_ERR_INVALID;
-    if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PKV_OK;
+    if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     const int64_t per = desc->dtype == PKV_BF16 ? 8 : 4;
     if (!out || !q || !query_start_loc || !key_start_loc || (num_keys > 0 && (!k || !v || !k_rope)) ||
         !aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) ||
