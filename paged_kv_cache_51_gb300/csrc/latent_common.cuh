@@ -27,6 +27,7 @@
 
 #include <algorithm>
 
+#include "latent_split.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -114,12 +115,6 @@ struct LatentFrag {
     int last_cta;                          // the CTA of the rows' last key (starts)
 };
 
-// a * b / c for values whose product stays below 2^63
-__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
-    const uint64_t x = uint64_t(a) * uint64_t(b);
-    return (x >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(c)) : int64_t(x / uint64_t(c));
-}
-
 template <int ROWS, int KEYS, int START>
 struct LatentWalk {
     int s;
@@ -137,14 +132,6 @@ struct LatentWalk {
         if (x.qlen == 0 || x.zero) return 0;
         return int64_t(groups(b, x.qlen * b.heads)) * ((x.ctx + KEYS - 1) / KEYS + START);
     }
-    // the stretch of team t begins at step t * total / teams; the team of a step
-    __device__ static int64_t start_of(int64_t t, int64_t total, int teams) { return mul_div(t, total, teams); }
-    __device__ static int owner(int64_t step, int64_t total, int teams) {
-        // the last t with t * total / teams <= step
-        int t = int(mul_div(step + 1, teams, total));
-        return mul_div(t, total, teams) <= step && t < teams ? t : t - 1;
-    }
-
     __device__ bool next(const LatentBatch& b, LatentFrag& f) {
         for (;;) {
             if (left <= 0) return false;
@@ -194,7 +181,7 @@ struct LatentWalk {
             const int want = (f.first_pos + last_tok) / KEYS + 1;   // tiles that any row sees
             f.n = max(0, min(end, want) - f.kt0);
             if (f.starts)
-                f.last_cta = owner(last, total, teams) * b.team + cta % b.team;
+                f.last_cta = stretch_of(last, total, teams) * b.team + cta % b.team;
         }
         begun = true;
         return true;
@@ -236,8 +223,8 @@ __device__ __forceinline__ LatentWalk<ROWS, KEYS, START> latent_plan(const Laten
     const int team = cta / b.team;
     x.teams = int(max(int64_t(1), min(int64_t(ctas) / b.team, total / least)));
     x.begun = false;
-    const int64_t from = Walk::start_of(team, total, x.teams);
-    x.left = team < x.teams ? Walk::start_of(team + 1, total, x.teams) - from : 0;
+    const int64_t from = stretch_begin(team, total, x.teams);
+    x.left = team < x.teams ? stretch_begin(team + 1, total, x.teams) - from : 0;
     x.pos = from;
     if (x.left > 0 && from < upto && from >= upto - mine) {
         int64_t at = upto - mine;
