@@ -176,6 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.abort = 0;
         fence_mbar_init();
     }
+    // Tensor memory is taken behind the wait, and the next kernel let in behind the plan's
+    // barriers: a kernel that held it while it waited for one that has yet to take its own
+    // would wait for ever where their CTAs share an SM.
+    pdl_wait_prerequisites();
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sh.tmem)),
@@ -183,10 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait_prerequisites();
-    pdl_launch_dependents();
     tc_fence_before();
     const Walk plan = latent_plan<kRows, kKeys, kStart, kThreads>(p.b, sh.sums, kLeastSteps, blockIdx.x, gridDim.x);
+    pdl_launch_dependents();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 

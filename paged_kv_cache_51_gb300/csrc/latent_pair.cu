@@ -198,6 +198,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sh.abort = 0;
         fence_mbar_init();
     }
+    // (as in latent_attn.cu, tensor memory is taken behind the wait)
+    pdl_wait_prerequisites();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sh.tmem)),
@@ -205,10 +207,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    pdl_wait_prerequisites();
-    pdl_launch_dependents();
     tc_fence_before();
     const Walk plan = latent_plan<kRows, kKeys, kStart, kThreads>(p.b, sh.sums, kLeastSteps, pair, int(gridDim.x) / 2);
+    pdl_launch_dependents();
     pair_sync();                                          // the other CTA's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
