@@ -549,7 +549,7 @@ int launch_latent_bf16(const LatentArgs& a) {
     p.b = a.batch;
     p.ws = a.ws;
     p.out = static_cast<__nv_bfloat16*>(a.out);
-    p.b.team = latent_team(p.b, kRows);
+    p.b.team = 1;                          // (a sequence has one tile of rows on average, or less)
     p.whole_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     // query rows of a unit: all 64, or those of the longest sequence if it has fewer (a
     // call of one token a sequence; with offsets the rows of a sequence are not known here)

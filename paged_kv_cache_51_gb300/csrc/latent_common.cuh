@@ -245,7 +245,11 @@ __device__ __forceinline__ LatentWalk<ROWS, KEYS, START> latent_plan(const Laten
     return x;
 }
 
-// rows of a sequence, on average
+// Rows of a sequence, on average: what the host knows of a batch whose offsets lie on the device.
+// It chooses the kernel and the size of its units, and neither changes what is computed: a
+// sequence of more rows than a unit's is several units.  Rows behind the last sequence (a
+// captured call's padding) count, so a call padded far beyond its tokens takes larger units
+// than its sequences fill.
 inline int64_t latent_rows(const LatentBatch& b) {
     return int64_t(ceil_div(b.num_query_tokens, b.num_seqs)) * b.heads;
 }
