@@ -48,6 +48,7 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 64;
+static_assert(kRows == kLatentRowTile, "states");
 constexpr int kKeys = 32;
 constexpr int kThreads = 256;
 constexpr int kSoftWarp0 = 4;

@@ -34,7 +34,7 @@
 namespace pkv {
 
 constexpr int kLatentRope = 64;            // rotated key values of a token
-constexpr int kLatentRowTile = 64;         // most rows of a unit (sizes the workspace)
+constexpr int kLatentRowTile = 64;         // most rows whose state one CTA writes (sizes the workspace)
 
 struct LatentBatch {
     const int32_t* block_tables;

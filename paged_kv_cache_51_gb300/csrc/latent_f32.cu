@@ -60,6 +60,7 @@ constexpr int smem_floats(int latent) {
 // RG: shares of the rows in the second product.
 template <int ROWS, int KEYS, int RG>
 __global__ void __launch_bounds__(kThreads) latent_f32_kernel(Params p) {
+    static_assert(ROWS <= kLatentRowTile, "states");
     constexpr int RPT = ROWS / RG, kPtPitch = ROWS + 4, kPitch = kPartPitch<KEYS>;
     extern __shared__ float4 smem4[];
     float* smem = reinterpret_cast<float*>(smem4);

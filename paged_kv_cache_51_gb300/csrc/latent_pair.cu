@@ -83,6 +83,28 @@ struct Smem {                              // behind the operands
     int abort;
 };
 static_assert(sizeof(Smem) <= 2048, "shared memory");
+static_assert(kMine == kLatentRowTile, "a CTA of a pair writes the states of its own rows");
+
+// Chunks and shared memory for a latent_dim: two tiles of keys where they fit, at the longest
+// latent vectors one; then as many chunks of values as fit.
+struct Slots {
+    int k, v, smem;
+};
+constexpr Slots slots_of(int latent) {
+    const int cols = latent / 64 + 1, vcols = latent / 128, chunks = (cols + kKCols - 1) / kKCols;
+    const int kchunk = kKCols * 1024 * (kMine / 8), vchunk = vcols * 1024 * (kVKeys / 8);
+    const int fixed = 1024 + int(sizeof(Smem)) + kPBytes + cols * 1024 * (kMine / 8);
+    const int k = fixed + 2 * chunks * kchunk + 4 * vchunk <= kSmemMost ? 2 * chunks : chunks;
+    const int room = (kSmemMost - fixed - k * kchunk) / vchunk, v = room < kMostV ? room : kMostV;
+    return {k, v, fixed + k * kchunk + v * vchunk};
+}
+// The value ring holds a tile at least: the softmax waits for the chunk that the context ends
+// in before its P lets the chunks in front of it go, and finds a chunk's slot by one subtraction.
+constexpr bool slots_fit(int latent) {
+    const Slots s = slots_of(latent);
+    return s.k >= 1 && s.k <= kMostK && s.v >= kKeys / kVKeys && s.v <= kMostV && s.smem <= kSmemMost;
+}
+static_assert(slots_fit(128) && slots_fit(256) && slots_fit(384) && slots_fit(512), "shared memory");
 
 struct Params {
     LatentBatch b;
@@ -621,18 +643,12 @@ int launch_latent_pair(const LatentArgs& a) {
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.b.team = latent_team(p.b, kRows);
     p.whole_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-    constexpr int kchunk = kKCols * 1024 * (kMine / 8);
-    const int qbytes = cols * 1024 * (kMine / 8), vchunk = vcols * 1024 * (kVKeys / 8);
-    const int fixed = 1024 + int(sizeof(Smem)) + kPBytes + qbytes;
-    static_assert(1024 + sizeof(Smem) + kPBytes + 9 * 8192 + 3 * kchunk + 4 * 16384 <= kSmemMost, "shared memory");
-    // two tiles where they fit; at the longest latent vectors one
-    const int chunks = (cols + kKCols - 1) / kKCols;
-    p.k_slots = fixed + 2 * chunks * kchunk + 4 * vchunk <= kSmemMost ? 2 * chunks : chunks;
-    p.v_slots = std::min(kMostV, (kSmemMost - fixed - p.k_slots * kchunk) / vchunk);
-    const int smem = fixed + p.k_slots * kchunk + p.v_slots * vchunk;
+    const Slots slots = slots_of(d->latent_dim);
+    p.k_slots = slots.k;
+    p.v_slots = slots.v;
     if (kernel_occupancy<latent_pair_kernel>(kThreads, kSmemMost) < 1) return PKV_ERR_CUDA;
     const int ctas = num_sms() & ~1;                      // whole pairs
-    cudaError_t e = launch_pdl(latent_pair_kernel, dim3(unsigned(ctas)), dim3(kThreads), size_t(smem), a.stream, k,
+    cudaError_t e = launch_pdl(latent_pair_kernel, dim3(unsigned(ctas)), dim3(kThreads), size_t(slots.smem), a.stream, k,
                                v, q, p);
     if (e != cudaSuccess) return cuda_status(e);
     LatentBatch b = p.b;
