@@ -284,8 +284,15 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < most && ok; ++j, ++tile) {
                     const int row = u.k0 + j * kT;
                     uint32_t dst;
+#ifdef PKV_TEST_SKIP_TILE
+                    // wait-timeout test build only, as in latent_attn.cu
+                    const bool skip = tile == uint32_t(PKV_TEST_SKIP_TILE);
+#else
+                    constexpr bool skip = false;
+#endif
                     for (int c = 0; c < S::kKBoxes; ++c) {
                         if (!slot(dst)) break;
+                        if (skip) continue;
                         if (c == 0) mbar_arrive_expect_tx(&bars[B_K_FULL + (tile & 1)], S::kKBoxes * kBox);
                         if (c < D / 64) tc_load_3d(dst, &map_k, c * 64, u.head, row, &bars[B_K_FULL + (tile & 1)]);
                         else tc_load_3d(dst, &map_r, 0, 0, row, &bars[B_K_FULL + (tile & 1)]);
@@ -293,6 +300,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
                     if (j == 0) load_q(1);
                     for (int c = 0; c < S::kVBoxes && ok; ++c) {
                         if (!slot(dst)) break;
+                        if (skip) continue;
                         if (c == 0) mbar_arrive_expect_tx(&bars[B_V_FULL + (tile & 1)], S::kVBoxes * kBox);
                         // D = 128: 64 keys of both halves of the values; D = 64: 128 keys
                         for (int e = 0; e < 2; ++e)

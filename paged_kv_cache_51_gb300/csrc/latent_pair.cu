@@ -274,6 +274,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < chunks; ++c, ++n) {
                     ok = !*abort_flag && (n < k_slots || mbar_wait_asleep(&bars[B_K_EMPTY + at.slot], at.phase ^ 1, err));
                     if (!ok) break;
+#ifdef PKV_TEST_SKIP_TILE
+                    // wait-timeout test build only, as in latent_attn.cu
+                    if (t.g == uint32_t(PKV_TEST_SKIP_TILE)) {
+                        at.next(k_slots);
+                        continue;
+                    }
+#endif
                     if (rank == 0) mbar_arrive_expect_tx(&bars[B_K_FULL + at.slot], 2 * kchunk);
                     const uint32_t dst = base + k_off + at.slot * kchunk, full = full0 + at.slot * 8;
 #pragma unroll
