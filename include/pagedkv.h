@@ -748,7 +748,8 @@ PKV_API size_t pkv_latent_workspace_bytes(const pkv_latent_desc* desc, int32_t n
  * (PKV_DEV_TABLE_TOO_NARROW) gives zeros; a block id out of range sets
  * PKV_DEV_BAD_BLOCK_ID and leaves the sequence's outputs undefined; a sequence whose
  * offsets fall or pass num_query_tokens, and the first where they do not begin with 0,
- * is not computed (PKV_DEV_BAD_QUERY_LAYOUT).  Rows of the cache behind a sequence's
+ * is not computed (PKV_DEV_BAD_QUERY_LAYOUT), and rows that offsets out of order give to
+ * two sequences are undefined.  Rows of the cache behind a sequence's
  * context may hold anything.  A row of its own that is not finite may make NaN of all of
  * the sequence's outputs, also of tokens in front of it: their weight for it is 0. */
 PKV_API int paged_attention_latent(void* out, const void* q, const void* latent_cache,
@@ -785,7 +786,9 @@ PKV_API size_t pkv_expanded_workspace_bytes(const pkv_expanded_desc* desc, int32
  *         PKV_DEV_BAD_QUERY_LAYOUT
  *   scale: above 0; usually 1 / sqrt(head_dim + 64)
  * Rows behind the last sequence are left as they are; a sequence whose offsets fall or
- * pass num_query_tokens or num_keys is not computed (PKV_DEV_BAD_QUERY_LAYOUT).  Keys and
+ * pass num_query_tokens or num_keys, and the first where they do not begin with 0, is not
+ * computed (PKV_DEV_BAD_QUERY_LAYOUT); rows that offsets out of order give to two sequences
+ * are undefined.  Keys and
  * values that no query of the call sees may hold anything; a value that is not finite may
  * make NaN of all outputs of its sequence and head, also of queries in front of it, whose
  * weight for it is 0.  Sums and softmax in fp32; for PKV_BF16 the weights enter the second

@@ -9,8 +9,8 @@ namespace pkv {
 // neighbouring units of a sequence form a group, and the units of all heads of a group are
 // taken head by head: those that run at the same time then read the same keys.  (Unit by unit
 // over all heads, eight prompts of up to 4096 tokens with 32 heads read 2.6 GB from HBM, three
-// times their keys and values, and took 590 us instead of 546.)  With fewer than eight units
-// an SM they mostly run at the same time anyway, and groups of one end more evenly (4 prompts
+// times their keys and values, and took 590 us instead of 546; now they read 1.1 GB, 0.67 GB
+// being their keys, values and queries.)  With fewer than eight units an SM they mostly run at the same time anyway, and groups of one end more evenly (4 prompts
 // of 2048 tokens, 19 heads: 83 us against 91).
 struct ExpandedItem {
     int32_t q0, rows;        // first query row of the call, rows of the unit

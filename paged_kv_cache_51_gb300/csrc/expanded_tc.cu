@@ -29,8 +29,9 @@
 // took 180 us with one CTA and takes 52 with four, 8 heads over 4k 51 and 19; two sequences
 // of 256 queries over 3256 keys, 16 heads, 55 and 37 with two).
 //
-// Measured, D = 128, 32 heads: 8 prompts of 1700 to 4096 tokens 540 us (1350 TFLOP/s, at the
-// power limit), 4 chunks of about 450 over 512 to 3584 cached 83 to 88 us.  A tile of both
+// Measured, D = 128, 32 heads: 8 prompts of 1700 to 4096 tokens 561 to 569 us (1290 TFLOP/s, at
+// the power limit), 4 chunks of about 450 over 512 to 3584 cached 90 us; D = 64: 406 us (1080
+// TFLOP/s) and 73.  A tile of both
 // streams takes 3350 to 3600 cycles, of which products 2560: a stream's softmax (1500 to 1600)
 // and its products (1280) cannot overlap, since S and P share their columns.
 #include <cuda.h>

@@ -8,7 +8,8 @@
 // and, through another descriptor over the same bytes, MN-major for the second.
 //
 // Shapes.  A CTA takes 64 (token, head) rows of one sequence and tiles of 32 keys (batches of
-// more rows a sequence go to pairs of CTAs, latent_pair.cu).
+// more rows a sequence on average go to pairs of CTAs, latent_pair.cu; a sequence of more rows
+// in a batch of few is several units here).
 // Products of this size are bound by the shared memory they read (128 bytes a cycle;
 // measured, in cycles: 64 x 32 x 16 takes 24, 64 x 64 x 16 32, 64 x 256 x 16 80 in the .ws
 // form, which spreads the halves of the columns over all 128 TMEM lanes, and 128 in the
@@ -32,7 +33,7 @@
 // cycles a tile, 450 of them its own waits and bookkeeping between the two.)
 //
 // Measured, with the merge: 4 requests of 32k tokens, 64 heads, 42 us; 64 of 512 to 4096, 32
-// heads, 44 us.  The tiles run at HBM's rate, 1650 cycles each; a start of 5 us, outputs of
+// heads, 45 us.  The tiles run at HBM's rate, 1650 cycles each; a start of 5 us, outputs of
 // 2.5 and the merge of 6 are the rest.
 #include <cuda.h>
 #include <cuda_runtime.h>

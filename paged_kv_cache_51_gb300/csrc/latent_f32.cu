@@ -1,9 +1,10 @@
 // Attention over a paged latent cache in single precision, on the CUDA cores.
 //
 // A CTA of eight warps takes ROWS (token, head) rows of one sequence and tiles of KEYS keys,
-// two of them in flight (cp.async).  Products in fp32 have no tensor-core form that keeps
-// their bits, so what bounds it beyond a few heads is the FMA rate, and in front of it what
-// shared memory returns: 128 bytes a cycle, so that a read of 16 bytes a lane costs a warp
+// two of them in flight (cp.async).  Tensor cores take no fp32 operands; an fp32 value is the
+// sum of three bf16 values, and six to nine such products in place of one would keep its bits,
+// which is not built.  So what bounds it beyond a few heads is the FMA rate, and in front of
+// it what shared memory returns: 128 bytes a cycle, so that a read of 16 bytes a lane costs a warp
 // four cycles even where all lanes read the same, the time of 16 FMAs of a warp.
 //   S: warp w holds an eighth of the dimensions of all ROWS x KEYS scores, a lane a part of
 //      RT x KT: RT + KT reads for 4 RT KT FMAs (rows against one key of a lane, 17 reads for

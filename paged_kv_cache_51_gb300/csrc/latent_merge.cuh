@@ -1,8 +1,10 @@
 // States of the cut units of a latent attention, joined in the order of their keys:
 //   M = max m_i,  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 //
-// One wave of CTAs, resident before the attention ends.  Every CTA lists the cut units for
-// itself; a warp takes 256 values of a unit at a time and asks for the states of several
+// One wave of CTAs, launched while the attention still runs.  (Its CTAs want 15 KB each: next to
+// an attention CTA there is room for none of them at latent 512 and for one at 256, so that most
+// start as the attention's leave; what the early launch hides is the launch.)
+// Every CTA lists the cut units for itself; a warp takes 256 values of a unit at a time and asks for the states of several
 // CTAs at once, so that what it waits for is one trip to L2 (reading state by state took
 // 13 us for 64 requests of 512 to 4096 tokens).  Where there are fewer such items than
 // warps, 2, 4 or 8 warps of a CTA share one, each with a share of the states, and meet in
