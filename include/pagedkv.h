@@ -788,7 +788,7 @@ PKV_API size_t pkv_expanded_workspace_bytes(const pkv_expanded_desc* desc, int32
  * Rows behind the last sequence are left as they are; a sequence whose offsets fall or
  * pass num_query_tokens or num_keys, and the first where they do not begin with 0, is not
  * computed (PKV_DEV_BAD_QUERY_LAYOUT); rows that offsets out of order give to two sequences
- * are undefined.  Keys and
+ * are undefined, and other rows may then be left as they are.  Keys and
  * values that no query of the call sees may hold anything; a value that is not finite may
  * make NaN of all outputs of its sequence and head, also of queries in front of it, whose
  * weight for it is 0.  Sums and softmax in fp32; for PKV_BF16 the weights enter the second
